@@ -405,6 +405,141 @@ recis_status recis_reduce_grad(recis_batch_t b, const int64_t* bag_offsets, int3
                                const float* grad_unpooled, const int32_t* out_index,
                                float* grad_out, recis_stream_t stream);
 
+/* ------------------------------------------------------------------ sequence operators */
+/* What turns the unpooled rows of a ragged sequence into an answer, and the
+ * answer's gradient back into rows: dense embedding tables for small
+ * vocabularies, layer norm, and attention over the keys of each bag (beside
+ * the SUM and MEAN pooling of recis_lookup_pooled).  The pages name sequence
+ * features only; the formulas are the usual ones and stand at each call.
+ *
+ * Conventions of this section:
+ *   - Floating arrays are fp32, bf16 or fp16 (RECIS_F32, RECIS_BF16,
+ *     RECIS_F16).  All arithmetic is in fp32 or fp64 and rounded once to the
+ *     output's type, except where a comment says otherwise.
+ *   - A `..._stride` counts elements from one row to the next (>= the row's
+ *     length); the elements of a row are contiguous.  Arrays are aligned to
+ *     their element type unless a call asks for more.  Outputs overlap
+ *     neither inputs nor one another.
+ *   - Scratch is the caller's: `..._workspace` (host only, no GPU) gives its
+ *     bytes, 256-byte aligned device memory that is the call's alone until
+ *     its work has finished.  The calls allocate nothing, keep nothing from
+ *     one call to the next and may be captured into graphs.
+ *   - Device-detected errors (a token out of range, malformed offsets) are
+ *     reported by recis_sequence_status_sync. */
+#define RECIS_F32 0
+#define RECIS_BF16 1
+#define RECIS_F16 2
+
+/* Synchronous: waits for `stream`, returns and clears the device-detected
+ * status of earlier calls of this section on the current device.  The first
+ * call of the section on a device looks up the status word's address; make it
+ * before any stream capture. */
+recis_status recis_sequence_status_sync(recis_stream_t stream);
+
+/* Dense embedding lookup: out[i][:] = scale * weight[tokens[i]][:].  A token
+ * equal to `padding` reads as zeros (whether or not it is a row of weight);
+ * any other token outside [0, V) reads as zeros and is a device-detected
+ * error (RECIS_ERR_INVALID_ARG).  weight: [V][D], contiguous; tokens: device
+ * int64[N]; out: [N][D].  0 <= N < 2^31, 1 <= V < 2^31, 1 <= D <= 65536. */
+recis_status recis_embed_lookup(const void* weight, int32_t weight_type, int64_t V, int32_t D,
+                                const int64_t* tokens, int64_t N, double scale, int64_t padding,
+                                void* out, int32_t out_type, int64_t out_stride,
+                                recis_stream_t stream);
+
+/* Gradient of recis_embed_lookup: grad_weight[v][:] = scale * the sum of
+ * grad_out[i][:] over the i with tokens[i] = v (accumulate 0: rows no token
+ * names become 0; accumulate 1: the sum is added to grad_weight and other rows
+ * are left alone).  Padding tokens have no gradient; a token out of range is
+ * skipped and reported as above.  The tokens are sorted and each row's terms
+ * added in occurrence order: fp32 within spans of the sorted positions, fp64
+ * across spans, so results do not depend on scheduling.  grad_weight: [V][D],
+ * contiguous.  0 <= N < 2^30, otherwise as above. */
+recis_status recis_embed_grad_workspace(int64_t N, int64_t V, int32_t D, int64_t* bytes_out);
+recis_status recis_embed_grad(const int64_t* tokens, int64_t N, const void* grad_out,
+                              int32_t grad_type, int64_t grad_stride, int64_t V, int32_t D,
+                              double scale, int64_t padding, int32_t accumulate, void* grad_weight,
+                              int32_t weight_type, void* workspace, int64_t workspace_bytes,
+                              recis_stream_t stream);
+
+/* Layer norm of M rows of D: mean[i] = sum_j x[i][j] / D, rstd[i] = 1 /
+ * sqrt(sum_j (x[i][j] - mean[i])^2 / D + eps), xh = (x - mean) * rstd,
+ * y = xh * weight + bias (weight NULL: ones; bias NULL: zeros; both of
+ * w_type).  mean and rstd: device fp32[M], kept for the backward (NULL: not
+ * wanted).  0 <= M < 2^31, 1 <= D <= 65536. */
+recis_status recis_layer_norm(const void* x, int32_t x_type, int64_t x_stride, int64_t M, int32_t D,
+                              const void* weight, const void* bias, int32_t w_type, double eps,
+                              void* y, int32_t y_type, int64_t y_stride, float* mean, float* rstd,
+                              recis_stream_t stream);
+
+/* Backward of recis_layer_norm, from its x, weight, mean and rstd and y's
+ * gradient (of y_type).  With g = grad_y * weight:
+ *   grad_x = rstd * (g - mean_j(g) - xh * mean_j(g * xh))   [M][D] of x_type,
+ *   grad_weight[j] = sum_i grad_y[i][j] * xh[i][j]           [D] of w_type,
+ *   grad_bias[j]   = sum_i grad_y[i][j]                      [D] of w_type;
+ * each may be NULL (not wanted).  The sums over rows are fp32 within a
+ * block's rows and fp64 across blocks, in a fixed order. */
+recis_status recis_layer_norm_backward_workspace(int64_t M, int32_t D, int64_t* bytes_out);
+recis_status recis_layer_norm_backward(const void* grad_y, int32_t y_type, int64_t grad_y_stride,
+                                       const void* x, int32_t x_type, int64_t x_stride, int64_t M,
+                                       int32_t D, const void* weight, int32_t w_type,
+                                       const float* mean, const float* rstd, void* grad_x,
+                                       int64_t grad_x_stride, void* grad_weight, void* grad_bias,
+                                       void* workspace, int64_t workspace_bytes,
+                                       recis_stream_t stream);
+
+/* Attention of the queries of each bag over the keys of the same bag.  Bag b's
+ * queries are rows q_offsets[b] .. q_offsets[b+1] of q, its keys rows
+ * k_offsets[b] .. k_offsets[b+1] of k and v (the two lengths are unrelated;
+ * there is no causal order).  Query head h reads key head h / (Hq / Hkv).
+ * With s = scale * q k^T over the bag's keys (key_mask: device uint8[Tk] or
+ * NULL; keys with 0 take no part, whatever their k and v hold):
+ *   out = softmax(s) v,   lse = log(sum(exp(s)));   no key: out 0, lse -inf.
+ * Rows of out and lse that belong to no bag are left as they were.
+ * Backward (recis_attend_backward), from out, lse and out's gradient:
+ *   p = exp(s - lse), dp = grad_out v^T, ds = p * (dp - sum(grad_out * out)),
+ *   grad_q = scale * ds k, grad_k = scale * ds^T q, grad_v = p^T grad_out,
+ * the last two summed over the query heads of the key head; masked keys get
+ * zeros; rows of no bag are left as they were.
+ *
+ * type: RECIS_BF16 or RECIS_F16, of every array but lse.  p and ds are rounded
+ * to it before their matrix products (tensor-core operands); all sums, the
+ * softmax statistics and the joining of partial results are fp32.
+ * Strides in elements, multiples of 8 (16 bytes), arrays 16-byte aligned:
+ * element (t, h, j) of q is q[t * q_stride + h * q_head_stride + j], grad_q
+ * and so on alike.  lse: fp32 [Tq][Hq], contiguous.  D: a multiple of 8, 8..128.
+ * Hq a multiple of Hkv, Hq / Hkv <= 128.  B, Tq, Tk, max_q * Hq and max_k * Hkv
+ * below 2^31 - 1.
+ * max_q and max_k (host) bound the bags' lengths.  Offsets that decrease,
+ * leave [0, Tq] or [0, Tk], or give a bag longer than its bound are a
+ * device-detected error (RECIS_ERR_INVALID_ARG); such a bag's rows are
+ * undefined, every access stays in bounds. */
+typedef struct {
+  int32_t type;
+  int32_t D, Hq, Hkv;
+  int64_t B, Tq, Tk;
+  int64_t max_q, max_k;
+  double scale;
+  const int64_t* q_offsets; /* device int64[B+1] */
+  const int64_t* k_offsets; /* device int64[B+1] */
+  const uint8_t* key_mask;  /* device uint8[Tk] or NULL */
+  const void *q, *k, *v;    /* [Tq][Hq][D], [Tk][Hkv][D], [Tk][Hkv][D] */
+  int64_t q_stride, q_head_stride, k_stride, k_head_stride, v_stride, v_head_stride;
+  void* out;                /* [Tq][Hq][D]: written by recis_attend, read by the backward */
+  int64_t out_stride, out_head_stride;
+  float* lse;               /* [Tq][Hq] */
+  /* backward only */
+  const void* grad_out;
+  int64_t grad_out_stride, grad_out_head_stride;
+  void *grad_q, *grad_k, *grad_v;
+  int64_t grad_q_stride, grad_q_head_stride, grad_k_stride, grad_k_head_stride, grad_v_stride,
+      grad_v_head_stride;
+} recis_attend_args;
+recis_status recis_attend_workspace(const recis_attend_args* a, int32_t backward, int64_t* bytes_out);
+recis_status recis_attend(const recis_attend_args* a, void* workspace, int64_t workspace_bytes,
+                          recis_stream_t stream);
+recis_status recis_attend_backward(const recis_attend_args* a, void* workspace,
+                                   int64_t workspace_bytes, recis_stream_t stream);
+
 /* ------------------------------------------------------------------ test hooks */
 /* Process-wide settings that let tests reach error paths without faulting the
  * GPU.  The pages have no counterpart (they describe no failure handling).

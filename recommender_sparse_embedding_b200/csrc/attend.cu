@@ -1,0 +1,585 @@
+// attend.cu -- attention of each bag's queries over the bag's keys: argument
+// checks, the plan of a call, and the forward pass for few queries.
+//
+//   s = scale q k^T over the bag's unmasked keys, out = softmax(s) v,
+//   lse = log sum exp s;  a bag without keys: out 0, lse -inf.
+//
+// The query heads that share a key head are rows of one matrix: row r of key
+// head h is query r / G, head h G + r % G, so K and V are read once for all of
+// them.
+#include <algorithm>
+
+#include "attend.cuh"
+
+namespace recis {
+
+namespace {
+
+__host__ __device__ constexpr int64_t align256(int64_t b) { return (b + 255) & ~(int64_t)255; }
+
+template <typename T>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
+template <>
+__device__ __forceinline__ void mma16816<__nv_bfloat16>(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <>
+__device__ __forceinline__ void mma16816<__half>(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+constexpr int kRowTile = 16;   // rows (query, head of the group) a block of few_kernel takes
+constexpr int kFewWarps = 4;
+
+// One block: 16 rows of one key head against one part of the bag's keys; warp w
+// takes every fourth block of 16 keys with a softmax of its own, and the warps'
+// results are joined in shared memory.
+//
+// K and V go from global memory to the matrix instruction's registers without
+// shared memory: 16 bytes a thread.  The order of the contracted index of
+// q k^T is free as long as both operands agree, so a thread's 16 bytes of a key
+// row (8 consecutive d) serve as the k pairs of two m16n8k16 steps; for p v the
+// thread reads the key rows whose pairs it needs and interleaves two rows by
+// byte permutes, which makes output column n of tile j stand for d = 8 n + j.
+template <typename T, int DP>  // DP: D rounded up to 32, 64 or 128
+__global__ void __launch_bounds__(kFewWarps * 32) few_kernel(const __grid_constant__ AttendParams p) {
+  constexpr int KG = DP / 32, VE = (DP + 63) / 64;
+  __shared__ float s_o[kFewWarps][kRowTile][DP + 4];
+  __shared__ float s_m[kFewWarps][kRowTile], s_l[kFewWarps][kRowTile];
+  const int rtiles = (p.max_q * p.G + kRowTile - 1) / kRowTile;
+  unsigned id = blockIdx.x;
+  const int rt = id % rtiles;
+  id /= rtiles;
+  const int h = id % p.Hkv;
+  id /= p.Hkv;
+  const int sp = id % p.splits, b = id / p.splits;
+  const Bag bag = load_bag(p, b);
+  const int rows = bag.nq * p.G, r0 = rt * kRowTile;
+  const int ks = sp * p.split_keys, ke = min(ks + p.split_keys, bag.nk);
+  if (r0 >= rows || (ks >= bag.nk && sp > 0)) return;
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, g = lane >> 2, c = lane & 3;
+  const T* kp = static_cast<const T*>(p.k) + bag.k0 * p.ks + h * p.kh;
+  const T* vp = static_cast<const T*>(p.v) + bag.k0 * p.vs + h * p.vh;
+  const uint8_t* mp = p.mask ? p.mask + bag.k0 : nullptr;
+
+  uint4 qa[KG], qb[KG];  // rows g and g + 8
+  {
+    const int ra = r0 + g, rb = ra + 8;
+#pragma unroll
+    for (int i = 0; i < KG; ++i) {
+      const int d = 32 * i + 8 * c;
+      qa[i] = qb[i] = make_uint4(0, 0, 0, 0);
+      if (d < p.D && ra < rows)
+        qa[i] = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + (bag.q0 + ra / p.G) * p.qs +
+                                                (h * p.G + ra % p.G) * p.qh + d);
+      if (d < p.D && rb < rows)
+        qb[i] = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + (bag.q0 + rb / p.G) * p.qs +
+                                                (h * p.G + rb % p.G) * p.qh + d);
+    }
+  }
+  float o[VE][8][4];
+#pragma unroll
+  for (int e = 0; e < VE; ++e)
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[e][j][i] = 0.f;
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+
+  uint4 kf[2][KG], vf[4][VE];
+  auto valid = [&](int key) { return key < ke && (!mp || mp[key]); };
+  auto load_k = [&](int kb) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int key = kb + t * 8 + g;
+      const bool ok = valid(key);
+#pragma unroll
+      for (int i = 0; i < KG; ++i) {
+        const int d = 32 * i + 8 * c;
+        kf[t][i] = make_uint4(0, 0, 0, 0);
+        if (ok && d < p.D) kf[t][i] = __ldg(reinterpret_cast<const uint4*>(kp + (int64_t)key * p.ks + d));
+      }
+    }
+  };
+  auto load_v = [&](int kb) {
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const int key = kb + 2 * c + (t & 1) + (t >> 1) * 8;
+      const bool ok = valid(key);
+#pragma unroll
+      for (int e = 0; e < VE; ++e) {
+        const int d = 64 * e + 8 * g;
+        vf[t][e] = make_uint4(0, 0, 0, 0);
+        if (ok && d < p.D) vf[t][e] = __ldg(reinterpret_cast<const uint4*>(vp + (int64_t)key * p.vs + d));
+      }
+    }
+  };
+  int kb = ks + w * 16;
+  if (kb < ke) load_k(kb);
+  for (; kb < ke; kb += kFewWarps * 16) {
+    load_v(kb);
+    float s[2][4];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[t][i] = 0.f;
+#pragma unroll
+      for (int i = 0; i < KG; ++i) {
+        const uint32_t a0[4] = {qa[i].x, qb[i].x, qa[i].y, qb[i].y}, a1[4] = {qa[i].z, qb[i].z, qa[i].w, qb[i].w};
+        mma16816<T>(s[t], a0, kf[t][i].x, kf[t][i].y);
+        mma16816<T>(s[t], a1, kf[t][i].z, kf[t][i].w);
+      }
+    }
+    bool ok[2][2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) ok[t][i] = valid(kb + t * 8 + 2 * c + i);
+    if (kb + kFewWarps * 16 < ke) load_k(kb + kFewWarps * 16);
+    float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        s[t][i] = ok[t][i & 1] ? s[t][i] * p.scale_log2 : -INFINITY;
+        mx[i >> 1] = fmaxf(mx[i >> 1], s[t][i]);
+      }
+    float corr[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
+      mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
+      const float mn = fmaxf(m[r], mx[r]);
+      const float base = mn == -INFINITY ? 0.f : mn;
+      corr[r] = exp2f(m[r] - base);
+      m[r] = mn;
+      mx[r] = base;
+      l[r] *= corr[r];
+    }
+    uint32_t pa[4];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        s[t][i] = exp2f(s[t][i] - mx[i >> 1]);
+        l[i >> 1] += s[t][i];
+      }
+      pa[t * 2] = pack2<T>(s[t][0], s[t][1]);
+      pa[t * 2 + 1] = pack2<T>(s[t][2], s[t][3]);
+    }
+#pragma unroll
+    for (int e = 0; e < VE; ++e) {
+      const uint32_t* v0 = reinterpret_cast<const uint32_t*>(&vf[0][e]);
+      const uint32_t* v1 = reinterpret_cast<const uint32_t*>(&vf[1][e]);
+      const uint32_t* v2 = reinterpret_cast<const uint32_t*>(&vf[2][e]);
+      const uint32_t* v3 = reinterpret_cast<const uint32_t*>(&vf[3][e]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const unsigned sel = (j & 1) ? 0x7632 : 0x5410;
+        o[e][j][0] *= corr[0];
+        o[e][j][1] *= corr[0];
+        o[e][j][2] *= corr[1];
+        o[e][j][3] *= corr[1];
+        mma16816<T>(o[e][j], pa, __byte_perm(v0[j >> 1], v1[j >> 1], sel), __byte_perm(v2[j >> 1], v3[j >> 1], sel));
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+    if (c == 0) {
+      s_m[w][g + 8 * r] = m[r];
+      s_l[w][g + 8 * r] = l[r];
+    }
+#pragma unroll
+    for (int e = 0; e < VE; ++e)
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int d = 64 * e + 16 * c + 8 * i + j;
+          if (d < DP) s_o[w][g + 8 * r][d] = o[e][j][2 * r + i];
+        }
+  }
+  __syncthreads();
+  // join the warps: 8 threads a row, each every eighth group of 8 columns
+  const int row = tid >> 3, r = r0 + row;
+  if (r >= rows) return;
+  float mm = s_m[0][row];
+#pragma unroll
+  for (int q = 1; q < kFewWarps; ++q) mm = fmaxf(mm, s_m[q][row]);
+  const float base = mm == -INFINITY ? 0.f : mm;
+  float f[kFewWarps], ll = 0.f;
+#pragma unroll
+  for (int q = 0; q < kFewWarps; ++q) {
+    f[q] = exp2f(s_m[q][row] - base);
+    ll = fmaf(s_l[q][row], f[q], ll);
+  }
+  const float inv = ll > 0.f ? 1.0f / ll : (ll == 0.f ? 0.f : ll);
+  const float lse = ll == 0.f ? -INFINITY : (base + log2f(ll)) * 0.6931471805599453f;
+  const int64_t t = bag.q0 + r / p.G;
+  const int hq = h * p.G + r % p.G;
+  for (int d = (tid & 7) * 8; d < p.D; d += 64) {
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      v[j] = 0.f;
+#pragma unroll
+      for (int q = 0; q < kFewWarps; ++q) v[j] = fmaf(s_o[q][row][d + j], f[q], v[j]);
+      v[j] *= inv;
+    }
+    if (p.splits == 1) store_vec(static_cast<T*>(p.out) + t * p.os + hq * p.oh + d, v);
+    else store_vec(p.po + (((int64_t)sp * p.Tq + t) * p.Hq + hq) * p.D + d, v);
+  }
+  if ((tid & 7) == 0) {
+    if (p.splits == 1) p.lse[t * p.Hq + hq] = lse;
+    else p.pl[((int64_t)sp * p.Tq + t) * p.Hq + hq] = lse;
+  }
+}
+
+// Joins the parts of the keys: out = sum_s exp(lse_s - lse) out_s; one warp a
+// (query, head), 4 columns a lane.
+template <typename T>
+__global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ AttendParams p) {
+  const int lane = threadIdx.x & 31;
+  const int tiles = (p.max_q * p.Hq + 3) / 4;
+  const int b = blockIdx.x / tiles, i = (blockIdx.x % tiles) * 4 + (threadIdx.x >> 5);
+  const Bag bag = load_bag(p, b);
+  if (i >= bag.nq * p.Hq) return;
+  const int64_t t = bag.q0 + i / p.Hq;
+  const int hq = i % p.Hq;
+  const int n = max(1, (bag.nk + p.split_keys - 1) / p.split_keys);
+  const int64_t step = p.Tq * p.Hq, at = t * p.Hq + hq;
+  float m = -INFINITY;
+  for (int s = lane; s < n; s += 32) m = fmaxf(m, __ldg(p.pl + s * step + at));
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+  const float base = m == -INFINITY ? 0.f : m;
+  float sum = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int d = lane * 4;
+  for (int s = 0; s < n; ++s) {
+    const float f = expf(__ldg(p.pl + s * step + at) - base);
+    sum += f;
+    if (d < p.D) {
+      const float4 v = *reinterpret_cast<const float4*>(p.po + (s * step + at) * p.D + d);
+      acc.x = fmaf(f, v.x, acc.x);
+      acc.y = fmaf(f, v.y, acc.y);
+      acc.z = fmaf(f, v.z, acc.z);
+      acc.w = fmaf(f, v.w, acc.w);
+    }
+  }
+  const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+  if (d < p.D) {
+    uint2 u = make_uint2(pack2<T>(acc.x * inv, acc.y * inv), pack2<T>(acc.z * inv, acc.w * inv));
+    *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + t * p.os + hq * p.oh + d) = u;
+  }
+  if (lane == 0) p.lse[at] = sum == 0.f ? -INFINITY : base + logf(sum);
+}
+
+// ---------------------------------------------------------------- backward
+// delta[t][h] = sum_d grad_out * out: one warp a (query, head)
+template <typename T>
+__global__ void __launch_bounds__(256) delta_kernel(const __grid_constant__ AttendParams p) {
+  const int lane = threadIdx.x & 31, d = lane * 4;
+  const int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (i >= p.Tq * p.Hq) return;
+  const int64_t t = i / p.Hq;
+  const int h = (int)(i % p.Hq);
+  float s = 0.f;
+  if (d < p.D) {
+    const uint2 a = *reinterpret_cast<const uint2*>(static_cast<const T*>(p.out) + t * p.os + h * p.oh + d);
+    const uint2 b = *reinterpret_cast<const uint2*>(static_cast<const T*>(p.go) + t * p.gos + h * p.goh + d);
+    const float2 a0 = unpack2<T>(a.x), a1 = unpack2<T>(a.y), b0 = unpack2<T>(b.x), b1 = unpack2<T>(b.y);
+    s = a0.x * b0.x + a0.y * b0.y + a1.x * b1.x + a1.y * b1.y;
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+  if (lane == 0) p.delta[i] = s;
+}
+
+template <typename T>
+__device__ __forceinline__ float4 load4(const void* base, int64_t at, int d, int D) {
+  if (d >= D) return make_float4(0.f, 0.f, 0.f, 0.f);
+  const uint2 a = *reinterpret_cast<const uint2*>(static_cast<const T*>(base) + at + d);
+  const float2 x = unpack2<T>(a.x), y = unpack2<T>(a.y);
+  return make_float4(x.x, x.y, y.x, y.y);
+}
+__device__ __forceinline__ float dot4(float4 a, float4 b) { return a.x * b.x + a.y * b.y + a.z * b.z + a.w * b.w; }
+__device__ __forceinline__ void warp_sum2(float& a, float& b) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    a += __shfl_xor_sync(0xffffffffu, a, off);
+    b += __shfl_xor_sync(0xffffffffu, b, off);
+  }
+}
+__device__ __forceinline__ void axpy4(float4& y, float a, float4 x) {
+  y.x = fmaf(a, x.x, y.x);
+  y.y = fmaf(a, x.y, y.y);
+  y.z = fmaf(a, x.z, y.z);
+  y.w = fmaf(a, x.w, y.w);
+}
+template <typename T>
+__device__ __forceinline__ void put4(void* base, int64_t at, int d, int D, float4 v) {
+  if (d < D)
+    *reinterpret_cast<uint2*>(static_cast<T*>(base) + at + d) = make_uint2(pack2<T>(v.x, v.y), pack2<T>(v.z, v.w));
+}
+
+// one warp a (query, head): grad_q over the bag's keys
+template <typename T>
+__global__ void __launch_bounds__(128) back_q_kernel(const __grid_constant__ AttendParams p) {
+  const int lane = threadIdx.x & 31, d = lane * 4;
+  const int tiles = (p.max_q * p.Hq + 3) / 4;
+  const int b = blockIdx.x / tiles, i = (blockIdx.x % tiles) * 4 + (threadIdx.x >> 5);
+  const Bag bag = load_bag(p, b);
+  if (i >= bag.nq * p.Hq) return;
+  const int64_t t = bag.q0 + i / p.Hq;
+  const int hq = i % p.Hq, h = hq / p.G;
+  const float4 q = load4<T>(p.q, t * p.qs + hq * p.qh, d, p.D), go = load4<T>(p.go, t * p.gos + hq * p.goh, d, p.D);
+  const float lse = p.lse[t * p.Hq + hq], delta = p.delta[t * p.Hq + hq];
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int j = 0; j < bag.nk; ++j) {
+    if (p.mask && !p.mask[bag.k0 + j]) continue;
+    const float4 k = load4<T>(p.k, (bag.k0 + j) * p.ks + h * p.kh, d, p.D);
+    float s = dot4(q, k), dp = dot4(go, load4<T>(p.v, (bag.k0 + j) * p.vs + h * p.vh, d, p.D));
+    warp_sum2(s, dp);
+    axpy4(acc, expf(s * p.scale - lse) * (dp - delta) * p.scale, k);
+  }
+  put4<T>(p.gq, t * p.gqs + hq * p.gqh, d, p.D, acc);
+}
+
+// one warp a (key, key head): grad_k and grad_v over the bag's rows
+template <typename T>
+__global__ void __launch_bounds__(128) back_k_kernel(const __grid_constant__ AttendParams p) {
+  const int lane = threadIdx.x & 31, d = lane * 4;
+  const int tiles = (p.max_k * p.Hkv + 3) / 4;
+  const int b = blockIdx.x / tiles, i = (blockIdx.x % tiles) * 4 + (threadIdx.x >> 5);
+  const Bag bag = load_bag(p, b);
+  if (i >= bag.nk * p.Hkv) return;
+  const int64_t t = bag.k0 + i / p.Hkv;
+  const int h = i % p.Hkv;
+  float4 gk = make_float4(0.f, 0.f, 0.f, 0.f), gv = gk;
+  if (!p.mask || p.mask[t]) {
+    const float4 k = load4<T>(p.k, t * p.ks + h * p.kh, d, p.D), v = load4<T>(p.v, t * p.vs + h * p.vh, d, p.D);
+    for (int r = 0; r < bag.nq * p.G; ++r) {
+      const int64_t tq = bag.q0 + r / p.G;
+      const int hq = h * p.G + r % p.G;
+      const float4 q = load4<T>(p.q, tq * p.qs + hq * p.qh, d, p.D);
+      const float4 go = load4<T>(p.go, tq * p.gos + hq * p.goh, d, p.D);
+      float s = dot4(q, k), dp = dot4(go, v);
+      warp_sum2(s, dp);
+      const float pr = expf(s * p.scale - p.lse[tq * p.Hq + hq]);
+      axpy4(gv, pr, go);
+      axpy4(gk, pr * (dp - p.delta[tq * p.Hq + hq]) * p.scale, q);
+    }
+  }
+  put4<T>(p.gk, t * p.gks + h * p.gkh, d, p.D, gk);
+  put4<T>(p.gv, t * p.gvs + h * p.gvh, d, p.D, gv);
+}
+
+// ---------------------------------------------------------------- host
+struct AttendPlan {
+  int splits, split_keys;
+  int64_t po_bytes, pl_bytes, delta_bytes;
+  int64_t bytes;
+};
+
+AttendPlan attend_plan(const recis_attend_args& a, bool backward) {
+  AttendPlan g = {};
+  g.splits = 1;
+  g.split_keys = (int)std::max<int64_t>(a.max_k, 1);
+  if (backward) {
+    g.delta_bytes = align256(a.Tq * a.Hq * 4);
+  } else {
+    // parts of the keys: enough blocks for every SM to hold a few, each part
+    // at least 256 keys (16 iterations a warp hide its fixed cost)
+    const int64_t G = a.Hq / a.Hkv, rtiles = std::max<int64_t>(1, (a.max_q * G + kRowTile - 1) / kRowTile);
+    const int64_t blocks = std::max<int64_t>(1, a.B * a.Hkv * rtiles);
+    const int64_t want = std::min<int64_t>((kSMs * 8 + blocks - 1) / blocks, (a.max_k + 255) / 256);
+    if (want > 1) {
+      g.split_keys = (int)((a.max_k + want - 1) / want + 63) / 64 * 64;
+      g.splits = (int)((a.max_k + g.split_keys - 1) / g.split_keys);
+    }
+    if (g.splits > 1) {
+      g.po_bytes = align256(g.splits * a.Tq * a.Hq * a.D * 4);
+      g.pl_bytes = align256(g.splits * a.Tq * a.Hq * 4);
+    }
+  }
+  g.bytes = g.po_bytes + g.pl_bytes + g.delta_bytes;
+  return g;
+}
+
+recis_status check_sizes(const recis_attend_args* a, const char* what) {
+  const int64_t top = INT32_MAX;
+  if (!a || (a->type != RECIS_BF16 && a->type != RECIS_F16) || a->D < 8 || a->D > 128 || a->D % 8 != 0 || a->Hkv < 1 ||
+      a->Hq < a->Hkv || a->Hq % a->Hkv != 0 || a->Hq / a->Hkv > 128 || a->B < 0 || a->Tq < 0 || a->Tk < 0 ||
+      a->max_q < 0 || a->max_k < 0 || a->B >= top || a->Tq >= top || a->Tk >= top || a->max_q >= top ||
+      a->max_k >= top || a->max_q * a->Hq >= top || a->max_k * a->Hkv >= top || !(a->scale > -1e30 && a->scale < 1e30)) {
+    set_error(std::string(what) + ": bad arguments (bf16 or fp16, D a multiple of 8 up to 128, Hq a multiple of Hkv, max_q * Hq and max_k * Hkv below 2^31)");
+    return RECIS_ERR_INVALID_ARG;
+  }
+  return RECIS_OK;
+}
+
+// rows of heads of D elements: aligned for 16-byte accesses
+bool bad_array(const void* p, int64_t stride, int64_t head_stride, int64_t rows) {
+  return rows > 0 && (!p || misaligned(p, 16) || stride % 8 != 0 || head_stride % 8 != 0 || stride < 0 ||
+                      head_stride < 0);
+}
+
+// bags, rows and blocks of a launch fit its grid
+bool grid_fits(int64_t n) { return n < ((int64_t)1 << 31); }
+
+recis_status fill(const recis_attend_args* a, AttendParams* p, const AttendPlan& g, void* ws) {
+  int* st = sequence_status();
+  if (!st) {
+    set_error("the sequence operators' status word is not reachable (no usable sm_100 device?)");
+    return RECIS_ERR_NO_DEVICE;
+  }
+  *p = AttendParams{};
+  p->q = a->q; p->k = a->k; p->v = a->v; p->go = a->grad_out;
+  p->out = a->out; p->gq = a->grad_q; p->gk = a->grad_k; p->gv = a->grad_v;
+  p->lse = a->lse;
+  p->qo = a->q_offsets; p->ko = a->k_offsets; p->mask = a->key_mask;
+  p->qs = a->q_stride; p->qh = a->q_head_stride; p->ks = a->k_stride; p->kh = a->k_head_stride;
+  p->vs = a->v_stride; p->vh = a->v_head_stride; p->os = a->out_stride; p->oh = a->out_head_stride;
+  p->gos = a->grad_out_stride; p->goh = a->grad_out_head_stride;
+  p->gqs = a->grad_q_stride; p->gqh = a->grad_q_head_stride; p->gks = a->grad_k_stride; p->gkh = a->grad_k_head_stride;
+  p->gvs = a->grad_v_stride; p->gvh = a->grad_v_head_stride;
+  p->Tq = a->Tq; p->Tk = a->Tk;
+  p->B = (int)a->B; p->Hq = a->Hq; p->Hkv = a->Hkv; p->G = a->Hq / a->Hkv; p->D = a->D;
+  p->max_q = (int)a->max_q; p->max_k = (int)a->max_k;
+  p->scale = (float)a->scale;
+  p->scale_log2 = (float)(a->scale * 1.4426950408889634);
+  p->splits = g.splits;
+  p->split_keys = g.split_keys;
+  char* at = static_cast<char*>(ws);
+  p->po = reinterpret_cast<float*>(at);
+  p->pl = reinterpret_cast<float*>(at + g.po_bytes);
+  p->delta = reinterpret_cast<float*>(at + g.po_bytes + g.pl_bytes);
+  p->status = st;
+  return RECIS_OK;
+}
+
+template <typename T>
+recis_status forward(const AttendParams& p, cudaStream_t s) {
+  const int64_t rtiles = ((int64_t)p.max_q * p.G + kRowTile - 1) / kRowTile;
+  const int64_t grid = (int64_t)p.B * p.splits * p.Hkv * rtiles, jgrid = (int64_t)p.B * (((int64_t)p.max_q * p.Hq + 3) / 4);
+  if (!grid_fits(grid) || !grid_fits(jgrid)) {
+    set_error("attend: too many blocks (bags times max_q times heads)");
+    return RECIS_ERR_INVALID_ARG;
+  }
+  {
+    LaunchScope ls("attend_few", s);
+    if (p.D <= 32) few_kernel<T, 32><<<(unsigned)grid, kFewWarps * 32, 0, s>>>(p);
+    else if (p.D <= 64) few_kernel<T, 64><<<(unsigned)grid, kFewWarps * 32, 0, s>>>(p);
+    else few_kernel<T, 128><<<(unsigned)grid, kFewWarps * 32, 0, s>>>(p);
+  }
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e, "attend launch");
+  if (p.splits > 1) {
+    LaunchScope ls("attend_join", s);
+    join_kernel<T><<<(unsigned)jgrid, 128, 0, s>>>(p);
+    if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "attend_join launch");
+  }
+  return RECIS_OK;
+}
+
+template <typename T>
+recis_status backward(const AttendParams& p, cudaStream_t s) {
+  const int64_t qgrid = (int64_t)p.B * (((int64_t)p.max_q * p.Hq + 3) / 4);
+  const int64_t kgrid = (int64_t)p.B * (((int64_t)p.max_k * p.Hkv + 3) / 4);
+  const int64_t dgrid = (p.Tq * p.Hq + 7) / 8;
+  if (!grid_fits(qgrid) || !grid_fits(kgrid) || !grid_fits(dgrid)) {
+    set_error("attend_backward: too many blocks (bags times longest bag times heads)");
+    return RECIS_ERR_INVALID_ARG;
+  }
+  cudaError_t e;
+  if (dgrid > 0) {
+    LaunchScope ls("attend_delta", s);
+    delta_kernel<T><<<(unsigned)dgrid, 256, 0, s>>>(p);
+    if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "attend_delta launch");
+  }
+  if (qgrid > 0) {
+    LaunchScope ls("attend_back_q", s);
+    back_q_kernel<T><<<(unsigned)qgrid, 128, 0, s>>>(p);
+    if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "attend_back_q launch");
+  }
+  if (kgrid > 0) {
+    LaunchScope ls("attend_back_k", s);
+    back_k_kernel<T><<<(unsigned)kgrid, 128, 0, s>>>(p);
+    if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "attend_back_k launch");
+  }
+  return RECIS_OK;
+}
+
+}  // namespace
+}  // namespace recis
+
+using namespace recis;
+
+extern "C" recis_status recis_attend_workspace(const recis_attend_args* a, int32_t backward, int64_t* bytes_out) {
+  recis_status st = check_sizes(a, "attend_workspace");
+  if (st != RECIS_OK) return st;
+  if (!bytes_out) {
+    set_error("attend_workspace: null argument");
+    return RECIS_ERR_INVALID_ARG;
+  }
+  *bytes_out = attend_plan(*a, backward != 0).bytes;
+  return RECIS_OK;
+}
+
+static recis_status check_call(const recis_attend_args* a, bool backward, void* ws, int64_t ws_bytes, const char* what) {
+  const recis_status st = check_sizes(a, what);
+  if (st != RECIS_OK) return st;
+  bool bad = (a->B > 0 && (!a->q_offsets || !a->k_offsets)) || misaligned(a->q_offsets, 8) ||
+             misaligned(a->k_offsets, 8) || misaligned(a->lse, 4) || (a->Tq > 0 && !a->lse);
+  bad = bad || bad_array(a->q, a->q_stride, a->q_head_stride, a->Tq) ||
+        bad_array(a->k, a->k_stride, a->k_head_stride, a->Tk) || bad_array(a->v, a->v_stride, a->v_head_stride, a->Tk) ||
+        bad_array(a->out, a->out_stride, a->out_head_stride, a->Tq);
+  if (backward)
+    bad = bad || bad_array(a->grad_out, a->grad_out_stride, a->grad_out_head_stride, a->Tq) ||
+          bad_array(a->grad_q, a->grad_q_stride, a->grad_q_head_stride, a->Tq) ||
+          bad_array(a->grad_k, a->grad_k_stride, a->grad_k_head_stride, a->Tk) ||
+          bad_array(a->grad_v, a->grad_v_stride, a->grad_v_head_stride, a->Tk);
+  if (bad) {
+    set_error(std::string(what) + ": null or misaligned array, or a stride that is not a multiple of 8 elements");
+    return RECIS_ERR_INVALID_ARG;
+  }
+  const int64_t need = attend_plan(*a, backward).bytes;
+  if (misaligned(ws, 256) || (need > 0 && (!ws || ws_bytes < need))) {
+    set_error(std::string(what) + ": workspace too small or not 256-byte aligned");
+    return RECIS_ERR_INVALID_ARG;
+  }
+  return RECIS_OK;
+}
+
+extern "C" recis_status recis_attend(const recis_attend_args* a, void* workspace, int64_t workspace_bytes,
+                                     recis_stream_t stream) {
+  recis_status st = check_call(a, false, workspace, workspace_bytes, "attend");
+  if (st != RECIS_OK) return st;
+  if (a->B == 0 || a->Tq == 0 || a->max_q == 0) return RECIS_OK;
+  AttendParams p;
+  if ((st = fill(a, &p, attend_plan(*a, false), workspace)) != RECIS_OK) return st;
+  return a->type == RECIS_BF16 ? forward<__nv_bfloat16>(p, (cudaStream_t)stream)
+                               : forward<__half>(p, (cudaStream_t)stream);
+}
+
+extern "C" recis_status recis_attend_backward(const recis_attend_args* a, void* workspace, int64_t workspace_bytes,
+                                              recis_stream_t stream) {
+  recis_status st = check_call(a, true, workspace, workspace_bytes, "attend_backward");
+  if (st != RECIS_OK) return st;
+  if (a->B == 0) return RECIS_OK;
+  AttendParams p;
+  if ((st = fill(a, &p, attend_plan(*a, true), workspace)) != RECIS_OK) return st;
+  return a->type == RECIS_BF16 ? backward<__nv_bfloat16>(p, (cudaStream_t)stream)
+                               : backward<__half>(p, (cudaStream_t)stream);
+}

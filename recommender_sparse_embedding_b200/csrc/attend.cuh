@@ -1,0 +1,45 @@
+// attend.cuh -- shared by the attention kernels (attend.cu, attend_back.cu).
+#pragma once
+#include "seqops.cuh"
+
+namespace recis {
+
+// What every attention kernel is given: recis_attend_args with the group size
+// and the plan of the call.
+struct AttendParams {
+  const void *q, *k, *v, *go;
+  void *out, *gq, *gk, *gv;
+  float* lse;
+  const int64_t *qo, *ko;
+  const uint8_t* mask;
+  int64_t qs, qh, ks, kh, vs, vh, os, oh, gos, goh, gqs, gqh, gks, gkh, gvs, gvh;  // strides: row, head
+  int64_t Tq, Tk;
+  int B, Hq, Hkv, G, D;
+  int max_q, max_k;
+  float scale, scale_log2;  // scale, scale * log2(e)
+  int splits, split_keys;   // parts of a bag's keys, keys a part
+  float* po;                // splits > 1: [splits][Tq][Hq][D] each part's output ...
+  float* pl;                // ... and [splits][Tq][Hq] its lse
+  float* delta;             // backward: [Tq][Hq] sum(grad_out * out)
+  int* status;
+};
+
+struct Bag {
+  int64_t q0, k0;
+  int nq, nk;
+};
+
+// Bag b's rows; a bag whose offsets are malformed or that passes its bound is
+// reported and has none, so no access leaves the arrays.
+__device__ __forceinline__ Bag load_bag(const AttendParams& p, int b) {
+  const int64_t q0 = __ldg(p.qo + b), q1 = __ldg(p.qo + b + 1), k0 = __ldg(p.ko + b), k1 = __ldg(p.ko + b + 1);
+  const bool ok = q0 >= 0 && q1 >= q0 && q1 <= p.Tq && q1 - q0 <= p.max_q && k0 >= 0 && k1 >= k0 && k1 <= p.Tk &&
+                  k1 - k0 <= p.max_k;
+  if (!ok) {
+    if (threadIdx.x == 0) atomicOr(p.status, kErrBadOffsets);
+    return Bag{0, 0, 0, 0};
+  }
+  return Bag{q0, k0, (int)(q1 - q0), (int)(k1 - k0)};
+}
+
+}  // namespace recis

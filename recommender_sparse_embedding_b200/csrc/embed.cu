@@ -1,0 +1,707 @@
+// embed.cu -- dense embedding tables: rows of a [V][D] weight looked up by
+// token with a scale, and the weight's gradient by sorted tokens.
+//
+//   out[i] = scale * W[t_i]            dW[v] = scale * sum_{i : t_i = v} dout[i]
+//
+// Both are bound by memory: the lookup reads N rows and writes N, the
+// gradient reads N rows of dout and writes the V rows of dW.
+//
+// The gradient sorts (token, position) by a stable radix sort, so that a row's
+// terms are added in occurrence order whatever the scheduling.  The sorted
+// positions are cut into spans; a group of lanes walks one span, 8 columns a
+// lane, and adds the rows of equal tokens in fp32 (at most kSpan terms).  A
+// run of one token inside a span is finished there; a run cut by span ends
+// leaves one fp32 partial per span, and a second kernel adds those in span
+// order, in fp64 -- a hot token's thousands of rows are summed by as many
+// groups, and no float atomic is used.
+#include <algorithm>
+
+#include "seqops.cuh"
+
+namespace recis {
+
+namespace {
+
+__device__ int g_seq_status;
+
+constexpr int kSmallN = 1024;     // up to here one kernel finds and sums each token's rows
+constexpr int kSortThreads = 256;
+constexpr int kMaxDigit = 10;     // bits a pass sorts by
+constexpr int kSpan = 64;         // sorted positions a group of lanes walks
+
+__host__ __device__ constexpr int64_t align256(int64_t b) { return (b + 255) & ~(int64_t)255; }
+
+// ---------------------------------------------------------------- lookup
+struct LookupParams {
+  const void* w;
+  const int64_t* tok;
+  void* out;
+  int64_t V, N, out_stride, padding;
+  int D, units, lanes;  // lanes: threads a row (a power of two)
+  float scale;
+  int* status;
+};
+
+// `lanes` threads walk the columns of R rows at once, so R independent row
+// loads a thread are in flight.
+template <typename TW, typename TO, int VEC, int R>
+__global__ void __launch_bounds__(256) embed_lookup_kernel(const __grid_constant__ LookupParams p) {
+  const int lane = threadIdx.x & (p.lanes - 1);
+  const int64_t group = ((int64_t)blockIdx.x * 256 + threadIdx.x) / p.lanes;
+  const int64_t groups = (int64_t)gridDim.x * 256 / p.lanes;
+  for (int64_t r0 = group * R; r0 < p.N; r0 += groups * R) {
+    int64_t t[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) t[r] = r0 + r < p.N ? __ldg(p.tok + r0 + r) : p.padding;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (t[r] == p.padding) t[r] = -1;
+      else if (t[r] < 0 || t[r] >= p.V) {
+        if (lane == 0) atomicOr(p.status, kErrTagOverflow);
+        t[r] = -1;
+      }
+    }
+    for (int c = lane; c < p.units; c += p.lanes) {
+      RawVec<TW, VEC> v[R];
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        if (t[r] >= 0) v[r].load(static_cast<const TW*>(p.w) + t[r] * p.D + (int64_t)c * VEC);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        if (r0 + r >= p.N) break;
+        float f[VEC];
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) f[j] = 0.f;
+        if (t[r] >= 0) {
+          v[r].unpack(f);
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) f[j] *= p.scale;
+        }
+        store_vec(static_cast<TO*>(p.out) + (r0 + r) * p.out_stride + (int64_t)c * VEC, f);
+      }
+    }
+  }
+}
+
+template <typename TW, typename TO, int VEC>
+cudaError_t lookup_launch(LookupParams p, cudaStream_t s) {
+  p.units = p.D / VEC;
+  p.lanes = 1;
+  while (p.lanes < p.units && p.lanes < 256) p.lanes *= 2;
+  // four rows a group once that still fills the machine; one row each below
+  const bool many = p.N / 4 * p.lanes >= (int64_t)kSMs * 1024;
+  const int64_t groups = many ? (p.N + 3) / 4 : p.N;
+  const int64_t blocks = std::min<int64_t>((groups * p.lanes + 255) / 256, (int64_t)1 << 30);
+  LaunchScope ls("embed_lookup", s);
+  if (many) embed_lookup_kernel<TW, TO, VEC, 4><<<(unsigned)blocks, 256, 0, s>>>(p);
+  else embed_lookup_kernel<TW, TO, VEC, 1><<<(unsigned)blocks, 256, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+// ---------------------------------------------------------------- gradient: radix sort
+// Sort key of a token: itself, or V for padding and tokens out of range (they
+// end up behind every row).
+__device__ __forceinline__ uint32_t sort_key(int64_t t, int64_t V, int64_t padding, int* status, bool report) {
+  if (t == padding) return (uint32_t)V;
+  if (t < 0 || t >= V) {
+    if (report) atomicOr(status, kErrTagOverflow);
+    return (uint32_t)V;
+  }
+  return (uint32_t)t;
+}
+
+struct PassParams {
+  const int64_t* tok;       // first pass: the tokens; later passes read `in`
+  const uint2* in;          // {key, position}
+  uint2* out;
+  int64_t N, V, padding;
+  int shift, bits;          // the pass's digit
+  int tiles;
+  uint32_t* hist;           // [tiles][bins]: counts, then exclusive prefixes over tiles
+  uint32_t* total;          // [bins]
+  int* status;
+};
+
+template <int ITEMS>
+__device__ __forceinline__ uint2 pass_item(const PassParams& p, int64_t i, bool report) {
+  if (p.in) return p.in[i];
+  return make_uint2(sort_key(p.tok[i], p.V, p.padding, p.status, report), (uint32_t)i);
+}
+
+// digit counts of each tile
+template <int ITEMS>
+__global__ void __launch_bounds__(kSortThreads) grad_count_kernel(const __grid_constant__ PassParams p) {
+  __shared__ uint32_t s_h[1 << kMaxDigit];
+  const int bins = 1 << p.bits;
+  pdl_wait();
+  for (int b = threadIdx.x; b < bins; b += kSortThreads) s_h[b] = 0;
+  __syncthreads();
+  const int64_t base = (int64_t)blockIdx.x * (kSortThreads * ITEMS);
+#pragma unroll
+  for (int j = 0; j < ITEMS; ++j) {
+    const int64_t i = base + j * kSortThreads + threadIdx.x;
+    if (i < p.N) atomicAdd(&s_h[(pass_item<ITEMS>(p, i, true).x >> p.shift) & (bins - 1)], 1u);
+  }
+  __syncthreads();
+  pdl_trigger();
+  for (int b = threadIdx.x; b < bins; b += kSortThreads) p.hist[(size_t)blockIdx.x * bins + b] = s_h[b];
+}
+
+// exclusive prefix over tiles of each bin's counts, and its total; a block
+// takes 32 bins, warp w the w-th part of the tiles
+__global__ void __launch_bounds__(1024) grad_scan_kernel(const __grid_constant__ PassParams p) {
+  __shared__ uint32_t s_part[32][33];
+  const int bins = 1 << p.bits, lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int b = blockIdx.x * 32 + lane;
+  const int per = (p.tiles + 31) / 32;
+  const int t0 = min(w * per, p.tiles), t1 = min(t0 + per, p.tiles);
+  pdl_wait();
+  uint32_t sum = 0;
+  if (b < bins)
+    for (int t = t0; t < t1; ++t) sum += p.hist[(size_t)t * bins + b];
+  s_part[w][lane] = sum;
+  __syncthreads();
+  uint32_t run = 0;
+  for (int q = 0; q < w; ++q) run += s_part[q][lane];
+  if (b < bins) {
+    for (int t = t0; t < t1; ++t) {
+      const uint32_t c = p.hist[(size_t)t * bins + b];
+      p.hist[(size_t)t * bins + b] = run;
+      run += c;
+    }
+    if (w == 31) p.total[b] = run;
+  }
+  pdl_trigger();
+}
+
+// stable move: a key's place = keys of lower digits + the same digit's keys in
+// earlier tiles, earlier warps of the tile, and before it in its warp
+template <int ITEMS>
+__global__ void __launch_bounds__(kSortThreads) grad_scatter_kernel(const __grid_constant__ PassParams p) {
+  constexpr int kWarps = kSortThreads / 32;
+  extern __shared__ uint32_t s_cnt[];  // [kWarps][bins], then the digits' bases [bins]
+  __shared__ uint32_t s_w[kWarps];
+  const int bins = 1 << p.bits, tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  uint32_t* s_base = s_cnt + kWarps * bins;
+  for (int b = tid; b < kWarps * bins; b += kSortThreads) s_cnt[b] = 0;
+  pdl_wait();
+  // exclusive scan of the digit totals: 4 (at most) consecutive bins a thread
+  const int per = (bins + kSortThreads - 1) / kSortThreads;
+  uint32_t mine = 0;
+  for (int j = 0; j < per; ++j) {
+    const int b = tid * per + j;
+    if (b < bins) mine += p.total[b];
+  }
+  uint32_t x = mine;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, x, off);
+    if (lane >= off) x += y;
+  }
+  if (lane == 31) s_w[w] = x;
+  __syncthreads();
+  uint32_t run = x - mine;
+  for (int q = 0; q < w; ++q) run += s_w[q];
+  for (int j = 0; j < per; ++j) {
+    const int b = tid * per + j;
+    if (b < bins) {
+      s_base[b] = run + p.hist[(size_t)blockIdx.x * bins + b];
+      run += p.total[b];
+    }
+  }
+  // ranks within the warp's keys, in order
+  const int64_t base = (int64_t)blockIdx.x * (kSortThreads * ITEMS) + (int64_t)w * 32 * ITEMS + lane;
+  uint32_t* cnt = s_cnt + w * bins;
+  uint2 v[ITEMS];
+  uint32_t rank[ITEMS];
+#pragma unroll
+  for (int j = 0; j < ITEMS; ++j)
+    v[j] = base + j * 32 < p.N ? pass_item<ITEMS>(p, base + j * 32, false) : make_uint2(0, 0);
+#pragma unroll
+  for (int j = 0; j < ITEMS; ++j) {
+    const bool ok = base + j * 32 < p.N;
+    const uint32_t d = (v[j].x >> p.shift) & (bins - 1);
+    const unsigned peers = __match_any_sync(0xffffffffu, ok ? d : 0xffffffffu);
+    const uint32_t before = ok ? cnt[d] : 0;
+    rank[j] = before + __popc(peers & ((1u << lane) - 1u));
+    __syncwarp();
+    if (ok && lane == __ffs(peers) - 1) cnt[d] = before + __popc(peers);
+    __syncwarp();
+  }
+  __syncthreads();
+  for (int b = tid; b < bins; b += kSortThreads) {
+    uint32_t at = s_base[b];
+    for (int q = 0; q < kWarps; ++q) {
+      const uint32_t c = s_cnt[q * bins + b];
+      s_cnt[q * bins + b] = at;
+      at += c;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < ITEMS; ++j)
+    if (base + j * 32 < p.N) p.out[cnt[(v[j].x >> p.shift) & (bins - 1)] + rank[j]] = v[j];
+  pdl_trigger();
+}
+
+// ---------------------------------------------------------------- gradient: sums
+struct SumParams {
+  const uint2* pairs;   // sorted {token, position}
+  const int64_t* tok;   // small path: the tokens
+  const void* g;
+  void* dw;
+  float* partial;       // [spans][2][D]: 0 a run begun in an earlier span, 1 the run that goes on into the next
+  int64_t N, V, g_stride, padding;
+  int D, units, lanes;
+  int accumulate;
+  float scale;
+  int* status;
+};
+
+// dw[row][c ..] (+)= scale * f
+template <typename TO, int VEC>
+__device__ __forceinline__ void grad_store(const SumParams& p, int64_t row, int c, float (&f)[VEC]) {
+  TO* at = static_cast<TO*>(p.dw) + row * p.D + (int64_t)c * VEC;
+  if (p.accumulate) {
+    RawVec<TO, VEC> old;
+    old.load(at);
+    float o[VEC];
+    old.unpack(o);
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) f[j] = fmaf(p.scale, f[j], o[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) f[j] *= p.scale;
+  }
+  store_vec(at, f);
+}
+
+// One group of `lanes` lanes (at most a warp) walks one span; blockIdx.y picks
+// the group's columns.  Rows are loaded 8 at a time, all in flight.
+template <typename TG, typename TO, int VEC>
+__global__ void __launch_bounds__(256) grad_span_kernel(const __grid_constant__ SumParams p) {
+  constexpr int U = 8;
+  const int lane = threadIdx.x & (p.lanes - 1);
+  const int64_t span = ((int64_t)blockIdx.x * 256 + threadIdx.x) / p.lanes;
+  const int64_t p0 = span * kSpan;
+  const int c = blockIdx.y * p.lanes + lane;
+  pdl_wait();
+  if (p0 >= p.N) return;
+  const int64_t p1 = p0 + kSpan < p.N ? p0 + kSpan : p.N;
+  const bool in = c < p.units;
+  float acc[VEC];
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) acc[j] = 0.f;
+  uint32_t cur = p.pairs[p0].x;
+  bool begun_before = p0 > 0 && p.pairs[p0 - 1].x == cur;
+  for (int64_t q = p0; q < p1; q += U) {
+    uint2 e[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) e[u] = q + u < p1 ? __ldg(p.pairs + q + u) : make_uint2((uint32_t)p.V, 0);
+    RawVec<TG, VEC> r[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (e[u].x < (uint32_t)p.V && in)
+        r[u].load(static_cast<const TG*>(p.g) + (int64_t)e[u].y * p.g_stride + (int64_t)c * VEC);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (q + u >= p1) break;
+      if (e[u].x != cur) {  // the run of `cur` ends in this span
+        if (in && cur < (uint32_t)p.V) {
+          if (begun_before) {
+            float* at = p.partial + (span * 2) * (int64_t)p.D + (int64_t)c * VEC;
+            store_vec(at, acc);
+          } else {
+            grad_store<TO, VEC>(p, cur, c, acc);
+          }
+        }
+        begun_before = false;
+        cur = e[u].x;
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) acc[j] = 0.f;
+      }
+      if (e[u].x < (uint32_t)p.V && in) {
+        float f[VEC];
+        r[u].unpack(f);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) acc[j] += f[j];
+      }
+    }
+  }
+  if (!in || cur >= (uint32_t)p.V) return;
+  const bool goes_on = p1 < p.N && p.pairs[p1].x == cur;
+  if (begun_before || goes_on) {
+    float* at = p.partial + (span * 2 + (begun_before ? 0 : 1)) * (int64_t)p.D + (int64_t)c * VEC;
+    store_vec(at, acc);
+  } else {
+    grad_store<TO, VEC>(p, cur, c, acc);
+  }
+}
+
+// Joins the runs cut by span ends: the block of the span in which such a run
+// begins adds the spans' partials, `256 / lanes` strided groups in fp64, then
+// the groups' sums in group order.
+template <typename TO, int VEC>
+__global__ void __launch_bounds__(256) grad_join_kernel(const __grid_constant__ SumParams p) {
+  __shared__ double s_sum[256][VEC];
+  __shared__ int64_t s_last;
+  const int64_t spans = (p.N + kSpan - 1) / kSpan;
+  const int lane = threadIdx.x & (p.lanes - 1), group = threadIdx.x / p.lanes, groups = 256 / p.lanes;
+  const int c = blockIdx.y * p.lanes + lane;
+  pdl_wait();
+  for (int64_t span = blockIdx.x; span + 1 < spans; span += gridDim.x) {
+    const int64_t p0 = span * kSpan, p1 = p0 + kSpan;
+    const uint32_t key = p.pairs[p1 - 1].x;
+    if (key >= (uint32_t)p.V || p.pairs[p1].x != key) continue;       // nothing goes on
+    if (p.pairs[p0].x == key && p0 > 0 && p.pairs[p0 - 1].x == key) continue;  // begun in an earlier span
+    if (threadIdx.x < 32) {  // the span the run ends in: 32 span ends a step
+      int64_t last = span;
+      for (int64_t t = span + 1;; t += 32) {
+        const int64_t mine = t + threadIdx.x, end = mine * kSpan + kSpan;
+        const bool whole = mine < spans && end < p.N && p.pairs[end].x == key;  // the run goes past span `mine`
+        const unsigned m = __ballot_sync(0xffffffffu, whole);
+        const int run = __ffs(~m) - 1;  // spans passed from t on (-1: all 32)
+        if (run >= 0) {
+          last = t + run;
+          break;
+        }
+      }
+      if (threadIdx.x == 0) s_last = last;
+    }
+    __syncthreads();
+    const int64_t last = s_last;
+    double sum[VEC];
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) sum[j] = 0.0;
+    if (c < p.units) {
+      for (int64_t t = span + group; t <= last; t += groups) {
+        const float* at = p.partial + (t * 2 + (t == span ? 1 : 0)) * (int64_t)p.D + (int64_t)c * VEC;
+        RawVec<float, VEC> r;
+        r.load(at);
+        float f[VEC];
+        r.unpack(f);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) sum[j] += (double)f[j];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) s_sum[threadIdx.x][j] = sum[j];
+    __syncthreads();
+    if (group == 0 && c < p.units) {
+      float f[VEC];
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        double t = 0.0;
+        for (int q = 0; q < groups; ++q) t += s_sum[q * p.lanes + lane][j];
+        f[j] = (float)t;
+      }
+      grad_store<TO, VEC>(p, key, c, f);
+    }
+    __syncthreads();
+  }
+}
+
+// Few tokens: block i takes the run of tok[i] if no earlier position holds the
+// token, lists its positions in order and adds their rows, `256 / lanes` rows
+// at a time; the groups' sums are joined in group order in fp64.
+template <typename TG, typename TO, int VEC>
+__global__ void __launch_bounds__(256) grad_small_kernel(const __grid_constant__ SumParams p) {
+  __shared__ int s_pos[kSmallN];
+  __shared__ int s_warp[8];
+  __shared__ double s_sum[256][VEC];
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const int i = blockIdx.x, N = (int)p.N;
+  const int64_t t = p.tok[i];
+  if (t == p.padding) return;
+  if (t < 0 || t >= p.V) {
+    if (tid == 0) atomicOr(p.status, kErrTagOverflow);
+    return;
+  }
+  bool earlier = false;
+  for (int j = tid; j < i; j += 256) earlier |= p.tok[j] == t;
+  if (__syncthreads_or(earlier)) return;
+  int n = 0;
+  for (int j0 = i; j0 < N; j0 += 256) {
+    const int j = j0 + tid;
+    const bool hit = j < N && p.tok[j] == t;
+    const unsigned m = __ballot_sync(0xffffffffu, hit);
+    if (lane == 0) s_warp[w] = __popc(m);
+    __syncthreads();
+    int at = n, all = 0;
+    for (int q = 0; q < 8; ++q) {
+      if (q < w) at += s_warp[q];
+      all += s_warp[q];
+    }
+    if (hit) s_pos[at + __popc(m & ((1u << lane) - 1u))] = j;
+    n += all;
+    __syncthreads();
+  }
+  const int gl = tid & (p.lanes - 1), group = tid / p.lanes, groups = 256 / p.lanes;
+  for (int c0 = 0; c0 < p.units; c0 += p.lanes) {
+    const int c = c0 + gl;
+    float acc[VEC];
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) acc[j] = 0.f;
+    if (c < p.units) {
+#pragma unroll 4
+      for (int q = group; q < n; q += groups) {
+        RawVec<TG, VEC> r;
+        r.load(static_cast<const TG*>(p.g) + (int64_t)s_pos[q] * p.g_stride + (int64_t)c * VEC);
+        float f[VEC];
+        r.unpack(f);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) acc[j] += f[j];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) s_sum[tid][j] = (double)acc[j];
+    __syncthreads();
+    if (group == 0 && c < p.units) {
+      float f[VEC];
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        double s = 0.0;
+        for (int q = 0; q < groups && q < n; ++q) s += s_sum[q * p.lanes + gl][j];
+        f[j] = (float)s;
+      }
+      grad_store<TO, VEC>(p, t, c, f);
+    }
+    __syncthreads();
+  }
+}
+
+// ---------------------------------------------------------------- gradient: host
+struct GradPlan {
+  int items, tiles, passes, bits;  // the sort
+  int64_t pairs_bytes, hist_bytes, total_bytes, partial_bytes;
+  int64_t bytes;
+};
+
+GradPlan grad_plan(int64_t N, int64_t V, int D) {
+  GradPlan g = {};
+  if (N <= kSmallN) return g;
+  int bits = 1;
+  while (((int64_t)1 << bits) <= V) ++bits;  // keys 0 .. V
+  g.passes = (bits + kMaxDigit - 1) / kMaxDigit;
+  g.bits = (bits + g.passes - 1) / g.passes;
+  if (g.bits < 5) g.bits = 5;  // the scan takes 32 bins at a time
+  // 16 keys a thread once there are tiles for every SM, 4 below
+  g.items = N >= (int64_t)kSMs * kSortThreads * 16 ? 16 : 4;
+  const int64_t tile = (int64_t)kSortThreads * g.items;
+  g.tiles = (int)((N + tile - 1) / tile);
+  g.pairs_bytes = align256(N * 8);
+  g.hist_bytes = align256(((int64_t)g.tiles << g.bits) * 4);
+  g.total_bytes = align256(((int64_t)1 << g.bits) * 4);
+  g.partial_bytes = align256((N + kSpan - 1) / kSpan * 2 * D * 4);
+  g.bytes = 2 * g.pairs_bytes + g.hist_bytes + g.total_bytes + g.partial_bytes;
+  return g;
+}
+
+template <int ITEMS>
+cudaError_t sort_pass_launch(const PassParams& pp, cudaStream_t s) {
+  const int bins = 1 << pp.bits;
+  cudaError_t e;
+  {
+    LaunchScope ls("embed_grad_count", s);
+    if ((e = launch_pdl(grad_count_kernel<ITEMS>, (unsigned)pp.tiles, kSortThreads, 0, s, pp)) != cudaSuccess)
+      return e;
+  }
+  {
+    LaunchScope ls("embed_grad_scan", s);
+    if ((e = launch_pdl(grad_scan_kernel, (unsigned)((bins + 31) / 32), 1024, 0, s, pp)) != cudaSuccess) return e;
+  }
+  LaunchScope ls("embed_grad_scatter", s);
+  return launch_pdl(grad_scatter_kernel<ITEMS>, (unsigned)pp.tiles, kSortThreads,
+                    (size_t)(kSortThreads / 32 + 1) * bins * 4, s, pp);
+}
+
+template <typename TG, typename TO, int VEC>
+cudaError_t grad_launch(SumParams p, const int64_t* tok, char* ws, cudaStream_t s) {
+  p.units = p.D / VEC;
+  p.lanes = 1;
+  while (p.lanes < p.units && p.lanes < 32) p.lanes *= 2;
+  cudaError_t e;
+  if (!p.accumulate) {
+    e = cudaMemsetAsync(p.dw, 0, (size_t)p.V * p.D * sizeof(TO), s);
+    if (e != cudaSuccess) return e;
+  }
+  if (p.N == 0) return cudaSuccess;
+  if (p.N <= kSmallN) {
+    LaunchScope ls("embed_grad_small", s);
+    grad_small_kernel<TG, TO, VEC><<<(unsigned)p.N, 256, 0, s>>>(p);
+    return cudaGetLastError();
+  }
+  const GradPlan g = grad_plan(p.N, p.V, p.D);
+  uint2* pairs[2] = {reinterpret_cast<uint2*>(ws), reinterpret_cast<uint2*>(ws + g.pairs_bytes)};
+  PassParams pp = {};
+  pp.tok = tok;
+  pp.N = p.N;
+  pp.V = p.V;
+  pp.padding = p.padding;
+  pp.bits = g.bits;
+  pp.tiles = g.tiles;
+  pp.hist = reinterpret_cast<uint32_t*>(ws + 2 * g.pairs_bytes);
+  pp.total = reinterpret_cast<uint32_t*>(ws + 2 * g.pairs_bytes + g.hist_bytes);
+  pp.status = p.status;
+  for (int i = 0; i < g.passes; ++i) {
+    pp.shift = i * g.bits;
+    pp.in = i == 0 ? nullptr : pairs[(i + 1) & 1];
+    pp.out = pairs[i & 1];
+    e = g.items == 16 ? sort_pass_launch<16>(pp, s) : sort_pass_launch<4>(pp, s);
+    if (e != cudaSuccess) return e;
+  }
+  p.pairs = pairs[(g.passes - 1) & 1];
+  p.partial = reinterpret_cast<float*>(ws + 2 * g.pairs_bytes + g.hist_bytes + g.total_bytes);
+  const int64_t spans = (p.N + kSpan - 1) / kSpan;
+  const int cols = (p.units + p.lanes - 1) / p.lanes;
+  {
+    LaunchScope ls("embed_grad_span", s);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((spans * p.lanes + 255) / 256), (unsigned)cols);
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    if ((e = cudaLaunchKernelEx(&cfg, grad_span_kernel<TG, TO, VEC>, p)) != cudaSuccess) return e;
+  }
+  if (spans > 1) {
+    LaunchScope ls("embed_grad_join", s);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)std::min<int64_t>(spans - 1, kSMs * 8), (unsigned)cols);
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    if ((e = cudaLaunchKernelEx(&cfg, grad_join_kernel<TO, VEC>, p)) != cudaSuccess) return e;
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+int* sequence_status() {
+  static int* at[128] = {nullptr};  // per device; every writer stores the same address
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return nullptr;
+  int* p = __atomic_load_n(&at[dev], __ATOMIC_ACQUIRE);
+  if (!p) {
+    void* q = nullptr;
+    if (cudaGetSymbolAddress(&q, g_seq_status) != cudaSuccess) return nullptr;
+    p = static_cast<int*>(q);
+    __atomic_store_n(&at[dev], p, __ATOMIC_RELEASE);
+  }
+  return p;
+}
+
+static recis_status status_missing() {
+  set_error("the sequence operators' status word is not reachable (no usable sm_100 device?)");
+  return RECIS_ERR_NO_DEVICE;
+}
+
+}  // namespace recis
+
+using namespace recis;
+
+extern "C" recis_status recis_sequence_status_sync(recis_stream_t stream) {
+  int* st = sequence_status();
+  if (!st) return status_missing();
+  cudaStream_t s = (cudaStream_t)stream;
+  int h = 0;
+  cudaError_t e = cudaMemcpyAsync(&h, st, sizeof(int), cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  if (e != cudaSuccess) return cuda_fail(e, "status read");
+  if (!h) return RECIS_OK;
+  if ((e = cudaMemsetAsync(st, 0, sizeof(int), s)) != cudaSuccess) return cuda_fail(e, "status clear");
+  if ((e = cudaStreamSynchronize(s)) != cudaSuccess) return cuda_fail(e, "status clear");
+  if (h & kErrTimeout) {
+    set_error("a bounded device-side wait gave up");
+    return RECIS_ERR_TIMEOUT;
+  }
+  set_error(h & kErrBadOffsets ? "bag offsets decrease, leave their array or pass the given bound"
+                               : "a token is neither padding nor a row of the weight");
+  return RECIS_ERR_INVALID_ARG;
+}
+
+extern "C" recis_status recis_embed_lookup(const void* weight, int32_t weight_type, int64_t V, int32_t D,
+                                           const int64_t* tokens, int64_t N, double scale, int64_t padding, void* out,
+                                           int32_t out_type, int64_t out_stride, recis_stream_t stream) {
+  if (!float_type(weight_type) || !float_type(out_type) || V < 1 || V > INT32_MAX || D < 1 || D > 65536 || N < 0 ||
+      N > INT32_MAX || !weight || out_stride < D || (N > 0 && (!tokens || !out))) {
+    set_error("embed_lookup: bad arguments");
+    return RECIS_ERR_INVALID_ARG;
+  }
+  if (misaligned(weight, type_bytes(weight_type)) || misaligned(out, type_bytes(out_type)) || misaligned(tokens, 8)) {
+    set_error("embed_lookup: misaligned array");
+    return RECIS_ERR_INVALID_ARG;
+  }
+  if (N == 0) return RECIS_OK;
+  int* st = sequence_status();
+  if (!st) return status_missing();
+  LookupParams p = {weight, tokens, out, V, N, out_stride, padding, D, 0, 0, (float)scale, st};
+  // 16-byte accesses where every row of both arrays allows them
+  const bool vec = D % 8 == 0 && rows_aligned16(weight, D, weight_type) && rows_aligned16(out, out_stride, out_type);
+  const cudaError_t e = with_type(weight_type, [&](auto w) {
+    return with_type(out_type, [&](auto o) {
+      using TW = decltype(w);
+      using TO = decltype(o);
+      return vec ? lookup_launch<TW, TO, 8>(p, (cudaStream_t)stream) : lookup_launch<TW, TO, 1>(p, (cudaStream_t)stream);
+    });
+  });
+  return e == cudaSuccess ? RECIS_OK : cuda_fail(e, "embed_lookup launch");
+}
+
+static bool grad_sizes_ok(int64_t N, int64_t V, int32_t D) {
+  return V >= 1 && V < INT32_MAX && D >= 1 && D <= 65536 && N >= 0 && N < ((int64_t)1 << 30);
+}
+
+extern "C" recis_status recis_embed_grad_workspace(int64_t N, int64_t V, int32_t D, int64_t* bytes_out) {
+  if (!bytes_out || !grad_sizes_ok(N, V, D)) {
+    set_error("embed_grad_workspace: bad arguments");
+    return RECIS_ERR_INVALID_ARG;
+  }
+  *bytes_out = grad_plan(N, V, D).bytes;
+  return RECIS_OK;
+}
+
+extern "C" recis_status recis_embed_grad(const int64_t* tokens, int64_t N, const void* grad_out, int32_t grad_type,
+                                         int64_t grad_stride, int64_t V, int32_t D, double scale, int64_t padding,
+                                         int32_t accumulate, void* grad_weight, int32_t weight_type, void* workspace,
+                                         int64_t workspace_bytes, recis_stream_t stream) {
+  if (!float_type(grad_type) || !float_type(weight_type) || !grad_sizes_ok(N, V, D) || !grad_weight ||
+      grad_stride < D || (accumulate != 0 && accumulate != 1) || (N > 0 && (!tokens || !grad_out))) {
+    set_error("embed_grad: bad arguments");
+    return RECIS_ERR_INVALID_ARG;
+  }
+  if (misaligned(grad_out, type_bytes(grad_type)) || misaligned(grad_weight, type_bytes(weight_type)) ||
+      misaligned(tokens, 8) || misaligned(workspace, 256)) {
+    set_error("embed_grad: misaligned array");
+    return RECIS_ERR_INVALID_ARG;
+  }
+  const int64_t need = grad_plan(N, V, D).bytes;
+  if (need > 0 && (!workspace || workspace_bytes < need)) {
+    set_error("embed_grad: workspace too small");
+    return RECIS_ERR_INVALID_ARG;
+  }
+  int* st = sequence_status();
+  if (!st) return status_missing();
+  SumParams p = {};
+  p.tok = tokens;
+  p.g = grad_out;
+  p.dw = grad_weight;
+  p.N = N;
+  p.V = V;
+  p.g_stride = grad_stride;
+  p.padding = padding;
+  p.D = D;
+  p.accumulate = accumulate;
+  p.scale = (float)scale;
+  p.status = st;
+  const bool vec =
+      D % 8 == 0 && rows_aligned16(grad_out, grad_stride, grad_type) && rows_aligned16(grad_weight, D, weight_type);
+  char* ws = static_cast<char*>(workspace);
+  const cudaError_t e = with_type(grad_type, [&](auto g) {
+    return with_type(weight_type, [&](auto o) {
+      using TG = decltype(g);
+      using TO = decltype(o);
+      return vec ? grad_launch<TG, TO, 8>(p, tokens, ws, (cudaStream_t)stream)
+                 : grad_launch<TG, TO, 1>(p, tokens, ws, (cudaStream_t)stream);
+    });
+  });
+  return e == cudaSuccess ? RECIS_OK : cuda_fail(e, "embed_grad launch");
+}

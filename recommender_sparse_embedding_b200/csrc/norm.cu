@@ -1,0 +1,494 @@
+// norm.cu -- layer norm of rows, forward and backward.
+//
+//   mu = mean(x), r = 1 / sqrt(mean((x - mu)^2) + eps), xh = (x - mu) r,
+//   y = xh w + b;
+//   with g = dy w:  dx = r (g - mean(g) - xh mean(g xh)),
+//                   dw = sum_rows dy xh,  db = sum_rows dy.
+//
+// Both passes are bound by memory: every element is read once and written
+// once.  A group of threads holds a whole row in registers, so the variance
+// is taken from the centred values (no cancellation) without reading the row
+// again.  The backward's blocks are persistent: a thread keeps its columns
+// through all its rows, adds dw and db in registers, and a second kernel joins
+// the blocks' sums in block order in fp64 (no float atomic).
+#include <algorithm>
+
+#include "seqops.cuh"
+
+namespace recis {
+
+namespace {
+
+constexpr int kMaxRowThreads = 512;   // a block of the kernels that hold a row
+constexpr int kWideThreads = 1024;    // a block of the kernels that read a row again
+
+struct NormParams {
+  const void* x;
+  const void* w;
+  const void* b;
+  const void* gy;
+  void* y;          // forward: y; backward: grad_x (or NULL)
+  float* mean;      // forward: written (or NULL); backward: read
+  float* rstd;
+  float* partial;   // backward: [blocks][2][D] (or NULL)
+  int64_t M, x_stride, gy_stride, y_stride;
+  int D, units, tpr;  // tpr: threads a row
+  int w_type;
+  float eps;
+};
+
+__device__ __forceinline__ float param_at(const void* p, int type, int i) {
+  if (type == RECIS_F32) return __ldg(static_cast<const float*>(p) + i);
+  if (type == RECIS_BF16) return to_f32(static_cast<const __nv_bfloat16*>(p)[i]);
+  return to_f32(static_cast<const __half*>(p)[i]);
+}
+
+// Sum of v over the tpr threads of the caller's row; every thread gets it.
+// tpr <= 32: shuffles within the warp; more: tpr is a multiple of 32, and every
+// thread of the block calls (`s` alternates between calls, so one barrier a
+// call suffices).
+template <int K>
+__device__ __forceinline__ void row_sum(float (&v)[K], int tpr, float (*s)[32]) {
+  const int top = tpr < 32 ? tpr : 32;
+  for (int off = top >> 1; off > 0; off >>= 1)
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], off);
+  if (tpr > 32) {
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    if (lane == 0)
+#pragma unroll
+      for (int k = 0; k < K; ++k) s[k][w] = v[k];
+    __syncthreads();
+    const int nw = tpr >> 5, w0 = w / nw * nw;  // the row's warps
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      float t = lane < nw ? s[k][w0 + lane] : 0.f;
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
+      v[k] = t;
+    }
+  }
+}
+
+// UPT vectors of VEC columns a thread: columns (lane + k * tpr) * VEC.
+template <typename TX, typename TY, int VEC, int UPT>
+__global__ void __launch_bounds__(kMaxRowThreads) norm_kernel(const __grid_constant__ NormParams p) {
+  __shared__ float s_red[2][1][32];
+  const int rows = blockDim.x / p.tpr;  // rows a block takes at once
+  const int lane = threadIdx.x % p.tpr;
+  const int64_t i = (int64_t)blockIdx.x * rows + threadIdx.x / p.tpr;
+  const bool live = i < p.M;  // a warp may hold several rows: all its lanes take part in the sums
+  const TX* x = static_cast<const TX*>(p.x) + i * p.x_stride;
+  float v[UPT][VEC];
+  float s[1] = {0.f};
+  {
+    RawVec<TX, VEC> raw[UPT];
+#pragma unroll
+    for (int k = 0; k < UPT; ++k) {
+      const int c = lane + k * p.tpr;
+      if (live && c < p.units) raw[k].load(x + (int64_t)c * VEC);
+    }
+#pragma unroll
+    for (int k = 0; k < UPT; ++k) {
+      const int c = lane + k * p.tpr;
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) v[k][j] = 0.f;
+      if (live && c < p.units) raw[k].unpack(v[k]);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) s[0] += v[k][j];
+    }
+  }
+  const float inv = 1.0f / (float)p.D;
+  row_sum<1>(s, p.tpr, s_red[0]);
+  const float mu = s[0] * inv;
+  s[0] = 0.f;
+#pragma unroll
+  for (int k = 0; k < UPT; ++k) {
+    if (lane + k * p.tpr >= p.units) break;
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      v[k][j] -= mu;
+      s[0] = fmaf(v[k][j], v[k][j], s[0]);
+    }
+  }
+  row_sum<1>(s, p.tpr, s_red[1]);
+  const float r = 1.0f / sqrtf(fmaf(s[0], inv, p.eps));
+  if (!live) return;
+  if (lane == 0) {
+    if (p.mean) p.mean[i] = mu;
+    if (p.rstd) p.rstd[i] = r;
+  }
+  TY* y = static_cast<TY*>(p.y) + i * p.y_stride;
+#pragma unroll
+  for (int k = 0; k < UPT; ++k) {
+    const int c = lane + k * p.tpr;
+    if (c >= p.units) break;
+    float f[VEC];
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      const float w = p.w ? param_at(p.w, p.w_type, c * VEC + j) : 1.0f;
+      const float b = p.b ? param_at(p.b, p.w_type, c * VEC + j) : 0.0f;
+      f[j] = fmaf(v[k][j] * r, w, b);
+    }
+    store_vec(y + (int64_t)c * VEC, f);
+  }
+}
+
+// Rows wider than the registers of a block hold: three reads of the row.
+template <typename TX, typename TY>
+__global__ void __launch_bounds__(kWideThreads) norm_wide_kernel(const __grid_constant__ NormParams p) {
+  __shared__ float s_red[2][1][32];
+  const TX* x = static_cast<const TX*>(p.x) + (int64_t)blockIdx.x * p.x_stride;
+  TY* y = static_cast<TY*>(p.y) + (int64_t)blockIdx.x * p.y_stride;
+  float s[1] = {0.f};
+  for (int c = threadIdx.x; c < p.D; c += kWideThreads) s[0] += to_f32(x[c]);
+  row_sum<1>(s, kWideThreads, s_red[0]);
+  const float mu = s[0] / (float)p.D;
+  s[0] = 0.f;
+  for (int c = threadIdx.x; c < p.D; c += kWideThreads) {
+    const float d = to_f32(x[c]) - mu;
+    s[0] = fmaf(d, d, s[0]);
+  }
+  row_sum<1>(s, kWideThreads, s_red[1]);
+  const float r = 1.0f / sqrtf(s[0] / (float)p.D + p.eps);
+  if (threadIdx.x == 0) {
+    if (p.mean) p.mean[blockIdx.x] = mu;
+    if (p.rstd) p.rstd[blockIdx.x] = r;
+  }
+  for (int c = threadIdx.x; c < p.D; c += kWideThreads) {
+    const float w = p.w ? param_at(p.w, p.w_type, c) : 1.0f, b = p.b ? param_at(p.b, p.w_type, c) : 0.0f;
+    y[c] = from_f32<TY>(fmaf((to_f32(x[c]) - mu) * r, w, b));
+  }
+}
+
+template <typename TX, typename TY, int VEC, int UPT>
+__global__ void __launch_bounds__(kMaxRowThreads) norm_back_kernel(const __grid_constant__ NormParams p) {
+  __shared__ float s_red[2][2][32];
+  extern __shared__ float s_part[];  // [2][tpr * UPT * VEC] sums of the block's rows at once
+  const int rows = blockDim.x / p.tpr, row = threadIdx.x / p.tpr, lane = threadIdx.x % p.tpr;
+  float w[UPT][VEC], dw[UPT][VEC], db[UPT][VEC];
+#pragma unroll
+  for (int k = 0; k < UPT; ++k) {
+    const int c = lane + k * p.tpr;
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      w[k][j] = c < p.units ? (p.w ? param_at(p.w, p.w_type, c * VEC + j) : 1.0f) : 0.f;
+      dw[k][j] = db[k][j] = 0.f;
+    }
+  }
+  const float inv = 1.0f / (float)p.D;
+  const int64_t step = (int64_t)gridDim.x * rows;
+  int flip = 0;
+  // every thread of the block goes through the same number of steps
+  for (int64_t i0 = (int64_t)blockIdx.x * rows; i0 < p.M; i0 += step, flip ^= 1) {
+    const int64_t i = i0 + row;
+    const bool live = i < p.M;
+    RawVec<TX, VEC> rx[UPT];
+    RawVec<TY, VEC> rg[UPT];
+#pragma unroll
+    for (int k = 0; k < UPT; ++k) {
+      const int c = lane + k * p.tpr;
+      if (live && c < p.units) {
+        rx[k].load(static_cast<const TX*>(p.x) + i * p.x_stride + (int64_t)c * VEC);
+        rg[k].load(static_cast<const TY*>(p.gy) + i * p.gy_stride + (int64_t)c * VEC);
+      }
+    }
+    const float mu = live ? __ldg(p.mean + i) : 0.f, r = live ? __ldg(p.rstd + i) : 0.f;
+    float xh[UPT][VEC], g[UPT][VEC];
+    float s[2] = {0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < UPT; ++k) {
+      const int c = lane + k * p.tpr;
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) xh[k][j] = g[k][j] = 0.f;
+      if (live && c < p.units) {
+        rx[k].unpack(xh[k]);
+        rg[k].unpack(g[k]);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+          xh[k][j] = (xh[k][j] - mu) * r;
+          db[k][j] += g[k][j];
+          dw[k][j] = fmaf(g[k][j], xh[k][j], dw[k][j]);
+          g[k][j] *= w[k][j];
+          s[0] += g[k][j];
+          s[1] = fmaf(g[k][j], xh[k][j], s[1]);
+        }
+      }
+    }
+    if (!p.y) continue;
+    row_sum<2>(s, p.tpr, s_red[flip]);
+    const float m0 = s[0] * inv, m1 = s[1] * inv;
+    if (live) {
+      TX* dx = static_cast<TX*>(p.y) + i * p.y_stride;
+#pragma unroll
+      for (int k = 0; k < UPT; ++k) {
+        const int c = lane + k * p.tpr;
+        if (c >= p.units) break;
+        float f[VEC];
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) f[j] = r * (g[k][j] - m0 - xh[k][j] * m1);
+        store_vec(dx + (int64_t)c * VEC, f);
+      }
+    }
+  }
+  if (!p.partial) return;
+  // the block's rows, added in row order
+  const int cols = p.tpr * UPT * VEC;
+  for (int q = 0; q < rows; ++q) {
+    if (row == q) {
+#pragma unroll
+      for (int k = 0; k < UPT; ++k)
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+          const int at = (lane + k * p.tpr) * VEC + j;
+          s_part[at] = q ? s_part[at] + dw[k][j] : dw[k][j];
+          s_part[cols + at] = q ? s_part[cols + at] + db[k][j] : db[k][j];
+        }
+    }
+    __syncthreads();
+  }
+  float* out = p.partial + (int64_t)blockIdx.x * 2 * p.D;
+  for (int c = threadIdx.x; c < p.D; c += blockDim.x) {
+    out[c] = s_part[c];
+    out[p.D + c] = s_part[cols + c];
+  }
+}
+
+// Wide rows: a row's sums and its dx from three reads; the block's dw and db
+// live in its partial row in global memory (no other block touches it).
+template <typename TX, typename TY>
+__global__ void __launch_bounds__(kWideThreads) norm_back_wide_kernel(const __grid_constant__ NormParams p) {
+  __shared__ float s_red[2][2][32];
+  float* out = p.partial ? p.partial + (int64_t)blockIdx.x * 2 * p.D : nullptr;
+  if (out)
+    for (int c = threadIdx.x; c < 2 * p.D; c += kWideThreads) out[c] = 0.f;
+  __syncthreads();
+  int flip = 0;
+  for (int64_t i = blockIdx.x; i < p.M; i += gridDim.x, flip ^= 1) {
+    const TX* x = static_cast<const TX*>(p.x) + i * p.x_stride;
+    const TY* gy = static_cast<const TY*>(p.gy) + i * p.gy_stride;
+    const float mu = __ldg(p.mean + i), r = __ldg(p.rstd + i);
+    float s[2] = {0.f, 0.f};
+    for (int c = threadIdx.x; c < p.D; c += kWideThreads) {
+      const float d = to_f32(gy[c]), xh = (to_f32(x[c]) - mu) * r;
+      const float g = d * (p.w ? param_at(p.w, p.w_type, c) : 1.0f);
+      s[0] += g;
+      s[1] = fmaf(g, xh, s[1]);
+      if (out) {  // column c is this thread's in every row
+        out[c] = fmaf(d, xh, out[c]);
+        out[p.D + c] += d;
+      }
+    }
+    if (!p.y) continue;
+    row_sum<2>(s, kWideThreads, s_red[flip]);
+    const float m0 = s[0] / (float)p.D, m1 = s[1] / (float)p.D;
+    TX* dx = static_cast<TX*>(p.y) + i * p.y_stride;
+    for (int c = threadIdx.x; c < p.D; c += kWideThreads) {
+      const float xh = (to_f32(x[c]) - mu) * r;
+      const float g = to_f32(gy[c]) * (p.w ? param_at(p.w, p.w_type, c) : 1.0f);
+      dx[c] = from_f32<TX>(r * (g - m0 - xh * m1));
+    }
+  }
+}
+
+// dw and db from the blocks' sums: 32 columns a block, warp k the k-th part of
+// the blocks in order, fp64.
+__global__ void __launch_bounds__(1024) norm_join_kernel(const float* partial, int blocks, int D, int w_type, void* dw,
+                                                         void* db) {
+  __shared__ double s[32][33];
+  const int lane = threadIdx.x & 31, k = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + lane;  // columns of [dw | db]
+  double t = 0.0;
+  const int per = (blocks + 31) / 32;
+  if (c < 2 * D)
+    for (int q = k * per; q < min((k + 1) * per, blocks); ++q) t += (double)partial[(int64_t)q * 2 * D + c];
+  s[k][lane] = t;
+  __syncthreads();
+  if (k != 0 || c >= 2 * D) return;
+  t = 0.0;
+  for (int q = 0; q < 32; ++q) t += s[q][lane];
+  void* out = c < D ? dw : db;
+  const int at = c < D ? c : c - D;
+  if (!out) return;
+  if (w_type == RECIS_F32) static_cast<float*>(out)[at] = (float)t;
+  else if (w_type == RECIS_BF16) static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn((float)t);
+  else static_cast<__half*>(out)[at] = __float2half_rn((float)t);
+}
+
+// threads a row: a power of two, with at most `upt` vectors a thread (0: the
+// row does not fit a block)
+int row_threads(int units, int upt) {
+  int t = 1;
+  while (t * upt < units && t <= kMaxRowThreads) t *= 2;
+  return t <= kMaxRowThreads ? t : 0;
+}
+
+template <typename TX, typename TY, int VEC>
+cudaError_t norm_launch(NormParams p, cudaStream_t s) {
+  p.units = p.D / VEC;
+  LaunchScope ls("layer_norm", s);
+  // a warp's width of threads first, then up to four vectors a thread, then more threads
+  int upt = p.units <= 32 ? 1 : p.units <= 64 ? 2 : 4;
+  p.tpr = row_threads(p.units, upt);
+  if (!p.tpr) {
+    norm_wide_kernel<TX, TY><<<(unsigned)p.M, kWideThreads, 0, s>>>(p);
+    return cudaGetLastError();
+  }
+  const int block = std::max(p.tpr, 128), rows = block / p.tpr;
+  const unsigned grid = (unsigned)((p.M + rows - 1) / rows);
+  if (upt == 1) norm_kernel<TX, TY, VEC, 1><<<grid, block, 0, s>>>(p);
+  else if (upt == 2) norm_kernel<TX, TY, VEC, 2><<<grid, block, 0, s>>>(p);
+  else norm_kernel<TX, TY, VEC, 4><<<grid, block, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+// blocks of the backward (its partial sums' rows): the same for every type
+int back_blocks(int64_t M) { return (int)std::min<int64_t>(M, kSMs * 4); }
+
+template <typename TX, typename TY, int VEC>
+cudaError_t back_launch(NormParams p, cudaStream_t s, int* blocks_out) {
+  p.units = p.D / VEC;
+  LaunchScope ls("layer_norm_backward", s);
+  const int upt = p.units <= 32 ? 1 : 2;
+  p.tpr = row_threads(p.units, upt);
+  int blocks = back_blocks(p.M);
+  if (!p.tpr) {
+    *blocks_out = blocks;
+    norm_back_wide_kernel<TX, TY><<<blocks, kWideThreads, 0, s>>>(p);
+    return cudaGetLastError();
+  }
+  const int block = std::max(p.tpr, 256), rows = block / p.tpr;
+  blocks = (int)std::min<int64_t>(blocks, (p.M + rows - 1) / rows);
+  *blocks_out = blocks;
+  const size_t smem = p.partial ? (size_t)2 * p.tpr * upt * VEC * 4 : 0;
+  auto go = [&](auto kernel) {
+    if (smem > 48 * 1024) {
+      const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      if (e != cudaSuccess) return e;
+    }
+    kernel<<<blocks, block, smem, s>>>(p);
+    return cudaGetLastError();
+  };
+  return upt == 1 ? go(norm_back_kernel<TX, TY, VEC, 1>) : go(norm_back_kernel<TX, TY, VEC, 2>);
+}
+
+bool norm_sizes_ok(int64_t M, int32_t D) { return M >= 0 && M <= INT32_MAX && D >= 1 && D <= 65536; }
+
+}  // namespace
+}  // namespace recis
+
+using namespace recis;
+
+extern "C" recis_status recis_layer_norm(const void* x, int32_t x_type, int64_t x_stride, int64_t M, int32_t D,
+                                         const void* weight, const void* bias, int32_t w_type, double eps, void* y,
+                                         int32_t y_type, int64_t y_stride, float* mean, float* rstd,
+                                         recis_stream_t stream) {
+  if (!float_type(x_type) || !float_type(y_type) || !float_type(w_type) || !norm_sizes_ok(M, D) || x_stride < D ||
+      y_stride < D || !(eps >= 0.0) || (M > 0 && (!x || !y))) {
+    set_error("layer_norm: bad arguments");
+    return RECIS_ERR_INVALID_ARG;
+  }
+  if (misaligned(x, type_bytes(x_type)) || misaligned(y, type_bytes(y_type)) ||
+      misaligned(weight, type_bytes(w_type)) || misaligned(bias, type_bytes(w_type)) || misaligned(mean, 4) ||
+      misaligned(rstd, 4)) {
+    set_error("layer_norm: misaligned array");
+    return RECIS_ERR_INVALID_ARG;
+  }
+  if (M == 0) return RECIS_OK;
+  NormParams p = {};
+  p.x = x;
+  p.w = weight;
+  p.b = bias;
+  p.y = y;
+  p.mean = mean;
+  p.rstd = rstd;
+  p.M = M;
+  p.x_stride = x_stride;
+  p.y_stride = y_stride;
+  p.D = D;
+  p.w_type = w_type;
+  p.eps = (float)eps;
+  const bool vec = D % 8 == 0 && rows_aligned16(x, x_stride, x_type) && rows_aligned16(y, y_stride, y_type);
+  const cudaError_t e = with_type(x_type, [&](auto a) {
+    return with_type(y_type, [&](auto b) {
+      using TX = decltype(a);
+      using TY = decltype(b);
+      return vec ? norm_launch<TX, TY, 8>(p, (cudaStream_t)stream) : norm_launch<TX, TY, 1>(p, (cudaStream_t)stream);
+    });
+  });
+  return e == cudaSuccess ? RECIS_OK : cuda_fail(e, "layer_norm launch");
+}
+
+extern "C" recis_status recis_layer_norm_backward_workspace(int64_t M, int32_t D, int64_t* bytes_out) {
+  if (!bytes_out || !norm_sizes_ok(M, D)) {
+    set_error("layer_norm_backward_workspace: bad arguments");
+    return RECIS_ERR_INVALID_ARG;
+  }
+  *bytes_out = (int64_t)back_blocks(M) * 2 * D * 4;
+  return RECIS_OK;
+}
+
+extern "C" recis_status recis_layer_norm_backward(const void* grad_y, int32_t y_type, int64_t grad_y_stride,
+                                                  const void* x, int32_t x_type, int64_t x_stride, int64_t M,
+                                                  int32_t D, const void* weight, int32_t w_type, const float* mean,
+                                                  const float* rstd, void* grad_x, int64_t grad_x_stride,
+                                                  void* grad_weight, void* grad_bias, void* workspace,
+                                                  int64_t workspace_bytes, recis_stream_t stream) {
+  if (!float_type(x_type) || !float_type(y_type) || !float_type(w_type) || !norm_sizes_ok(M, D) || x_stride < D ||
+      grad_y_stride < D || (grad_x && grad_x_stride < D) || (M > 0 && (!x || !grad_y || !mean || !rstd))) {
+    set_error("layer_norm_backward: bad arguments");
+    return RECIS_ERR_INVALID_ARG;
+  }
+  if (misaligned(x, type_bytes(x_type)) || misaligned(grad_y, type_bytes(y_type)) ||
+      misaligned(weight, type_bytes(w_type)) || misaligned(grad_x, type_bytes(x_type)) ||
+      misaligned(grad_weight, type_bytes(w_type)) || misaligned(grad_bias, type_bytes(w_type)) || misaligned(mean, 4) ||
+      misaligned(rstd, 4) || misaligned(workspace, 256)) {
+    set_error("layer_norm_backward: misaligned array");
+    return RECIS_ERR_INVALID_ARG;
+  }
+  const bool sums = grad_weight || grad_bias;
+  cudaStream_t s = (cudaStream_t)stream;
+  if (M == 0) {
+    cudaError_t e = cudaSuccess;
+    if (grad_weight) e = cudaMemsetAsync(grad_weight, 0, (size_t)D * type_bytes(w_type), s);
+    if (e == cudaSuccess && grad_bias) e = cudaMemsetAsync(grad_bias, 0, (size_t)D * type_bytes(w_type), s);
+    return e == cudaSuccess ? RECIS_OK : cuda_fail(e, "layer_norm_backward memset");
+  }
+  if (!sums && !grad_x) return RECIS_OK;
+  if (sums && (!workspace || workspace_bytes < (int64_t)back_blocks(M) * 2 * D * 4)) {
+    set_error("layer_norm_backward: workspace too small");
+    return RECIS_ERR_INVALID_ARG;
+  }
+  NormParams p = {};
+  p.x = x;
+  p.w = weight;
+  p.gy = grad_y;
+  p.y = grad_x;
+  p.mean = const_cast<float*>(mean);
+  p.rstd = const_cast<float*>(rstd);
+  p.partial = sums ? static_cast<float*>(workspace) : nullptr;
+  p.M = M;
+  p.x_stride = x_stride;
+  p.gy_stride = grad_y_stride;
+  p.y_stride = grad_x_stride;
+  p.D = D;
+  p.w_type = w_type;
+  const bool vec = D % 8 == 0 && rows_aligned16(x, x_stride, x_type) && rows_aligned16(grad_y, grad_y_stride, y_type) &&
+                   (!grad_x || rows_aligned16(grad_x, grad_x_stride, x_type));
+  int blocks = 0;
+  cudaError_t e = with_type(x_type, [&](auto a) {
+    return with_type(y_type, [&](auto b) {
+      using TX = decltype(a);
+      using TY = decltype(b);
+      return vec ? back_launch<TX, TY, 8>(p, s, &blocks) : back_launch<TX, TY, 1>(p, s, &blocks);
+    });
+  });
+  if (e != cudaSuccess) return cuda_fail(e, "layer_norm_backward launch");
+  if (sums) {
+    LaunchScope ls("layer_norm_join", s);
+    norm_join_kernel<<<(unsigned)((2 * D + 31) / 32), 1024, 0, s>>>(p.partial, blocks, D, w_type, grad_weight,
+                                                                  grad_bias);
+    if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "layer_norm_join launch");
+  }
+  return RECIS_OK;
+}

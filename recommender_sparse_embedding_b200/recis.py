@@ -36,6 +36,9 @@ EXPORTS = (
     "recis_debug_set", "recis_plan_tables", "recis_table_reserve", "recis_table_save",
     "recis_table_load", "recis_table_evict", "recis_table_clock", "recis_batch_dedup",
     "recis_partition_keys", "recis_pool_rows", "recis_reduce_grad",
+    "recis_sequence_status_sync", "recis_embed_lookup", "recis_embed_grad_workspace",
+    "recis_embed_grad", "recis_layer_norm", "recis_layer_norm_backward_workspace",
+    "recis_layer_norm_backward", "recis_attend_workspace", "recis_attend", "recis_attend_backward",
 )
 DEBUG_SPIN_LIMIT, DEBUG_MAP_LIMIT = 1, 2
 
@@ -89,6 +92,7 @@ _lib = None
 _vp = ctypes.c_void_p
 _i64 = ctypes.c_int64
 _i32 = ctypes.c_int32
+_f64 = ctypes.c_double
 
 
 def load(path: str = LIB_PATH):
@@ -131,6 +135,19 @@ def load(path: str = LIB_PATH):
             "recis_partition_keys": [_vp, _vp, _i64, _i32, ctypes.c_uint64, _vp, _vp, _vp, _vp],
             "recis_pool_rows": [_vp, _vp, _vp, _vp, _i32, _i64, _i32, _i32, _vp, _vp],
             "recis_reduce_grad": [_vp, _vp, _i32, _i64, _i32, _i32, _vp, _vp, _vp, _vp, _vp],
+            "recis_sequence_status_sync": [_vp],
+            "recis_embed_lookup": [_vp, _i32, _i64, _i32, _vp, _i64, _f64, _i64, _vp, _i32, _i64, _vp],
+            "recis_embed_grad_workspace": [_i64, _i64, _i32, _vp],
+            "recis_embed_grad": [_vp, _i64, _vp, _i32, _i64, _i64, _i32, _f64, _i64, _i32, _vp, _i32, _vp, _i64,
+                                 _vp],
+            "recis_layer_norm": [_vp, _i32, _i64, _i64, _i32, _vp, _vp, _i32, _f64, _vp, _i32, _i64, _vp, _vp,
+                                 _vp],
+            "recis_layer_norm_backward_workspace": [_i64, _i32, _vp],
+            "recis_layer_norm_backward": [_vp, _i32, _i64, _vp, _i32, _i64, _i64, _i32, _vp, _i32, _vp, _vp, _vp,
+                                          _i64, _vp, _vp, _vp, _i64, _vp],
+            "recis_attend_workspace": [_vp, _i32, _vp],
+            "recis_attend": [_vp, _vp, _i64, _vp],
+            "recis_attend_backward": [_vp, _vp, _i64, _vp],
         }
         for name, args in sig.items():
             fn = getattr(L, name)

@@ -1,0 +1,521 @@
+"""Sequence operators on the GPU against their plain 64-bit forms
+(sequence_ref.py, where the tolerances are derived): dense embedding lookup and
+gradient, layer norm, attention over the keys of each bag, and the attention
+pooling of a table's bags built from them."""
+import math
+
+import pytest
+import torch
+
+import sequence_ref as S
+
+pytestmark = pytest.mark.gpu
+BF16, F16, F32 = torch.bfloat16, torch.float16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def R():
+    import recommender_sparse_embedding_b200 as R
+    from recommender_sparse_embedding_b200 import build
+    build.build()
+    assert torch.cuda.is_available()
+    R.load()
+    R.sequence_status_sync()
+    return R
+
+
+def _gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def _randn(shape, dtype, g, mul=1.0):
+    return (torch.randn(shape, device="cuda", generator=g) * mul).to(dtype)
+
+
+# ------------------------------------------------------------------ dense embedding
+@pytest.mark.parametrize("wt,ot", [(F32, F32), (F32, BF16), (BF16, BF16), (F16, F32), (BF16, F16)])
+@pytest.mark.parametrize("N,V,D", [(0, 5, 8), (1, 1, 1), (3, 7, 33), (64, 1000, 1024), (4097, 300, 40),
+                                   (100000, 5000, 64), (30, 11, 2056)])
+def test_embed_lookup(R, wt, ot, N, V, D):
+    g = _gen(N + D)
+    w = _randn((V, D), wt, g)
+    t = torch.randint(-1, V, (N,), device="cuda", generator=g)
+    scale = 0.375 if N % 2 else math.sqrt(D)
+    out = R.embed_lookup(w, t, scale=scale, out_dtype=ot)
+    R.sequence_status_sync()
+    want = S.lookup(w, t, scale, -1)
+    # the factor and the product round to fp32, the result to its type
+    S.close(out, want, (S.half_step(ot) * 1.001 + 2 * S.F32) * want.abs() + (2.0 ** -24 if ot == F16 else 0), "lookup")
+
+
+def test_embed_lookup_padding_and_bad_tokens(R):
+    g = _gen(3)
+    w = _randn((10, 24), F32, g)
+    w[4] = math.nan
+    t = torch.tensor([[4, 0], [9, 4]], device="cuda")
+    out = R.embed_lookup(w, t, padding=4)  # a padding token reads zeros, whatever its row holds
+    R.sequence_status_sync()
+    assert torch.equal(out[0, 0], torch.zeros(24, device="cuda")) and torch.equal(out[1, 0], w[9])
+    out = R.embed_lookup(w, torch.tensor([10, 1, -7, 2**40], device="cuda"))
+    with pytest.raises(R.RecisError):
+        R.sequence_status_sync()
+    R.sequence_status_sync()  # cleared
+    assert torch.equal(out[1], w[1]) and not out[[0, 2, 3]].any()
+
+
+def test_embed_lookup_into_strided_rows_and_misaligned_weight(R):
+    g = _gen(4)
+    wide = torch.zeros((50, 96), device="cuda", dtype=BF16)
+    w = _randn((20 * 16 + 1,), BF16, g)[1:].view(20, 16)  # rows off the 16-byte boundary
+    t = torch.randint(0, 20, (50,), device="cuda", generator=g)
+    R.embed_lookup(w, t, out=wide[:, 40:56])
+    assert torch.equal(wide[:, 40:56], w[t])
+    assert not wide[:, :40].any() and not wide[:, 56:].any()
+
+
+def _tokens(kind, N, V, g):
+    if kind == "one":
+        return torch.full((N,), V - 1, device="cuda")
+    if kind == "padding":
+        return torch.full((N,), -1, device="cuda")
+    if kind == "hot":  # half the positions hold one token, the rest spread, some padding
+        t = torch.randint(-1, V, (N,), device="cuda", generator=g)
+        return torch.where(torch.rand(N, device="cuda", generator=g) < 0.5, V // 2, t)
+    return torch.randint(0, V, (N,), device="cuda", generator=g)
+
+
+@pytest.mark.parametrize("gt,ot", [(F32, F32), (BF16, F32), (F16, F16), (F32, BF16)])
+@pytest.mark.parametrize("kind,N,V,D", [
+    ("even", 0, 5, 8), ("even", 1, 1, 1), ("hot", 1024, 40, 72), ("hot", 1025, 40, 72), ("one", 1000, 3, 16),
+    ("one", 5000, 70000, 16), ("even", 20011, 31, 33), ("hot", 70000, 1 << 17, 64), ("padding", 3000, 9, 8),
+    ("even", 4096, 1 << 21, 8), ("hot", 9999, 1000, 520), ("even", 300, 7, 300), ("hot", 700001, 3000, 8)])
+def test_embed_grad(R, gt, ot, kind, N, V, D):
+    g = _gen(N + V + D)
+    t = _tokens(kind, N, V, g)
+    grad = _randn((N, D), gt, g)
+    scale = 1.5
+    out = R.embed_grad(t, grad, V, scale=scale, dtype=ot)
+    again = R.embed_grad(t, grad, V, scale=scale, dtype=ot)
+    R.sequence_status_sync()
+    assert torch.equal(out, again)  # the order of the sums does not depend on scheduling
+    want, mag = S.embed_grad(t, grad, V, scale, -1)
+    # at most 128 terms a thread in fp32, then fp64; the scaled sum rounds to fp32 and to the type
+    S.close(out, want, 132 * S.F32 * mag + S.half_step(ot) * 1.01 * want.abs() + (2.0 ** -24 if ot == F16 else 0), "grad")
+
+
+@pytest.mark.parametrize("N", [500, 6000])
+@pytest.mark.parametrize("dt", [F32, BF16])
+def test_embed_grad_accumulates(R, N, dt):
+    g = _gen(N)
+    V, D = 3000, 48
+    t = _tokens("hot", N, V, g)
+    t[:5] = torch.tensor([V, -9, 2**33, -1, 0])  # three of them out of range
+    grad = _randn((N, 2 * D), F32, g)[:, D:]      # rows of a wider tensor
+    old = _randn((V, D), dt, g)
+    out = old.clone()
+    res = R.embed_grad(t, grad, V, out=out, accumulate=True)
+    with pytest.raises(R.RecisError):
+        R.sequence_status_sync()
+    assert res is out
+    want, mag = S.embed_grad(t, grad, V, 1.0, -1)
+    untouched = mag.sum(1) == 0
+    assert torch.equal(out[untouched], old[untouched])
+    want = want + old.double()
+    S.close(out, want, 132 * S.F32 * (mag + old.double().abs()) + S.half_step(dt) * 1.01 * want.abs(), "accumulated")
+
+
+# ------------------------------------------------------------------ layer norm
+NORM_SIZES = [(1, 1), (5, 7), (64, 256), (1000, 8), (257, 40), (33, 128), (300, 1001), (70, 4096), (9, 8192),
+              (5, 16384), (3, 5003), (4, 40000), (20000, 16), (2, 512), (40, 520)]
+
+
+@pytest.mark.parametrize("xt,yt,wt", [(F32, F32, F32), (F32, BF16, F32), (BF16, BF16, BF16), (F16, F16, F32),
+                                      (BF16, F32, F16)])
+@pytest.mark.parametrize("M,D", NORM_SIZES)
+def test_layer_norm(R, M, D, xt, yt, wt):
+    g = _gen(M * 7 + D)
+    x = _randn((M, D), xt, g, 2.0) + 0.5
+    x = x.to(xt)
+    w, b = (_randn((D,), wt, g) + 1).to(wt), _randn((D,), wt, g)
+    gy = _randn((M, D), yt, g)
+    y, mean, rstd = R.layer_norm(x, w, b, eps=1e-5, out_dtype=yt)
+    dx, dw, db = R.layer_norm_backward(gy, x, mean, rstd, w, b)
+    ref = S.Norm(x, w, b, 1e-5)
+    S.close(mean, ref.mean, ref.mean_err + S.F32 * ref.mean.abs(), "mean")
+    S.close(rstd, ref.rstd, ref.rstd_err, "rstd")
+    tiny = 2.0 ** -24
+    S.close(y, ref.y, ref.y_err * 1.01 + S.half_step(yt) * 1.01 * ref.y.abs() + (tiny if yt == F16 else 0), "y")
+    # rows a thread adds in fp32: those of one block, then fp64
+    n_rows = M // 100 + 64
+    (rx, ex), (rw, ew), (rb, eb) = ref.back(gy, n_rows)
+    S.close(dx, rx, ex * 1.01 + S.half_step(xt) * 1.01 * rx.abs() + (tiny if xt == F16 else 1e-37), "grad_x")
+    S.close(dw, rw, ew * 1.01 + S.half_step(wt) * 1.01 * rw.abs() + tiny * (wt == F16), "grad_weight")
+    S.close(db, rb, eb * 1.01 + S.half_step(wt) * 1.01 * rb.abs() + tiny * (wt == F16), "grad_bias")
+    again = R.layer_norm_backward(gy, x, mean, rstd, w, b)
+    assert all(torch.equal(p, q) for p, q in zip((dx, dw, db), again))
+
+
+def test_layer_norm_strided_rows_and_no_parameters(R):
+    g = _gen(8)
+    buf = _randn((40, 3, 48), F32, g)
+    x, gy = buf[:, 1, 8:32], _randn((40, 64), BF16, g)[:, 3:27]  # gy's rows are off the 16-byte boundary
+    y = torch.zeros((40, 32), dtype=BF16, device="cuda")
+    _, mean, rstd = R.layer_norm(x, out=y[:, 8:])
+    ref = S.Norm(x, None, None, 1e-5)
+    S.close(y[:, 8:], ref.y, ref.y_err + S.half_step(BF16) * 1.01 * ref.y.abs(), "y")
+    assert not y[:, :8].any()
+    dx, dw, db = R.layer_norm_backward(gy, x, mean, rstd)
+    assert dw is None and db is None
+    (rx, ex), _, _ = ref.back(gy, 64)
+    S.close(dx, rx, ex * 1.01 + S.F32 * rx.abs(), "grad_x")
+    out = torch.empty((0, 24), device="cuda")
+    assert R.layer_norm(out)[0].shape == (0, 24)
+    w = torch.ones(24, device="cuda")
+    _, dw, db = R.layer_norm_backward(out, out, mean[:0], rstd[:0], w, w)
+    assert not dw.any() and not db.any()
+
+
+def test_layer_norm_large_offset_keeps_the_variance(R):
+    x = (torch.arange(64, device="cuda").float()[None] * 0.25 + 4096.0).repeat(3, 1)  # all exact in fp32
+    y, mean, rstd = R.layer_norm(x)
+    ref = S.Norm(x, None, None, 1e-5)
+    S.close(rstd, ref.rstd, ref.rstd_err, "rstd")
+    S.close(y, ref.y, ref.y_err, "y")
+
+
+# ------------------------------------------------------------------ attention
+def _offsets(lengths):
+    return torch.tensor([0] + list(lengths), device="cuda").cumsum(0)
+
+
+def _bags(seed, B, q, k):
+    g = torch.Generator()
+    g.manual_seed(seed)
+    ql = torch.randint(q[0], q[1] + 1, (B,), generator=g).tolist()
+    kl = torch.randint(k[0], k[1] + 1, (B,), generator=g).tolist()
+    return ql, kl
+
+
+ATTEND = [
+    # B, q lengths, k lengths, Hq, Hkv, D, share of masked keys
+    (1, (1, 1), (1, 1), 1, 1, 8, 0.0),
+    (8, (1, 4), (0, 50), 4, 4, 32, 0.0),
+    (5, (1, 1), (900, 2100), 8, 2, 128, 0.0),
+    (3, (1, 1), (300, 700), 16, 1, 64, 0.2),
+    (7, (0, 16), (0, 300), 2, 2, 64, 0.1),
+    (4, (17, 40), (100, 400), 6, 2, 72, 0.0),
+    (2, (130, 260), (120, 390), 4, 4, 128, 0.05),
+    (2, (128, 128), (128, 256), 2, 1, 64, 0.0),
+    (3, (60, 90), (1, 140), 10, 2, 24, 0.3),
+    (1, (513, 513), (1025, 1025), 3, 1, 96, 0.0),
+    (1, (2, 2), (9000, 9000), 2, 1, 128, 0.0),
+    (2, (3, 9), (60, 70), 130, 2, 16, 0.0),
+    (6, (1, 200), (0, 500), 1, 1, 40, 1.0),
+]
+
+
+def _check_attend(R, seed, case, dtype, train=True, strided=False):
+    B, ql, kl, Hq, Hkv, D, masked = case
+    g = _gen(seed)
+    ql, kl = _bags(seed, B, ql, kl)
+    qo, ko = _offsets(ql), _offsets(kl)
+    Tq, Tk, extra = sum(ql), sum(kl), 3  # rows behind the last bag
+    if strided:  # q from heads-major memory, k and v halves of one row, out inside a wider row
+        q = _randn((Hq, Tq + extra, D), dtype, g).transpose(0, 1)
+        kv = _randn((Tk + extra, 2, Hkv, D), dtype, g)
+        k, v = kv[:, 0], kv[:, 1]
+        out = torch.full((Tq + extra, Hq, D + 8), 7.0, dtype=dtype, device="cuda")[:, :, 8:]
+        dkv = torch.full_like(kv, 7.0)
+        gk, gv = dkv[:, 0], dkv[:, 1]
+    else:
+        q, k, v = (_randn((n + extra, h, D), dtype, g) for n, h in ((Tq, Hq), (Tk, Hkv), (Tk, Hkv)))
+        out = torch.full((Tq + extra, Hq, D), 7.0, dtype=dtype, device="cuda")
+        gk, gv = torch.full_like(k, 7.0), torch.full_like(v, 7.0)
+    gq = torch.full_like(out, 7.0)
+    grad = _randn((Tq + extra, Hq, D), dtype, g)
+    lse = torch.full((Tq + extra, Hq), 7.0, device="cuda")
+    mask = None
+    if masked:
+        mask = torch.rand(Tk + extra, device="cuda", generator=g) >= masked
+    # what no bag and no unmasked key holds must not matter
+    q[Tq:], k[Tk:], v[Tk:], grad[Tq:] = math.nan, math.inf, math.nan, math.inf
+    if mask is not None:
+        k[~mask], v[~mask] = math.nan, -math.inf
+    scale = None if seed % 2 else 0.3
+    mq, mk = max(ql + [1]), max(kl + [0]) + seed % 3
+    R.attend(q, k, v, qo, ko, mq, mk, scale=scale, key_mask=mask, out=out, lse=lse)
+    R.sequence_status_sync()
+    sc = D ** -0.5 if scale is None else scale
+    ref = S.attend(q[:Tq], k[:Tk], v[:Tk], qo, ko, sc, mask, grad[:Tq] if train else None)
+    S.close(out[:Tq], *ref["out"], "out")
+    S.close(lse[:Tq], *ref["lse"], "lse")
+    assert (out[Tq:] == 7.0).all() and (lse[Tq:] == 7.0).all()
+    if not train:
+        return
+    R.attend_backward(grad, q, k, v, out, lse, qo, ko, mq, mk, scale=scale, key_mask=mask, grad_q=gq, grad_k=gk,
+                      grad_v=gv)
+    R.sequence_status_sync()
+    S.close(gq[:Tq], *ref["grad_q"], "grad_q")
+    S.close(gk[:Tk], *ref["grad_k"], "grad_k")
+    S.close(gv[:Tk], *ref["grad_v"], "grad_v")
+    assert (gq[Tq:] == 7.0).all() and (gk[Tk:] == 7.0).all() and (gv[Tk:] == 7.0).all()
+    first = [t.clone() for t in (gq, gk, gv)]
+    R.attend_backward(grad, q, k, v, out, lse, qo, ko, mq, mk, scale=scale, key_mask=mask, grad_q=gq, grad_k=gk,
+                      grad_v=gv)
+    assert all(torch.equal(x[:n], y[:n]) for x, y, n in zip(first, (gq, gk, gv), (Tq, Tk, Tk)))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("i", range(len(ATTEND)))
+def test_attend(R, i, dtype):
+    _check_attend(R, 100 + i, ATTEND[i], dtype)
+
+
+@pytest.mark.parametrize("i", [1, 2, 4, 6, 9])
+def test_attend_strided(R, i):
+    _check_attend(R, 200 + i, ATTEND[i], BF16, strided=True)
+
+
+def test_attend_large_scores(R):
+    """Scores of thousands, of both signs: the running maximum carries them."""
+    g = _gen(5)
+    D = 64
+    q, k, v = (_randn((n, 1, D), F16, g, m) for n, m in ((20, 30.0), (700, 30.0), (700, 1.0)))
+    qo, ko = _offsets([20]), _offsets([700])
+    out, lse = R.attend(q, k, v, qo, ko, 20, 700, scale=1.0)
+    ref = S.attend(q, k, v, qo, ko, 1.0)
+    S.close(out, *ref["out"], "out")
+    S.close(lse, *ref["lse"], "lse")
+
+
+def test_attend_offsets_past_32_bits(R):
+    """A cache whose last rows lie more than 2^32 elements in."""
+    Tk, H, D = 1 << 20, 40, 128
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("needs 60 GB")
+    kv = torch.zeros((2, Tk, H, D), dtype=BF16, device="cuda")
+    g = _gen(6)
+    n = 300
+    kv[:, -n:] = _randn((2, n, H, D), BF16, g)
+    q, grad = _randn((3, H, D), BF16, g), _randn((3, H, D), BF16, g)
+    qo, ko = _offsets([0, 3]), torch.tensor([0, Tk - n, Tk], device="cuda")
+    out, lse = R.attend(q, kv[0], kv[1], qo, ko, 3, Tk)
+    small = S.attend(q, kv[0, -n:], kv[1, -n:], _offsets([3]), _offsets([n]), D ** -0.5, None, grad)
+    S.close(out, *small["out"], "out")
+    gk = torch.empty_like(kv)
+    gq, _, _ = R.attend_backward(grad, q, kv[0], kv[1], out, lse, qo, ko, 3, Tk, grad_k=gk[0], grad_v=gk[1])
+    R.sequence_status_sync()
+    S.close(gq, *small["grad_q"], "grad_q")
+    S.close(gk[0, -n:], *small["grad_k"], "grad_k")
+    S.close(gk[1, -n:], *small["grad_v"], "grad_v")
+    assert not gk[:, : Tk - n].any()  # keys of a bag without queries
+
+
+def test_attend_bad_offsets_are_reported(R):
+    g = _gen(7)
+    q, k, v = (_randn((40, 2, 32), BF16, g) for _ in range(3))
+    good = _offsets([10, 30])
+    for qo, ko, mq, mk in ((_offsets([10, 31]), good, 31, 30), (good, torch.tensor([0, 30, 20], device="cuda"), 30, 30),
+                           (good, good, 29, 30), (good, good, 30, 20), (torch.tensor([-1, 10, 40], device="cuda"), good, 30, 30)):
+        out, lse = R.attend(q, k, v, qo, ko, mq, mk)
+        with pytest.raises(R.RecisError):
+            R.sequence_status_sync()
+        R.attend_backward(out, q, k, v, out, lse, qo, ko, mq, mk)
+        with pytest.raises(R.RecisError):
+            R.sequence_status_sync()
+    R.attend(q, k, v, good, good, 30, 30)
+    R.sequence_status_sync()
+
+
+def test_attend_empty_calls(R):
+    e = torch.empty((0, 2, 16), dtype=BF16, device="cuda")
+    none = torch.zeros(1, dtype=torch.int64, device="cuda")
+    out, lse = R.attend(e, e, e, none, none, 0, 0)
+    assert out.shape == (0, 2, 16) and lse.shape == (0, 2)
+    q = torch.ones((3, 2, 16), dtype=BF16, device="cuda")
+    out, lse = R.attend(q, e, e, _offsets([1, 2]), _offsets([0, 0]), 2, 0)
+    assert not out.any() and (lse == -math.inf).all()
+    gq, gk, gv = R.attend_backward(q, q, e, e, out, lse, _offsets([1, 2]), _offsets([0, 0]), 2, 0)
+    assert not gq.any() and gk.shape == (0, 2, 16)
+    gq, gk, gv = R.attend_backward(e, e, q, q, e, lse[:0], _offsets([0, 0]), _offsets([1, 2]), 0, 2)
+    assert not gk.any() and not gv.any()
+
+
+# ------------------------------------------------------------------ differences
+def test_gradients_against_differences(R):
+    """Each gradient's product with a direction against the central difference
+    of the 64-bit forward (its error is of the step's square and far below)."""
+    g = _gen(9)
+    x, gy = _randn((6, 24), F32, g), _randn((6, 24), F32, g)
+    w, b = _randn((24,), F32, g), _randn((24,), F32, g)
+    dirs = [_randn(t.shape, F32, g).double() for t in (x, w, b)]
+    y, mean, rstd = R.layer_norm(x, w, b)
+    grads = R.layer_norm_backward(gy, x, mean, rstd, w, b)
+    h = 1e-4
+
+    def norm(t):
+        return (S.Norm(x.double() + t * dirs[0], w.double() + t * dirs[1], b.double() + t * dirs[2], 1e-5).y
+                * gy.double()).sum()
+
+    want = (norm(h) - norm(-h)) / (2 * h)
+    got = sum((p.double() * d).sum() for p, d in zip(grads, dirs))
+    mag = sum((p.double() * d).abs().sum() for p, d in zip(grads, dirs))
+    assert abs(got - want) <= 400 * S.F32 * mag + 1e-5
+    qo, ko = _offsets([3, 2]), _offsets([5, 40])
+    q, k, v, go = (_randn((n, 2, 16), F16, g) for n in (5, 45, 45, 5))
+    dirs = [_randn(t.shape, F32, g).double() for t in (q, k, v)]
+    out, lse = R.attend(q, k, v, qo, ko, 3, 40)
+    grads = R.attend_backward(go, q, k, v, out, lse, qo, ko, 3, 40)
+
+    def att(t):
+        ts = [p.double() + t * d for p, d in zip((q, k, v), dirs)]
+        total = 0.0
+        for i in range(2):
+            for hd in range(2):
+                Q, K, V = (p[a[i]:a[i + 1], hd] for p, a in zip(ts, (qo, ko, ko)))
+                total = total + (torch.softmax(Q @ K.T * 0.25, 1) @ V * go.double()[qo[i]:qo[i + 1], hd]).sum()
+        return total
+
+    want = (att(h) - att(-h)) / (2 * h)
+    tol = S.attend(q, k, v, qo, ko, 0.25, None, go)
+    got = sum((p.double() * d).sum() for p, d in zip(grads, dirs))
+    most = sum((tol[n][1] * d.abs()).sum() for n, d in zip(("grad_q", "grad_k", "grad_v"), dirs))
+    assert abs(got - want) <= most + 1e-5
+    t = torch.tensor([0, 2, 2, 1], device="cuda")
+    grad = _randn((4, 8), F32, g)
+    d = _randn((3, 8), F32, g).double()
+    dw = R.embed_grad(t, grad, 3, scale=0.5)
+    want = (S.lookup(d, t, 0.5, -1) * grad.double()).sum()  # the lookup is linear in the weight
+    assert abs((dw.double() * d).sum() - want) <= 10 * S.F32 * (dw.double() * d).abs().sum() + 1e-6
+
+
+# ------------------------------------------------------------------ streams, graphs
+def _step(R, s):
+    q = R.embed_lookup(s["w"], s["tok"], scale=2.0, out_dtype=BF16).view(-1, 4, 32)
+    kv, mean, rstd = R.layer_norm(s["x"], s["g"], s["b"], out_dtype=BF16)
+    k, v = kv[:, :64].unflatten(1, (2, 32)), kv[:, 64:].unflatten(1, (2, 32))
+    bags = (s["qo"], s["ko"], s["mq"], s["mk"])
+    out, lse = R.attend(q, k, v, *bags)
+    dkv = torch.empty_like(kv)
+    dq, _, _ = R.attend_backward(s["go"], q, k, v, out, lse, *bags, grad_k=dkv[:, :64].unflatten(1, (2, 32)),
+                                 grad_v=dkv[:, 64:].unflatten(1, (2, 32)))
+    dx, dg, db = R.layer_norm_backward(dkv, s["x"], mean, rstd, s["g"], s["b"])
+    dw = R.embed_grad(s["tok"], dq.flatten(1), s["w"].shape[0], scale=2.0)
+    return out, lse, dx, dg, db, dw
+
+
+def _state(seed, ql=(3, 0, 40, 7), kl=(500, 9, 130, 0), V=50):
+    g = _gen(seed)
+    s = dict(w=_randn((V, 128), F32, g), x=_randn((sum(kl), 128), F32, g), g=_randn((128,), F32, g),
+             b=_randn((128,), F32, g), go=_randn((sum(ql), 4, 32), BF16, g), qo=_offsets(ql), ko=_offsets(kl),
+             mq=max(ql), mk=max(kl))
+    s["tok"] = torch.randint(-1, V, (sum(ql),), device="cuda", generator=g)
+    return s
+
+
+def test_operators_together_captured_and_replayed(R):
+    """The whole run captured twice (two graphs alive at once), replayed on new
+    inputs in the captured buffers, against eager runs; and on another stream."""
+    states = [_state(20), _state(21, (1, 1, 1, 1), (2000, 1, 64, 65), V=2000)]
+    _step(R, states[0])  # the first call looks up the status word
+    torch.cuda.synchronize()
+    graphs = []
+    for s in states:
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            res = _step(R, s)
+        graphs.append((gr, res))
+    for k in range(2):
+        for s in states:
+            for n in ("w", "x", "g", "b", "go"):
+                s[n].copy_(_randn(s[n].shape, s[n].dtype, _gen(30 + k)))
+        want = [[t.clone() for t in _step(R, s)] for s in states]
+        for gr, _ in graphs:
+            gr.replay()
+        torch.cuda.synchronize()
+        for (_, got), w in zip(graphs, want):
+            assert all(torch.equal(p, q) for p, q in zip(got, w))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = _step(R, states[0])
+    side.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(got, want[0]))
+    y = R.layer_norm(states[0]["x"], stream=side)[0]  # the stream as an argument
+    side.synchronize()
+    assert torch.equal(y, R.layer_norm(states[0]["x"])[0])
+    R.sequence_status_sync()
+
+
+def test_calls_on_two_streams_at_once(R):
+    states = [_state(40 + i) for i in range(4)]
+    want = [_step(R, s) for s in states]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in states]
+    got = []
+    for _ in range(5):
+        got = []
+        for s, st in zip(states, streams):
+            with torch.cuda.stream(st):
+                got.append(_step(R, s))
+    torch.cuda.synchronize()
+    for p, q in zip(want, got):
+        assert all(torch.equal(a, b) for a, b in zip(p, q))
+
+
+# ------------------------------------------------------------------ attention pooling of a table
+def test_sequence_attention_trains_the_table(R):
+    """Two steps of the attention pooling against the 64-bit chain on the same
+    rows: the answers, the dense gradients, and the table's rows after Adagrad
+    with the chain's row gradients."""
+    g = _gen(50)
+    Hkv, Dh, Hq, V = 2, 16, 4, 30
+    D = 2 * Hkv * Dh
+    kw = dict(lr=0.05, adagrad_init_acc=0.5, init_scale=1.0, init_seed=3)
+    table, plain = R.Table(D, R.ADAGRAD, **kw), R.Table(D, R.ADAGRAD, **kw)
+    b0, b1 = R.Batch(), R.Batch()
+    qw, nw, nb = _randn((V, Hq * Dh), F32, g), _randn((D,), F32, g) + 1, _randn((D,), F32, g)
+    att = R.SequenceAttention(table, qw, Hq, Hkv, nw, nb, query_scale=1.5, dtype=F16)
+    kl, ql = [40, 0, 7, 130], [2, 3, 0, 21]
+    for step in range(2):
+        keys = torch.randint(0, 60, (sum(kl),), device="cuda", generator=g) * 1009 + step
+        tok = torch.randint(-1, V, (sum(ql),), device="cuda", generator=g)
+        qo, ko = _offsets(ql), _offsets(kl)
+        go = _randn((sum(ql), Hq, Dh), F16, g)
+        mask = torch.rand(sum(kl), device="cuda", generator=g) < 0.9
+        out = att.forward(b0, keys, ko, tok, qo, max(ql), max(kl), key_mask=mask)
+        dquery, dnw, dnb = att.backward(go)
+        table.status_sync()
+        rows = torch.empty((sum(kl), D), device="cuda")
+        plain.lookup_pooled(b1, keys, ko, 1, 4, unpooled_out=rows)
+        # the chain in 64 bits, its 16-bit activations rounded where the kernels round them
+        ref = S.Norm(rows, nw, nb, 1e-5)
+        kv, q = ref.y.to(F16), S.lookup(qw, tok, 1.5, -1).to(F16).view(-1, Hq, Dh)
+        k, v = kv[:, : D // 2].view(-1, Hkv, Dh), kv[:, D // 2:].view(-1, Hkv, Dh)
+        a = S.attend(q, k, v, qo, ko, Dh ** -0.5, mask, go)
+        # an input of the attention may round the other way (its fp32 value was next to a border): a step of
+        # each input's type, 4 tolerances in all (those of q, k, v and the sums themselves)
+        S.close(out, a["out"][0], 4 * a["out"][1] + 1e-4, "out")
+        dkv, ekv = (torch.cat([a["grad_k"][i].flatten(1), a["grad_v"][i].flatten(1)], 1) for i in range(2))
+        (dx, ex), (dw, ew), (db, eb) = ref.back(dkv, 64)
+        S.close(dnb, db, eb + 4 * ekv.sum(0) + 1e-3, "norm bias")
+        S.close(dnw, dw, ew + 4 * (ekv * ref.xh.abs()).sum(0) + 1e-3, "norm weight")
+        wq, _ = S.embed_grad(tok, a["grad_q"][0].flatten(1), V, 1.5, -1)
+        eq, _ = S.embed_grad(tok, a["grad_q"][1].flatten(1), V, 1.5, -1)
+        S.close(dquery, wq, 4 * eq + 1e-4, "query weight")
+        plain.backward_update(b1, grad_unpooled=dx.float())
+        gk, ge, gs, _ = table.export()
+        pk, pe, ps, _ = plain.export()
+        assert (gk == pk).all()
+        # a row moves by lr * g / (sqrt(acc) + eps), sqrt(acc) >= sqrt(0.5): 0.071 |dg| for a row's summed gradient,
+        # whose terms are off by at most r (|e w| + mean|e w| + |xh| mean|e w xh|), e the attention's tolerance
+        e = 4 * ekv * nw.double().abs()
+        xh = ref.xh.abs()
+        off = ref.rstd[:, None] * (e + e.mean(1, keepdim=True) + xh * (e * xh).mean(1, keepdim=True)) + ex
+        per_key, _ = S.embed_grad(torch.searchsorted(torch.unique(keys), keys), off, torch.unique(keys).numel(), 1.0, -1)
+        most = float(per_key.max()) * 0.071 * (step + 1) + 1e-5
+        assert float(abs(ge - pe).max()) <= most
+    for t in (table, plain, b0, b1):
+        t.close()
