@@ -504,7 +504,7 @@ recis_status recis_layer_norm_backward(const void* grad_y, int32_t y_type, int64
  * type: RECIS_BF16 or RECIS_F16, of every array but lse.  p and ds are rounded
  * to it before their matrix products (tensor-core operands); all sums, the
  * softmax statistics and the joining of partial results are fp32.
- * Strides in elements, multiples of 8 (16 bytes), arrays 16-byte aligned:
+ * Strides in elements, positive multiples of 8 (16 bytes), arrays 16-byte aligned:
  * element (t, h, j) of q is q[t * q_stride + h * q_head_stride + j], grad_q
  * and so on alike.  lse: fp32 [Tq][Hq], contiguous.  D: a multiple of 8, 8..128.
  * Hq a multiple of Hkv, Hq / Hkv <= 128.  B, Tq, Tk, max_q * Hq and max_k * Hkv

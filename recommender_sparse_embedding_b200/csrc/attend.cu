@@ -8,6 +8,7 @@
 // head h is query r / G, head h G + r % G, so K and V are read once for all of
 // them.
 #include <algorithm>
+#include <type_traits>
 
 #include "attend.cuh"
 
@@ -35,7 +36,7 @@ __device__ __forceinline__ void mma16816<__half>(float (&c)[4], const uint32_t (
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-constexpr int kRowTile = 16;   // rows (query, head of the group) a block of few_kernel takes
+constexpr int kRowTile = kFewRows;  // rows (query, head of the group) a block of few_kernel takes
 constexpr int kFewWarps = 4;
 
 // One block: 16 rows of one key head against one part of the bag's keys; warp w
@@ -400,12 +401,15 @@ AttendPlan attend_plan(const recis_attend_args& a, bool backward) {
     g.delta_bytes = align256(a.Tq * a.Hq * 4);
   } else {
     // parts of the keys: enough blocks for every SM to hold a few, each part
-    // at least 256 keys (16 iterations a warp hide its fixed cost)
-    const int64_t G = a.Hq / a.Hkv, rtiles = std::max<int64_t>(1, (a.max_q * G + kRowTile - 1) / kRowTile);
-    const int64_t blocks = std::max<int64_t>(1, a.B * a.Hkv * rtiles);
-    const int64_t want = std::min<int64_t>((kSMs * 8 + blocks - 1) / blocks, (a.max_k + 255) / 256);
+    // at least 256 keys (few rows: 16 iterations a warp) or 512 (tiles: 4 steps)
+    const int64_t G = a.Hq / a.Hkv;
+    const bool few = a.max_q * G <= kFewRows;
+    const int64_t tile = few ? std::max<int64_t>(kRowTile / G, 1) : 128 / G;  // queries a block
+    const int64_t blocks = std::max<int64_t>(1, a.B * a.Hkv * ((a.max_q + tile - 1) / tile));
+    const int64_t least = few ? 256 : 512;
+    const int64_t want = std::min<int64_t>((kSMs * (few ? 8 : 4) + blocks - 1) / blocks, (a.max_k + least - 1) / least);
     if (want > 1) {
-      g.split_keys = (int)((a.max_k + want - 1) / want + 63) / 64 * 64;
+      g.split_keys = (int)((a.max_k + want - 1) / want + 127) / 128 * 128;
       g.splits = (int)((a.max_k + g.split_keys - 1) / g.split_keys);
     }
     if (g.splits > 1) {
@@ -431,8 +435,8 @@ recis_status check_sizes(const recis_attend_args* a, const char* what) {
 
 // rows of heads of D elements: aligned for 16-byte accesses
 bool bad_array(const void* p, int64_t stride, int64_t head_stride, int64_t rows) {
-  return rows > 0 && (!p || misaligned(p, 16) || stride % 8 != 0 || head_stride % 8 != 0 || stride < 0 ||
-                      head_stride < 0);
+  return rows > 0 && (!p || misaligned(p, 16) || stride % 8 != 0 || head_stride % 8 != 0 || stride <= 0 ||
+                      head_stride <= 0);
 }
 
 // bags, rows and blocks of a launch fit its grid
@@ -471,13 +475,17 @@ recis_status fill(const recis_attend_args* a, AttendParams* p, const AttendPlan&
 
 template <typename T>
 recis_status forward(const AttendParams& p, cudaStream_t s) {
+  const bool few = p.max_q * p.G <= kFewRows;
   const int64_t rtiles = ((int64_t)p.max_q * p.G + kRowTile - 1) / kRowTile;
   const int64_t grid = (int64_t)p.B * p.splits * p.Hkv * rtiles, jgrid = (int64_t)p.B * (((int64_t)p.max_q * p.Hq + 3) / 4);
-  if (!grid_fits(grid) || !grid_fits(jgrid)) {
+  if ((few && !grid_fits(grid)) || !grid_fits(jgrid)) {
     set_error("attend: too many blocks (bags times max_q times heads)");
     return RECIS_ERR_INVALID_ARG;
   }
-  {
+  if (!few) {
+    const recis_status st = launch_attend_tc(p, std::is_same<T, __nv_bfloat16>::value, s);
+    if (st != RECIS_OK) return st;
+  } else {
     LaunchScope ls("attend_few", s);
     if (p.D <= 32) few_kernel<T, 32><<<(unsigned)grid, kFewWarps * 32, 0, s>>>(p);
     else if (p.D <= 64) few_kernel<T, 64><<<(unsigned)grid, kFewWarps * 32, 0, s>>>(p);

@@ -42,4 +42,8 @@ __device__ __forceinline__ Bag load_bag(const AttendParams& p, int b) {
   return Bag{q0, k0, (int)(q1 - q0), (int)(k1 - k0)};
 }
 
+// more rows (queries times heads of a group) than this in a bag: tensor-core tiles
+constexpr int kFewRows = 16;
+recis_status launch_attend_tc(const AttendParams& p, bool bf16, cudaStream_t s);
+
 }  // namespace recis
