@@ -286,106 +286,6 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Atten
   if (lane == 0) p.lse[at] = sum == 0.f ? -INFINITY : base + logf(sum);
 }
 
-// ---------------------------------------------------------------- backward
-// delta[t][h] = sum_d grad_out * out: one warp a (query, head)
-template <typename T>
-__global__ void __launch_bounds__(256) delta_kernel(const __grid_constant__ AttendParams p) {
-  const int lane = threadIdx.x & 31, d = lane * 4;
-  const int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (i >= p.Tq * p.Hq) return;
-  const int64_t t = i / p.Hq;
-  const int h = (int)(i % p.Hq);
-  float s = 0.f;
-  if (d < p.D) {
-    const uint2 a = *reinterpret_cast<const uint2*>(static_cast<const T*>(p.out) + t * p.os + h * p.oh + d);
-    const uint2 b = *reinterpret_cast<const uint2*>(static_cast<const T*>(p.go) + t * p.gos + h * p.goh + d);
-    const float2 a0 = unpack2<T>(a.x), a1 = unpack2<T>(a.y), b0 = unpack2<T>(b.x), b1 = unpack2<T>(b.y);
-    s = a0.x * b0.x + a0.y * b0.y + a1.x * b1.x + a1.y * b1.y;
-  }
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-  if (lane == 0) p.delta[i] = s;
-}
-
-template <typename T>
-__device__ __forceinline__ float4 load4(const void* base, int64_t at, int d, int D) {
-  if (d >= D) return make_float4(0.f, 0.f, 0.f, 0.f);
-  const uint2 a = *reinterpret_cast<const uint2*>(static_cast<const T*>(base) + at + d);
-  const float2 x = unpack2<T>(a.x), y = unpack2<T>(a.y);
-  return make_float4(x.x, x.y, y.x, y.y);
-}
-__device__ __forceinline__ float dot4(float4 a, float4 b) { return a.x * b.x + a.y * b.y + a.z * b.z + a.w * b.w; }
-__device__ __forceinline__ void warp_sum2(float& a, float& b) {
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) {
-    a += __shfl_xor_sync(0xffffffffu, a, off);
-    b += __shfl_xor_sync(0xffffffffu, b, off);
-  }
-}
-__device__ __forceinline__ void axpy4(float4& y, float a, float4 x) {
-  y.x = fmaf(a, x.x, y.x);
-  y.y = fmaf(a, x.y, y.y);
-  y.z = fmaf(a, x.z, y.z);
-  y.w = fmaf(a, x.w, y.w);
-}
-template <typename T>
-__device__ __forceinline__ void put4(void* base, int64_t at, int d, int D, float4 v) {
-  if (d < D)
-    *reinterpret_cast<uint2*>(static_cast<T*>(base) + at + d) = make_uint2(pack2<T>(v.x, v.y), pack2<T>(v.z, v.w));
-}
-
-// one warp a (query, head): grad_q over the bag's keys
-template <typename T>
-__global__ void __launch_bounds__(128) back_q_kernel(const __grid_constant__ AttendParams p) {
-  const int lane = threadIdx.x & 31, d = lane * 4;
-  const int tiles = (p.max_q * p.Hq + 3) / 4;
-  const int b = blockIdx.x / tiles, i = (blockIdx.x % tiles) * 4 + (threadIdx.x >> 5);
-  const Bag bag = load_bag(p, b);
-  if (i >= bag.nq * p.Hq) return;
-  const int64_t t = bag.q0 + i / p.Hq;
-  const int hq = i % p.Hq, h = hq / p.G;
-  const float4 q = load4<T>(p.q, t * p.qs + hq * p.qh, d, p.D), go = load4<T>(p.go, t * p.gos + hq * p.goh, d, p.D);
-  const float lse = p.lse[t * p.Hq + hq], delta = p.delta[t * p.Hq + hq];
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int j = 0; j < bag.nk; ++j) {
-    if (p.mask && !p.mask[bag.k0 + j]) continue;
-    const float4 k = load4<T>(p.k, (bag.k0 + j) * p.ks + h * p.kh, d, p.D);
-    float s = dot4(q, k), dp = dot4(go, load4<T>(p.v, (bag.k0 + j) * p.vs + h * p.vh, d, p.D));
-    warp_sum2(s, dp);
-    axpy4(acc, expf(s * p.scale - lse) * (dp - delta) * p.scale, k);
-  }
-  put4<T>(p.gq, t * p.gqs + hq * p.gqh, d, p.D, acc);
-}
-
-// one warp a (key, key head): grad_k and grad_v over the bag's rows
-template <typename T>
-__global__ void __launch_bounds__(128) back_k_kernel(const __grid_constant__ AttendParams p) {
-  const int lane = threadIdx.x & 31, d = lane * 4;
-  const int tiles = (p.max_k * p.Hkv + 3) / 4;
-  const int b = blockIdx.x / tiles, i = (blockIdx.x % tiles) * 4 + (threadIdx.x >> 5);
-  const Bag bag = load_bag(p, b);
-  if (i >= bag.nk * p.Hkv) return;
-  const int64_t t = bag.k0 + i / p.Hkv;
-  const int h = i % p.Hkv;
-  float4 gk = make_float4(0.f, 0.f, 0.f, 0.f), gv = gk;
-  if (!p.mask || p.mask[t]) {
-    const float4 k = load4<T>(p.k, t * p.ks + h * p.kh, d, p.D), v = load4<T>(p.v, t * p.vs + h * p.vh, d, p.D);
-    for (int r = 0; r < bag.nq * p.G; ++r) {
-      const int64_t tq = bag.q0 + r / p.G;
-      const int hq = h * p.G + r % p.G;
-      const float4 q = load4<T>(p.q, tq * p.qs + hq * p.qh, d, p.D);
-      const float4 go = load4<T>(p.go, tq * p.gos + hq * p.goh, d, p.D);
-      float s = dot4(q, k), dp = dot4(go, v);
-      warp_sum2(s, dp);
-      const float pr = expf(s * p.scale - p.lse[tq * p.Hq + hq]);
-      axpy4(gv, pr, go);
-      axpy4(gk, pr * (dp - p.delta[tq * p.Hq + hq]) * p.scale, q);
-    }
-  }
-  put4<T>(p.gk, t * p.gks + h * p.gkh, d, p.D, gk);
-  put4<T>(p.gv, t * p.gvs + h * p.gvh, d, p.D, gv);
-}
-
 // ---------------------------------------------------------------- host
 struct AttendPlan {
   int splits, split_keys;
@@ -399,6 +299,14 @@ AttendPlan attend_plan(const recis_attend_args& a, bool backward) {
   g.split_keys = (int)std::max<int64_t>(a.max_k, 1);
   if (backward) {
     g.delta_bytes = align256(a.Tq * a.Hq * 4);
+    // parts of the keys for grad_q, as in the forward: two blocks an SM, 512 keys a part
+    const int64_t TQ = 128 / (a.Hq / a.Hkv), blocks = std::max<int64_t>(1, a.B * a.Hkv * ((a.max_q + TQ - 1) / TQ));
+    const int64_t want = std::min<int64_t>((kSMs * 2 + blocks - 1) / blocks, (a.max_k + 511) / 512);
+    if (want > 1) {
+      g.split_keys = (int)((a.max_k + want - 1) / want + 127) / 128 * 128;
+      g.splits = (int)((a.max_k + g.split_keys - 1) / g.split_keys);
+    }
+    if (g.splits > 1) g.po_bytes = align256(g.splits * a.Tq * a.Hq * a.D * 4);
   } else {
     // parts of the keys: enough blocks for every SM to hold a few, each part
     // at least 256 keys (few rows: 16 iterations a warp) or 512 (tiles: 4 steps)
@@ -460,7 +368,8 @@ recis_status fill(const recis_attend_args* a, AttendParams* p, const AttendPlan&
   p->gvs = a->grad_v_stride; p->gvh = a->grad_v_head_stride;
   p->Tq = a->Tq; p->Tk = a->Tk;
   p->B = (int)a->B; p->Hq = a->Hq; p->Hkv = a->Hkv; p->G = a->Hq / a->Hkv; p->D = a->D;
-  p->max_q = (int)a->max_q; p->max_k = (int)a->max_k;
+  // a bound of 0 still launches the blocks that look at every bag's offsets
+  p->max_q = (int)std::max<int64_t>(a->max_q, 1); p->max_k = (int)std::max<int64_t>(a->max_k, 1);
   p->scale = (float)a->scale;
   p->scale_log2 = (float)(a->scale * 1.4426950408889634);
   p->splits = g.splits;
@@ -497,34 +406,6 @@ recis_status forward(const AttendParams& p, cudaStream_t s) {
     LaunchScope ls("attend_join", s);
     join_kernel<T><<<(unsigned)jgrid, 128, 0, s>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "attend_join launch");
-  }
-  return RECIS_OK;
-}
-
-template <typename T>
-recis_status backward(const AttendParams& p, cudaStream_t s) {
-  const int64_t qgrid = (int64_t)p.B * (((int64_t)p.max_q * p.Hq + 3) / 4);
-  const int64_t kgrid = (int64_t)p.B * (((int64_t)p.max_k * p.Hkv + 3) / 4);
-  const int64_t dgrid = (p.Tq * p.Hq + 7) / 8;
-  if (!grid_fits(qgrid) || !grid_fits(kgrid) || !grid_fits(dgrid)) {
-    set_error("attend_backward: too many blocks (bags times longest bag times heads)");
-    return RECIS_ERR_INVALID_ARG;
-  }
-  cudaError_t e;
-  if (dgrid > 0) {
-    LaunchScope ls("attend_delta", s);
-    delta_kernel<T><<<(unsigned)dgrid, 256, 0, s>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "attend_delta launch");
-  }
-  if (qgrid > 0) {
-    LaunchScope ls("attend_back_q", s);
-    back_q_kernel<T><<<(unsigned)qgrid, 128, 0, s>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "attend_back_q launch");
-  }
-  if (kgrid > 0) {
-    LaunchScope ls("attend_back_k", s);
-    back_k_kernel<T><<<(unsigned)kgrid, 128, 0, s>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "attend_back_k launch");
   }
   return RECIS_OK;
 }
@@ -574,7 +455,7 @@ extern "C" recis_status recis_attend(const recis_attend_args* a, void* workspace
                                      recis_stream_t stream) {
   recis_status st = check_call(a, false, workspace, workspace_bytes, "attend");
   if (st != RECIS_OK) return st;
-  if (a->B == 0 || a->Tq == 0 || a->max_q == 0) return RECIS_OK;
+  if (a->B == 0 || a->Tq == 0) return RECIS_OK;
   AttendParams p;
   if ((st = fill(a, &p, attend_plan(*a, false), workspace)) != RECIS_OK) return st;
   return a->type == RECIS_BF16 ? forward<__nv_bfloat16>(p, (cudaStream_t)stream)
@@ -588,6 +469,5 @@ extern "C" recis_status recis_attend_backward(const recis_attend_args* a, void* 
   if (a->B == 0) return RECIS_OK;
   AttendParams p;
   if ((st = fill(a, &p, attend_plan(*a, true), workspace)) != RECIS_OK) return st;
-  return a->type == RECIS_BF16 ? backward<__nv_bfloat16>(p, (cudaStream_t)stream)
-                               : backward<__half>(p, (cudaStream_t)stream);
+  return launch_attend_back(p, a->type == RECIS_BF16, (cudaStream_t)stream);
 }

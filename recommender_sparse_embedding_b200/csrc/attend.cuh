@@ -45,5 +45,6 @@ __device__ __forceinline__ Bag load_bag(const AttendParams& p, int b) {
 // more rows (queries times heads of a group) than this in a bag: tensor-core tiles
 constexpr int kFewRows = 16;
 recis_status launch_attend_tc(const AttendParams& p, bool bf16, cudaStream_t s);
+recis_status launch_attend_back(const AttendParams& p, bool bf16, cudaStream_t s);
 
 }  // namespace recis

@@ -1,0 +1,475 @@
+// attend_back.cu -- attention backward, on the tensor cores.
+//
+//   p = exp(s - lse), dp = dO V^T, ds = p (dp - delta), delta = sum(dO * O),
+//   dV = p^T dO,  dK = scale ds^T Q,  dQ = scale ds K.
+//
+// Two passes of one kernel.  Each block keeps a pair of 128-row tiles X1, X2 in
+// shared memory and streams pairs of 64-row tiles Y1, Y2 past them:
+//
+//   keys:    X = (K, V) of 128 keys,  Y = (Q, dO);  A1 = dV += P^T Y2, A2 = dK += dS^T Y1
+//   queries: X = (Q, dO) of 128 rows, Y = (K, V);                      A2 = dQ += dS Y1
+//
+// S = X1 Y1^T and dP = X2 Y2^T go to tensor memory, the compute warps (one row
+// of X a thread) write P and dS over them as 16-bit values, and the second
+// products take them from there; the accumulators stay in tensor memory.  The
+// scores are thus computed twice (7 products instead of 5), but no block adds
+// to another's output: no atomics, and the result does not depend on
+// scheduling.  The query heads that share a key head are rows of one matrix
+// (row r: query r / G, head r % G), so dK and dV sum over them in the
+// accumulator.
+//
+// Rows of a tile that belong to another bag, or to masked keys, are overwritten
+// with zeros before the products (0 * NaN is NaN) by the warp that issues the
+// copies, which waits for such a tile's data itself.
+#include <algorithm>
+#include <type_traits>
+
+#include "attend.cuh"
+#include "tc.cuh"
+
+namespace recis {
+
+namespace {
+
+constexpr int kX = 128;  // resident rows
+constexpr int kY = 64;   // streamed rows a step
+constexpr int kNS = 4;   // streamed tiles in flight
+
+template <int DP>
+struct BackCfg {
+  static constexpr int kBlocks = DP / 64;
+  static constexpr int kXBytes = kBlocks * kX * 128, kYBytes = kBlocks * kY * 128;  // one tile
+  // D <= 64: two blocks an SM hide each other's waits (half of tensor memory
+  // each, S and dP once); D <= 128: one block, S and dP twice
+  static constexpr int kBuf = DP == 64 ? 1 : 2;
+  static constexpr int kWG = DP == 64 ? 1 : 2;      // compute warpgroups
+  static constexpr int kThreads = kWG * 128 + 64;
+  static constexpr int kBlocksPerSM = DP == 64 ? 2 : 1;
+  static constexpr uint32_t kCols = DP == 64 ? 256 : 512;
+  static constexpr uint32_t kAcc1 = kBuf * 128, kAcc2 = kAcc1 + DP;
+  static constexpr int kTotal = 2 * kXBytes + 2 * kNS * kYBytes + 1024 + 256 + 2 * kNS * kY * 4;
+};
+
+struct BackMaps {
+  CUtensorMap x1, x2, y1, y2;
+};
+
+template <typename T, int DP, bool KEYS>
+__global__ void __launch_bounds__(BackCfg<DP>::kThreads, BackCfg<DP>::kBlocksPerSM)
+    attend_back_kernel(const __grid_constant__ AttendParams p, const __grid_constant__ BackMaps maps, int spin_max) {
+  using C = BackCfg<DP>;
+  constexpr int NB = C::kBuf, WG = C::kWG;
+  constexpr int kDelay = NB == 2 ? kNS - 2 : kNS - 1;  // tiles asked for ahead of the one that is finished
+  extern __shared__ uint8_t s_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(s_raw) + 1023) & ~(uintptr_t)1023);
+  uint8_t *x1 = base, *x2 = x1 + C::kXBytes, *y1 = x2 + C::kXBytes, *y2 = y1 + kNS * C::kYBytes;
+  uint64_t* bar = reinterpret_cast<uint64_t*>(y2 + kNS * C::kYBytes);
+  uint64_t *x_full = bar, *acc_full = bar + 1, *s_full = bar + 2, *e_full = s_full + NB;
+  uint64_t *y_full = e_full + NB, *y_empty = y_full + kNS, *y_raw = y_empty + kNS;
+  float* s_lse = reinterpret_cast<float*>(y2 + kNS * C::kYBytes + 256);  // KEYS: [kNS][kY] lse * log2(e)
+  float* s_delta = s_lse + kNS * kY;                                     // KEYS: [kNS][kY]
+  __shared__ uint32_t s_tmem;
+  __shared__ uint32_t s_valid[kNS][2];  // queries: the streamed keys that take part
+
+  // the block's tile: of keys, or of (query, head) rows against a part of the keys
+  const int TQ = kX / p.G;                                  // queries: queries a tile
+  const int per_bag = KEYS ? (p.max_k + kX - 1) / kX : (p.max_q + TQ - 1) / TQ;
+  unsigned id = blockIdx.x;
+  const int tile = id % per_bag;
+  id /= per_bag;
+  const int h = id % p.Hkv;
+  id /= p.Hkv;
+  const int sp = KEYS ? 0 : id % p.splits, b = KEYS ? id : id / p.splits;
+  const Bag bag = load_bag(p, b);
+  const int first = tile * (KEYS ? kX : TQ);                // first key, or query, of the tile
+  const int ks = KEYS ? 0 : sp * p.split_keys, ke = KEYS ? bag.nk : min(ks + p.split_keys, bag.nk);
+  if (first >= (KEYS ? bag.nk : bag.nq) || (!KEYS && sp > 0 && ks >= bag.nk)) return;
+  // streamed tiles; keys: heads in chunks of at most 64, the queries of a chunk's tile
+  const int gc = min(p.G, kY), chunks = (p.G + gc - 1) / gc, tq = kY / gc;
+  const int n = KEYS ? (bag.nq + tq - 1) / tq * chunks : ke > ks ? (ke - ks + kY - 1) / kY : 0;
+
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  constexpr int kLoader = WG * 4, kIssuer = kLoader + 1;
+  if (w == kIssuer) tmem_alloc(&s_tmem, C::kCols);
+  if (tid == kLoader * 32) {
+    mbar_init(x_full, 1);
+    mbar_init(acc_full, 1);
+    for (int i = 0; i < NB; ++i) {
+      mbar_init(s_full + i, 1);
+      mbar_init(e_full + i, WG * 128);
+    }
+    for (int i = 0; i < kNS; ++i) {
+      mbar_init(y_full + i, 2);
+      mbar_init(y_empty + i, 1);
+      mbar_init(y_raw + i, 1);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  bool ok = true;  // false: a wait gave up
+
+  if (w == kLoader) {
+    if (n > 0) {
+      if (lane == 0) {
+        const int rows = KEYS ? kX : TQ * p.G;
+        mbar_arrive_expect(x_full, (unsigned)(2 * C::kBlocks * rows * 128));
+        for (int i = 0; i < C::kBlocks; ++i) {
+          const int y = KEYS ? h : h * p.G, z = (int)((KEYS ? bag.k0 : bag.q0) + first);
+          tma_load3(x1 + i * kX * 128, &maps.x1, 64 * i, y, z, x_full);
+          tma_load3(x2 + i * kX * 128, &maps.x2, 64 * i, y, z, x_full);
+        }
+      }
+      // a streamed tile that holds rows which must be zeroed
+      auto special = [&](int j) {
+        if (!KEYS) return ks + (j + 1) * kY > ke || p.mask != nullptr;
+        return tq * gc < kY || (j / chunks + 1) * tq > bag.nq || (j % chunks + 1) * gc > p.G;
+      };
+      int asked = 0;
+      for (int j = 0; j < n + kDelay && ok; ++j) {
+        if (j < n) {
+          const int st = j % kNS;
+          if (j >= kNS) ok = mbar_wait(y_empty + st, ((j / kNS) & 1) ^ 1, spin_max);
+          if (!__all_sync(0xffffffffu, ok)) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) {
+            uint64_t* full = y_full + st;
+            if (special(j)) {
+              mbar_arrive(full);
+              full = y_raw + st;
+            }
+            const int rows = KEYS ? tq * gc : kY;
+            mbar_arrive_expect(full, (unsigned)(2 * C::kBlocks * rows * 128));
+            const int y = KEYS ? h * p.G + (j % chunks) * gc : h;
+            const int z = KEYS ? (int)(bag.q0 + (j / chunks) * tq) : (int)(bag.k0 + ks + j * kY);
+            for (int i = 0; i < C::kBlocks; ++i) {
+              tma_load3(y1 + st * C::kYBytes + i * kY * 128, &maps.y1, 64 * i, y, z, full);
+              tma_load3(y2 + st * C::kYBytes + i * kY * 128, &maps.y2, 64 * i, y, z, full);
+            }
+          }
+          asked = j + 1;
+        }
+        const int f = j - kDelay;
+        if (f < 0) continue;
+        const int st = f % kNS;
+        bool v[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = lane + 32 * i;
+          if (KEYS) {
+            const int q = (f / chunks) * tq + r / gc, g = (f % chunks) * gc + r % gc;
+            v[i] = r < tq * gc && q < bag.nq && g < p.G;
+            float lse = INFINITY, delta = 0.f;
+            if (v[i]) {
+              const int64_t at = (bag.q0 + q) * p.Hq + h * p.G + g;
+              lse = __ldg(p.lse + at) * 1.4426950408889634f;
+              if (lse == -INFINITY) lse = INFINITY;  // a row without keys: p = 0
+              delta = __ldg(p.delta + at);
+            }
+            s_lse[st * kY + r] = lse;
+            s_delta[st * kY + r] = delta;
+          } else {
+            const int key = ks + f * kY + r;
+            v[i] = key < ke && (!p.mask || p.mask[bag.k0 + key]);
+            const unsigned bits = __ballot_sync(0xffffffffu, v[i]);
+            if (lane == 0) s_valid[st][i] = bits;
+          }
+        }
+        if (special(f)) {
+          ok = mbar_wait(y_raw + st, (f / kNS) & 1, spin_max);  // every tile of a stage's turn completes this phase
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            if (!v[i])
+              for (int k = 0; k < C::kBlocks; ++k) {
+                uint4* a = reinterpret_cast<uint4*>(y1 + st * C::kYBytes + (k * kY + lane + 32 * i) * 128);
+                uint4* c = reinterpret_cast<uint4*>(y2 + st * C::kYBytes + (k * kY + lane + 32 * i) * 128);
+#pragma unroll
+                for (int u = 0; u < 8; ++u) a[u] = c[u] = make_uint4(0, 0, 0, 0);
+              }
+          fence_async_smem();
+        } else if (lane == 0) {
+          mbar_arrive(y_raw + st);  // keeps the stage's phases in step
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(y_full + st);
+      }
+      // copies in flight end before the block does
+      ok = mbar_wait(x_full, 0, spin_max) && ok;
+      if (!ok)
+        for (int j = max(asked - kNS, 0); j < asked; ++j)
+          mbar_wait((special(j) ? y_raw : y_full) + j % kNS, (j / kNS) & 1, 64);
+    }
+  } else if (w == kIssuer) {
+    if (lane == 0 && n > 0) {
+      constexpr uint32_t id_s = mma_desc<T>(kX, kY, false, false), id_a = mma_desc<T>(kX, DP, false, true);
+      const uint32_t ax1 = smem_u32(x1), ax2 = smem_u32(x2), ay1 = smem_u32(y1), ay2 = smem_u32(y2);
+      auto scores = [&](int j) {
+        const int st = j % kNS, bf = j % NB;
+        if (!mbar_wait(y_full + st, (j / kNS) & 1, spin_max)) return false;
+        tc_fence_after();
+        const uint32_t d = tmem + bf * 128;
+#pragma unroll
+        for (int k = 0; k < DP / 16; ++k) {
+          const uint32_t xo = (k >> 2) * kX * 128 + (k & 3) * 32, yo = st * C::kYBytes + (k >> 2) * kY * 128 + (k & 3) * 32;
+          mma_ss(d, smem_desc(ax1 + xo, 16), smem_desc(ay1 + yo, 16), id_s, k > 0);
+        }
+#pragma unroll
+        for (int k = 0; k < DP / 16; ++k) {
+          const uint32_t xo = (k >> 2) * kX * 128 + (k & 3) * 32, yo = st * C::kYBytes + (k >> 2) * kY * 128 + (k & 3) * 32;
+          mma_ss(d + 64, smem_desc(ax2 + xo, 16), smem_desc(ay2 + yo, 16), id_s, k > 0);
+        }
+        mma_commit(s_full + bf);
+        return true;
+      };
+      ok = mbar_wait(x_full, 0, spin_max) && scores(0);
+      for (int j = 0; j < n && ok; ++j) {
+        const int st = j % kNS, bf = j % NB;
+        if (NB == 2 && j + 1 < n && !(ok = scores(j + 1))) break;
+        if (!(ok = mbar_wait(e_full + bf, (j / NB) & 1, spin_max))) break;
+        tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < kY / 16; ++k) {
+          const uint32_t e = tmem + bf * 128 + (k >> 1) * 32 + (k & 1) * 8;
+          if (KEYS)
+            mma_ts(tmem + C::kAcc1, e, smem_desc(ay2 + st * C::kYBytes + k * 2048, kY * 128), id_a, j > 0 || k > 0);
+          mma_ts(tmem + C::kAcc2, e + 64, smem_desc(ay1 + st * C::kYBytes + k * 2048, kY * 128), id_a, j > 0 || k > 0);
+        }
+        mma_commit(y_empty + st);
+        if (NB == 1 && j + 1 < n && !(ok = scores(j + 1))) break;
+      }
+      mma_commit(acc_full);
+      ok = mbar_wait(acc_full, 0, spin_max) && ok;
+    }
+    __syncwarp();
+  } else {
+    const int row = tid & 127, wg = tid >> 7;  // the thread's row of X
+    const uint32_t mine = tmem + ((uint32_t)(w & 3) << 21);
+    bool live;
+    int64_t t;       // its row in memory
+    int hx;          // its head
+    float lse = INFINITY, delta = 0.f;
+    if (KEYS) {
+      live = first + row < bag.nk;
+      t = bag.k0 + first + row;
+      hx = h;
+    } else {
+      live = row < TQ * p.G && first + row / p.G < bag.nq;
+      t = bag.q0 + first + row / p.G;
+      hx = h * p.G + row % p.G;
+      if (live) {
+        lse = p.lse[t * p.Hq + hx] * 1.4426950408889634f;
+        if (lse == -INFINITY) lse = INFINITY;
+        delta = p.delta[t * p.Hq + hx];
+      }
+    }
+    const bool any = __any_sync(0xffffffffu, live);
+    const float c = p.scale_log2;
+    for (int j = 0; j < n; ++j) {
+      const int st = j % kNS, bf = j % NB;
+      ok = mbar_wait(y_full + st, (j / kNS) & 1, spin_max) && mbar_wait(s_full + bf, (j / NB) & 1, spin_max);
+      if (!__all_sync(0xffffffffu, ok)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      if (any) {
+#pragma unroll
+        for (int q = 0; q < 2 / WG; ++q) {
+          const int col = (wg + q) * 32;  // WG == 2: the warpgroup's half; else both in turn
+          uint32_t s[32], d[32];
+          tmem_ld32(mine + bf * 128 + col, s);
+          tmem_ld32(mine + bf * 128 + 64 + col, d);
+          tmem_wait_ld();
+          uint32_t valid = 0xffffffffu;
+          if (!KEYS) valid = s_valid[st][col >> 5];
+          uint32_t pk[16], dk[16];
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) {
+            float4 ls = make_float4(lse, lse, lse, lse), de = make_float4(delta, delta, delta, delta);
+            if (KEYS) {
+              ls = *reinterpret_cast<const float4*>(s_lse + st * kY + col + i);
+              de = *reinterpret_cast<const float4*>(s_delta + st * kY + col + i);
+            }
+            float e[4], f[4];
+            e[0] = ex2(fmaf(__uint_as_float(s[i]), c, -ls.x));
+            e[1] = ex2(fmaf(__uint_as_float(s[i + 1]), c, -ls.y));
+            e[2] = ex2(fmaf(__uint_as_float(s[i + 2]), c, -ls.z));
+            e[3] = ex2(fmaf(__uint_as_float(s[i + 3]), c, -ls.w));
+            f[0] = e[0] * (__uint_as_float(d[i]) - de.x);
+            f[1] = e[1] * (__uint_as_float(d[i + 1]) - de.y);
+            f[2] = e[2] * (__uint_as_float(d[i + 2]) - de.z);
+            f[3] = e[3] * (__uint_as_float(d[i + 3]) - de.w);
+            if (!KEYS && valid != 0xffffffffu)
+#pragma unroll
+              for (int u = 0; u < 4; ++u)
+                if (!(valid >> (i + u) & 1)) f[u] = 0.f;
+            if (KEYS) {
+              pk[i / 2] = pack2<T>(e[0], e[1]);
+              pk[i / 2 + 1] = pack2<T>(e[2], e[3]);
+            }
+            dk[i / 2] = pack2<T>(f[0], f[1]);
+            dk[i / 2 + 1] = pack2<T>(f[2], f[3]);
+          }
+          if (KEYS) tmem_st16(mine + bf * 128 + col, pk);
+          tmem_st16(mine + bf * 128 + 64 + col, dk);
+        }
+        tmem_wait_st();
+      }
+      tc_fence_before();
+      mbar_arrive(e_full + bf);
+    }
+    if (n > 0) ok = mbar_wait(acc_full, 0, spin_max) && ok;
+    ok = __all_sync(0xffffffffu, ok);
+    tc_fence_after();
+    const bool have = n > 0 && ok;
+    const bool takes = !KEYS || !p.mask || (live && p.mask[t]);  // a masked key's gradients are zero
+    // 2 accumulators (keys) or 1 (queries) of DP columns, in pieces of 32
+    constexpr int kPieces = (KEYS ? 2 : 1) * DP / 32;
+#pragma unroll
+    for (int q = 0; q < kPieces / WG; ++q) {
+      const int piece = q + wg * (kPieces / WG);
+      const bool acc1 = KEYS && piece < DP / 32;
+      const int d0 = piece * 32 % DP;
+      uint32_t r[32];
+      if (have) {
+        tmem_ld32(mine + (acc1 ? C::kAcc1 : C::kAcc2) + d0, r);
+        tmem_wait_ld();
+      }
+      const float mul = acc1 ? 1.0f : p.scale;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int d = d0 + 8 * i;
+        float f[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = have && takes ? __uint_as_float(r[8 * i + e]) * mul : 0.f;
+        if (live && d < p.D) {
+          if (KEYS) store_vec(static_cast<T*>(acc1 ? p.gv : p.gk) + t * (acc1 ? p.gvs : p.gks) +
+                                  hx * (acc1 ? p.gvh : p.gkh) + d, f);
+          else if (p.splits == 1) store_vec(static_cast<T*>(p.gq) + t * p.gqs + hx * p.gqh + d, f);
+          else store_vec(p.po + (((int64_t)sp * p.Tq + t) * p.Hq + hx) * p.D + d, f);
+        }
+      }
+    }
+  }
+  if (!ok) atomicOr(p.status, kErrTimeout);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (w == kIssuer) tmem_free(tmem, C::kCols);
+}
+
+// delta[t][h] = sum_d grad_out * out: one warp a (query, head)
+template <typename T>
+__global__ void __launch_bounds__(256) delta_kernel(const __grid_constant__ AttendParams p) {
+  const int lane = threadIdx.x & 31, d = lane * 4;
+  const int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (i >= p.Tq * p.Hq) return;
+  const int64_t t = i / p.Hq;
+  const int h = (int)(i % p.Hq);
+  float s = 0.f;
+  if (d < p.D) {
+    const uint2 a = *reinterpret_cast<const uint2*>(static_cast<const T*>(p.out) + t * p.os + h * p.oh + d);
+    const uint2 b = *reinterpret_cast<const uint2*>(static_cast<const T*>(p.go) + t * p.gos + h * p.goh + d);
+    const float2 a0 = unpack2<T>(a.x), a1 = unpack2<T>(a.y), b0 = unpack2<T>(b.x), b1 = unpack2<T>(b.y);
+    s = a0.x * b0.x + a0.y * b0.y + a1.x * b1.x + a1.y * b1.y;
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+  if (lane == 0) p.delta[i] = s;
+}
+
+// grad_q from the parts of the keys, added in order: one warp a (query, head)
+template <typename T>
+__global__ void __launch_bounds__(128) join_q_kernel(const __grid_constant__ AttendParams p) {
+  const int lane = threadIdx.x & 31, d = lane * 4;
+  const int tiles = (p.max_q * p.Hq + 3) / 4;
+  const int b = blockIdx.x / tiles, i = (blockIdx.x % tiles) * 4 + (threadIdx.x >> 5);
+  const Bag bag = load_bag(p, b);
+  if (i >= bag.nq * p.Hq || d >= p.D) return;
+  const int64_t t = bag.q0 + i / p.Hq, step = p.Tq * p.Hq;
+  const int hq = i % p.Hq, n = max(1, (bag.nk + p.split_keys - 1) / p.split_keys);
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s = 0; s < n; ++s) {
+    const float4 v = *reinterpret_cast<const float4*>(p.po + (s * step + t * p.Hq + hq) * p.D + d);
+    a.x += v.x;
+    a.y += v.y;
+    a.z += v.z;
+    a.w += v.w;
+  }
+  *reinterpret_cast<uint2*>(static_cast<T*>(p.gq) + t * p.gqs + hq * p.gqh + d) =
+      make_uint2(pack2<T>(a.x, a.y), pack2<T>(a.z, a.w));
+}
+
+template <typename T, int DP, bool KEYS>
+cudaError_t back_launch(const AttendParams& p, const BackMaps& m, int64_t grid, cudaStream_t s) {
+  using C = BackCfg<DP>;
+  auto kernel = attend_back_kernel<T, DP, KEYS>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kTotal);
+  if (e != cudaSuccess) return e;
+  kernel<<<(unsigned)grid, C::kThreads, C::kTotal, s>>>(p, m, spin_limit());
+  return cudaGetLastError();
+}
+
+template <typename T>
+recis_status back(const AttendParams& p, cudaStream_t s) {
+  constexpr bool bf16 = std::is_same<T, __nv_bfloat16>::value;
+  const int TQ = kX / p.G, gc = std::min(p.G, kY), tq = kY / gc;
+  const int64_t kgrid = (int64_t)p.B * p.Hkv * (((int64_t)p.max_k + kX - 1) / kX);
+  const int64_t qgrid = (int64_t)p.B * p.splits * p.Hkv * (((int64_t)p.max_q + TQ - 1) / TQ);
+  const int64_t dgrid = (p.Tq * p.Hq + 7) / 8, jgrid = (int64_t)p.B * (((int64_t)p.max_q * p.Hq + 3) / 4);
+  for (int64_t g : {kgrid, qgrid, dgrid, jgrid})
+    if (g >= ((int64_t)1 << 31)) {
+      set_error("attend_backward: too many blocks (bags times longest bag times heads)");
+      return RECIS_ERR_INVALID_ARG;
+    }
+  BackMaps mk = {}, mq = {};
+  bool ok = true;
+  // a map is made only where its array has rows; without rows no block uses it
+  if (p.Tq > 0)
+    ok = ok && rows_map(&mk.y1, p.q, bf16, p.D, p.Hq, p.Tq, p.qs, p.qh, gc, tq) &&
+         rows_map(&mk.y2, p.go, bf16, p.D, p.Hq, p.Tq, p.gos, p.goh, gc, tq) &&
+         rows_map(&mq.x1, p.q, bf16, p.D, p.Hq, p.Tq, p.qs, p.qh, p.G, TQ) &&
+         rows_map(&mq.x2, p.go, bf16, p.D, p.Hq, p.Tq, p.gos, p.goh, p.G, TQ);
+  if (p.Tk > 0)
+    ok = ok && rows_map(&mk.x1, p.k, bf16, p.D, p.Hkv, p.Tk, p.ks, p.kh, 1, kX) &&
+         rows_map(&mk.x2, p.v, bf16, p.D, p.Hkv, p.Tk, p.vs, p.vh, 1, kX) &&
+         rows_map(&mq.y1, p.k, bf16, p.D, p.Hkv, p.Tk, p.ks, p.kh, 1, kY) &&
+         rows_map(&mq.y2, p.v, bf16, p.D, p.Hkv, p.Tk, p.vs, p.vh, 1, kY);
+  if (!ok) {
+    set_error("attend_backward: the driver refused a tensor map");
+    return RECIS_ERR_CUDA;
+  }
+  cudaError_t e;
+  if (dgrid > 0) {
+    LaunchScope ls("attend_delta", s);
+    delta_kernel<T><<<(unsigned)dgrid, 256, 0, s>>>(p);
+    if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "attend_delta launch");
+  }
+  if (kgrid > 0) {
+    LaunchScope ls("attend_back_keys", s);
+    e = p.D <= 64 ? back_launch<T, 64, true>(p, mk, kgrid, s) : back_launch<T, 128, true>(p, mk, kgrid, s);
+    if (e != cudaSuccess) return cuda_fail(e, "attend_back_keys launch");
+  }
+  if (qgrid > 0) {
+    LaunchScope ls("attend_back_queries", s);
+    e = p.D <= 64 ? back_launch<T, 64, false>(p, mq, qgrid, s) : back_launch<T, 128, false>(p, mq, qgrid, s);
+    if (e != cudaSuccess) return cuda_fail(e, "attend_back_queries launch");
+    if (p.splits > 1) {
+      LaunchScope lj("attend_join_q", s);
+      join_q_kernel<T><<<(unsigned)jgrid, 128, 0, s>>>(p);
+      if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "attend_join_q launch");
+    }
+  }
+  return RECIS_OK;
+}
+
+}  // namespace
+
+recis_status launch_attend_back(const AttendParams& p, bool bf16, cudaStream_t s) {
+  return bf16 ? back<__nv_bfloat16>(p, s) : back<__half>(p, s);
+}
+
+}  // namespace recis
