@@ -11,6 +11,7 @@
 #include <type_traits>
 
 #include "attend.cuh"
+#include "tc.cuh"
 
 namespace recis {
 
@@ -36,23 +37,47 @@ __device__ __forceinline__ void mma16816<__half>(float (&c)[4], const uint32_t (
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-constexpr int kRowTile = kFewRows;  // rows (query, head of the group) a block of few_kernel takes
-constexpr int kFewWarps = 4;
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
 
-// One block: 16 rows of one key head against one part of the bag's keys; warp w
-// takes every fourth block of 16 keys with a softmax of its own, and the warps'
-// results are joined in shared memory.
-//
-// K and V go from global memory to the matrix instruction's registers without
-// shared memory: 16 bytes a thread.  The order of the contracted index of
-// q k^T is free as long as both operands agree, so a thread's 16 bytes of a key
-// row (8 consecutive d) serve as the k pairs of two m16n8k16 steps; for p v the
-// thread reads the key rows whose pairs it needs and interleaves two rows by
-// byte permutes, which makes output column n of tile j stand for d = 8 n + j.
-template <typename T, int DP>  // DP: D rounded up to 32, 64 or 128
-__global__ void __launch_bounds__(kFewWarps * 32) few_kernel(const __grid_constant__ AttendParams p) {
-  constexpr int KG = DP / 32, VE = (DP + 63) / 64;
-  __shared__ float s_o[kFewWarps][kRowTile][DP + 4];
+constexpr int kRowTile = kFewRows;  // rows (query, head of the group) a block of few_kernel takes
+constexpr int kFewWarps = 4;        // warps of products, 16 keys of a tile each
+constexpr int kFewKeys = 64;        // keys a tile
+
+template <int DP>
+struct FewCfg {
+  static constexpr int kBlocks = DP / 64;
+  static constexpr int kBytes = kBlocks * kFewKeys * 128;  // one tile of K or V
+  static constexpr int kStages = DP == 64 ? 4 : 3;         // 64 and 96 KB in flight: three and two blocks an SM
+  static constexpr int kTotal = 2 * kStages * kBytes + 1024 + 128;
+};
+
+// One block: 16 rows of one key head against one part of the bag's keys, bound
+// by reading K and V.  A fifth warp keeps tiles of 64 keys coming by
+// tensor-map copies, kStages deep; warp w takes 16 keys of each tile with a
+// softmax of its own (one m16n8k16 step of p v), and the warps' results are
+// joined in shared memory at the end, so the warps never wait for one another
+// in between.
+template <typename T, int DP>  // DP: D rounded up to 64 or 128
+__global__ void __launch_bounds__(kFewWarps * 32 + 32)
+    few_kernel(const __grid_constant__ AttendParams p, const __grid_constant__ CUtensorMap mk,
+               const __grid_constant__ CUtensorMap mv, int spin_max) {
+  using C = FewCfg<DP>;
+  constexpr int NS = C::kStages, LD = DP + 4;
+  extern __shared__ uint8_t s_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(s_raw) + 1023) & ~(uintptr_t)1023);
+  uint64_t* full = reinterpret_cast<uint64_t*>(base + 2 * NS * C::kBytes);
+  uint64_t* empty = full + NS;
   __shared__ float s_m[kFewWarps][kRowTile], s_l[kFewWarps][kRowTile];
   const int rtiles = (p.max_q * p.G + kRowTile - 1) / kRowTile;
   unsigned id = blockIdx.x;
@@ -65,185 +90,205 @@ __global__ void __launch_bounds__(kFewWarps * 32) few_kernel(const __grid_consta
   const int rows = bag.nq * p.G, r0 = rt * kRowTile;
   const int ks = sp * p.split_keys, ke = min(ks + p.split_keys, bag.nk);
   if (r0 >= rows || (ks >= bag.nk && sp > 0)) return;
+  const int n = ke > ks ? (ke - ks + kFewKeys - 1) / kFewKeys : 0;
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, g = lane >> 2, c = lane & 3;
-  const T* kp = static_cast<const T*>(p.k) + bag.k0 * p.ks + h * p.kh;
-  const T* vp = static_cast<const T*>(p.v) + bag.k0 * p.vs + h * p.vh;
-  const uint8_t* mp = p.mask ? p.mask + bag.k0 : nullptr;
-
-  uint4 qa[KG], qb[KG];  // rows g and g + 8
-  {
-    const int ra = r0 + g, rb = ra + 8;
-#pragma unroll
-    for (int i = 0; i < KG; ++i) {
-      const int d = 32 * i + 8 * c;
-      qa[i] = qb[i] = make_uint4(0, 0, 0, 0);
-      if (d < p.D && ra < rows)
-        qa[i] = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + (bag.q0 + ra / p.G) * p.qs +
-                                                (h * p.G + ra % p.G) * p.qh + d);
-      if (d < p.D && rb < rows)
-        qb[i] = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + (bag.q0 + rb / p.G) * p.qs +
-                                                (h * p.G + rb % p.G) * p.qh + d);
+  if (tid == kFewWarps * 32) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(full + i, 1);
+      mbar_init(empty + i, kFewWarps);
     }
-  }
-  float o[VE][8][4];
-#pragma unroll
-  for (int e = 0; e < VE; ++e)
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) o[e][j][i] = 0.f;
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-
-  uint4 kf[2][KG], vf[4][VE];
-  auto valid = [&](int key) { return key < ke && (!mp || mp[key]); };
-  auto load_k = [&](int kb) {
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const int key = kb + t * 8 + g;
-      const bool ok = valid(key);
-#pragma unroll
-      for (int i = 0; i < KG; ++i) {
-        const int d = 32 * i + 8 * c;
-        kf[t][i] = make_uint4(0, 0, 0, 0);
-        if (ok && d < p.D) kf[t][i] = __ldg(reinterpret_cast<const uint4*>(kp + (int64_t)key * p.ks + d));
-      }
-    }
-  };
-  auto load_v = [&](int kb) {
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const int key = kb + 2 * c + (t & 1) + (t >> 1) * 8;
-      const bool ok = valid(key);
-#pragma unroll
-      for (int e = 0; e < VE; ++e) {
-        const int d = 64 * e + 8 * g;
-        vf[t][e] = make_uint4(0, 0, 0, 0);
-        if (ok && d < p.D) vf[t][e] = __ldg(reinterpret_cast<const uint4*>(vp + (int64_t)key * p.vs + d));
-      }
-    }
-  };
-  int kb = ks + w * 16;
-  if (kb < ke) load_k(kb);
-  for (; kb < ke; kb += kFewWarps * 16) {
-    load_v(kb);
-    float s[2][4];
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s[t][i] = 0.f;
-#pragma unroll
-      for (int i = 0; i < KG; ++i) {
-        const uint32_t a0[4] = {qa[i].x, qb[i].x, qa[i].y, qb[i].y}, a1[4] = {qa[i].z, qb[i].z, qa[i].w, qb[i].w};
-        mma16816<T>(s[t], a0, kf[t][i].x, kf[t][i].y);
-        mma16816<T>(s[t], a1, kf[t][i].z, kf[t][i].w);
-      }
-    }
-    bool ok[2][2];
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) ok[t][i] = valid(kb + t * 8 + 2 * c + i);
-    if (kb + kFewWarps * 16 < ke) load_k(kb + kFewWarps * 16);
-    float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        s[t][i] = ok[t][i & 1] ? s[t][i] * p.scale_log2 : -INFINITY;
-        mx[i >> 1] = fmaxf(mx[i >> 1], s[t][i]);
-      }
-    float corr[2];
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
-      mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
-      const float mn = fmaxf(m[r], mx[r]);
-      const float base = mn == -INFINITY ? 0.f : mn;
-      corr[r] = exp2f(m[r] - base);
-      m[r] = mn;
-      mx[r] = base;
-      l[r] *= corr[r];
-    }
-    uint32_t pa[4];
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        s[t][i] = exp2f(s[t][i] - mx[i >> 1]);
-        l[i >> 1] += s[t][i];
-      }
-      pa[t * 2] = pack2<T>(s[t][0], s[t][1]);
-      pa[t * 2 + 1] = pack2<T>(s[t][2], s[t][3]);
-    }
-#pragma unroll
-    for (int e = 0; e < VE; ++e) {
-      const uint32_t* v0 = reinterpret_cast<const uint32_t*>(&vf[0][e]);
-      const uint32_t* v1 = reinterpret_cast<const uint32_t*>(&vf[1][e]);
-      const uint32_t* v2 = reinterpret_cast<const uint32_t*>(&vf[2][e]);
-      const uint32_t* v3 = reinterpret_cast<const uint32_t*>(&vf[3][e]);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const unsigned sel = (j & 1) ? 0x7632 : 0x5410;
-        o[e][j][0] *= corr[0];
-        o[e][j][1] *= corr[0];
-        o[e][j][2] *= corr[1];
-        o[e][j][3] *= corr[1];
-        mma16816<T>(o[e][j], pa, __byte_perm(v0[j >> 1], v1[j >> 1], sel), __byte_perm(v2[j >> 1], v3[j >> 1], sel));
-      }
-    }
-  }
-#pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-    if (c == 0) {
-      s_m[w][g + 8 * r] = m[r];
-      s_l[w][g + 8 * r] = l[r];
-    }
-#pragma unroll
-    for (int e = 0; e < VE; ++e)
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int d = 64 * e + 16 * c + 8 * i + j;
-          if (d < DP) s_o[w][g + 8 * r][d] = o[e][j][2 * r + i];
-        }
   }
   __syncthreads();
-  // join the warps: 8 threads a row, each every eighth group of 8 columns
-  const int row = tid >> 3, r = r0 + row;
-  if (r >= rows) return;
-  float mm = s_m[0][row];
-#pragma unroll
-  for (int q = 1; q < kFewWarps; ++q) mm = fmaxf(mm, s_m[q][row]);
-  const float base = mm == -INFINITY ? 0.f : mm;
-  float f[kFewWarps], ll = 0.f;
-#pragma unroll
-  for (int q = 0; q < kFewWarps; ++q) {
-    f[q] = exp2f(s_m[q][row] - base);
-    ll = fmaf(s_l[q][row], f[q], ll);
-  }
-  const float inv = ll > 0.f ? 1.0f / ll : (ll == 0.f ? 0.f : ll);
-  const float lse = ll == 0.f ? -INFINITY : (base + log2f(ll)) * 0.6931471805599453f;
-  const int64_t t = bag.q0 + r / p.G;
-  const int hq = h * p.G + r % p.G;
-  for (int d = (tid & 7) * 8; d < p.D; d += 64) {
-    float v[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      v[j] = 0.f;
-#pragma unroll
-      for (int q = 0; q < kFewWarps; ++q) v[j] = fmaf(s_o[q][row][d + j], f[q], v[j]);
-      v[j] *= inv;
+  bool ok = true;  // false: a wait gave up
+  if (w == kFewWarps) {
+    if (lane == 0) {
+      int asked = 0;
+      for (int j = 0; j < n; ++j) {
+        const int st = j % NS;
+        if (j >= NS && !(ok = mbar_wait(empty + st, ((j / NS) & 1) ^ 1, spin_max))) break;
+        mbar_arrive_expect(full + st, 2 * C::kBytes);
+        const int row = (int)(bag.k0 + ks + j * kFewKeys);
+        for (int i = 0; i < C::kBlocks; ++i) {
+          tma_load3(base + 2 * st * C::kBytes + i * kFewKeys * 128, &mk, 64 * i, h, row, full + st);
+          tma_load3(base + (2 * st + 1) * C::kBytes + i * kFewKeys * 128, &mv, 64 * i, h, row, full + st);
+        }
+        asked = j + 1;
+      }
+      // copies in flight end before the block does
+      for (int j = max(asked - NS, 0); j < asked; ++j) ok = mbar_wait(full + j % NS, (j / NS) & 1, spin_max) && ok;
     }
-    if (p.splits == 1) store_vec(static_cast<T*>(p.out) + t * p.os + hq * p.oh + d, v);
-    else store_vec(p.po + (((int64_t)sp * p.Tq + t) * p.Hq + hq) * p.D + d, v);
+  } else {
+    uint32_t qa[DP / 16][4];
+#pragma unroll
+    for (int i = 0; i < DP / 16; ++i)
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int r = r0 + g + 8 * (u & 1), d = 16 * i + 2 * c + 8 * (u >> 1);
+        qa[i][u] = 0;
+        if (d < p.D && r < rows)
+          qa[i][u] = *reinterpret_cast<const uint32_t*>(static_cast<const T*>(p.q) + (bag.q0 + r / p.G) * p.qs +
+                                                        (h * p.G + r % p.G) * p.qh + d);
+      }
+    float o[DP / 8][4];
+#pragma unroll
+    for (int j = 0; j < DP / 8; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[j][i] = 0.f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    // the lane's rows of K and V for the matrix loads, and its swizzle
+    const int krow = w * 16 + (lane >> 4) * 8 + (lane & 7), vrow = w * 16 + ((lane >> 3) & 1) * 8 + (lane & 7);
+    const int kch = (lane >> 3) & 1, vch = lane >> 4, sw = lane & 7;
+    for (int j = 0; j < n; ++j) {
+      const int st = j % NS, k0 = ks + j * kFewKeys + w * 16;  // the warp's first key
+      ok = mbar_wait(full + st, (j / NS) & 1, spin_max);
+      if (!__all_sync(0xffffffffu, ok)) {
+        ok = false;
+        break;
+      }
+      const uint32_t ak = smem_u32(base + 2 * st * C::kBytes) + krow * 128;
+      const uint32_t av = smem_u32(base + (2 * st + 1) * C::kBytes) + vrow * 128;
+      float s[2][4];
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[t][i] = 0.f;
+#pragma unroll
+      for (int i = 0; i < DP / 16; ++i) {
+        uint32_t kf[4];
+        ldsm4(kf, ak + (i >> 2) * kFewKeys * 128 + ((((i & 3) * 2 + kch) ^ sw) << 4));
+        mma16816<T>(s[0], qa[i], kf[0], kf[1]);
+        mma16816<T>(s[1], qa[i], kf[2], kf[3]);
+      }
+      if (k0 + 16 > ke || p.mask) {
+        // keys that take no part: their scores -inf, their rows of V zeros (0 * NaN is NaN)
+        const int key = k0 + (lane & 15);
+        const bool v = key < ke && (!p.mask || p.mask[bag.k0 + key]);
+        const unsigned bits = __ballot_sync(0xffffffffu, v);
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (!(bits >> (t * 8 + 2 * c + (i & 1)) & 1)) s[t][i] = -INFINITY;
+            else s[t][i] *= p.scale_log2;
+        if (!v && lane < 16)
+          for (int i = 0; i < C::kBlocks; ++i) {
+            uint4* row = reinterpret_cast<uint4*>(base + (2 * st + 1) * C::kBytes + (i * kFewKeys + w * 16 + lane) * 128);
+#pragma unroll
+            for (int u = 0; u < 8; ++u) row[u] = make_uint4(0, 0, 0, 0);
+          }
+        fence_async_smem();
+        __syncwarp();
+      } else {
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[t][i] *= p.scale_log2;
+      }
+      float mx[2] = {fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1])),
+                     fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]))};
+      float corr[2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
+        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
+        const float mn = fmaxf(m[r], mx[r]);
+        mx[r] = mn == -INFINITY ? 0.f : mn;
+        corr[r] = ex2(m[r] - mx[r]);
+        m[r] = mn;
+        l[r] *= corr[r];
+      }
+      uint32_t pa[4];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          s[t][i] = ex2(s[t][i] - mx[i >> 1]);
+          l[i >> 1] += s[t][i];
+        }
+        pa[t * 2] = pack2<T>(s[t][0], s[t][1]);
+        pa[t * 2 + 1] = pack2<T>(s[t][2], s[t][3]);
+      }
+      if (__any_sync(0xffffffffu, corr[0] != 1.f || corr[1] != 1.f)) {
+#pragma unroll
+        for (int i = 0; i < DP / 8; ++i) {
+          o[i][0] *= corr[0];
+          o[i][1] *= corr[0];
+          o[i][2] *= corr[1];
+          o[i][3] *= corr[1];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < DP / 16; ++i) {
+        uint32_t vf[4];
+        ldsm4t(vf, av + (i >> 2) * kFewKeys * 128 + ((((i & 3) * 2 + vch) ^ sw) << 4));
+        mma16816<T>(o[2 * i], pa, vf[0], vf[1]);
+        mma16816<T>(o[2 * i + 1], pa, vf[2], vf[3]);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty + st);
+    }
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+      if (c == 0) {
+        s_m[w][g + 8 * r] = m[r];
+        s_l[w][g + 8 * r] = l[r];
+      }
+    }
+    // every tile was waited for by every warp before it passes this barrier,
+    // so the tiles' memory takes the warps' results
+    asm volatile("bar.sync 1, %0;" ::"n"(kFewWarps * 32) : "memory");
+    float* s_o = reinterpret_cast<float*>(base);
+#pragma unroll
+    for (int i = 0; i < DP / 8; ++i)
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+        *reinterpret_cast<float2*>(s_o + (w * kRowTile + g + 8 * r) * LD + 8 * i + 2 * c) =
+            make_float2(o[i][2 * r], o[i][2 * r + 1]);
+    asm volatile("bar.sync 1, %0;" ::"n"(kFewWarps * 32) : "memory");
+    // join the warps: 8 threads a row, each every eighth group of 8 columns
+    const int row = tid >> 3, r = r0 + row;
+    if (r < rows) {
+      float mm = s_m[0][row];
+#pragma unroll
+      for (int q = 1; q < kFewWarps; ++q) mm = fmaxf(mm, s_m[q][row]);
+      const float mb = mm == -INFINITY ? 0.f : mm;
+      float f[kFewWarps], ll = 0.f;
+#pragma unroll
+      for (int q = 0; q < kFewWarps; ++q) {
+        f[q] = ex2(s_m[q][row] - mb);
+        ll = fmaf(s_l[q][row], f[q], ll);
+      }
+      const float inv = ll == 0.f ? 0.f : 1.0f / ll;
+      const float lse = ll == 0.f ? -INFINITY : (mb + log2f(ll)) * 0.6931471805599453f;
+      const int64_t t = bag.q0 + r / p.G;
+      const int hq = h * p.G + r % p.G;
+      for (int d = (tid & 7) * 8; d < p.D; d += 64) {
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = 0.f;
+#pragma unroll
+        for (int q = 0; q < kFewWarps; ++q) {
+          RawVec<float, 8> raw;
+          raw.load(s_o + (q * kRowTile + row) * LD + d);
+          float x[8];
+          raw.unpack(x);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j] = fmaf(x[j], f[q], v[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] *= inv;
+        if (p.splits == 1) store_vec(static_cast<T*>(p.out) + t * p.os + hq * p.oh + d, v);
+        else store_vec(p.po + (((int64_t)sp * p.Tq + t) * p.Hq + hq) * p.D + d, v);
+      }
+      if ((tid & 7) == 0) {
+        if (p.splits == 1) p.lse[t * p.Hq + hq] = lse;
+        else p.pl[((int64_t)sp * p.Tq + t) * p.Hq + hq] = lse;
+      }
+    }
   }
-  if ((tid & 7) == 0) {
-    if (p.splits == 1) p.lse[t * p.Hq + hq] = lse;
-    else p.pl[((int64_t)sp * p.Tq + t) * p.Hq + hq] = lse;
-  }
+  if (!ok) atomicOr(p.status, kErrTimeout);
 }
 
 // Joins the parts of the keys: out = sum_s exp(lse_s - lse) out_s; one warp a
@@ -298,10 +343,15 @@ AttendPlan attend_plan(const recis_attend_args& a, bool backward) {
   g.splits = 1;
   g.split_keys = (int)std::max<int64_t>(a.max_k, 1);
   if (backward) {
-    g.delta_bytes = align256(a.Tq * a.Hq * 4);
-    // parts of the keys for grad_q, as in the forward: two blocks an SM, 512 keys a part
-    const int64_t TQ = 128 / (a.Hq / a.Hkv), blocks = std::max<int64_t>(1, a.B * a.Hkv * ((a.max_q + TQ - 1) / TQ));
-    const int64_t want = std::min<int64_t>((kSMs * 2 + blocks - 1) / blocks, (a.max_k + 511) / 512);
+    // parts of the keys for grad_q.  Few rows: the keys' pass makes it, three
+    // rounds of blocks on every SM even out the bags' lengths; many: a pass
+    // over query tiles of its own, two blocks an SM.  At least 512 keys a part.
+    const int64_t G = a.Hq / a.Hkv, rows = a.max_q * G;
+    const bool few = rows <= kFewBackRows;
+    if (!few) g.delta_bytes = align256(a.Tq * a.Hq * 4);
+    const int64_t blocks = std::max<int64_t>(1, a.B * a.Hkv * (few ? 1 : (a.max_q + 128 / G - 1) / (128 / G)));
+    const int64_t target = kSMs * (few ? 3 * few_back_per_sm(a.D, rows) : 2);
+    const int64_t want = std::min<int64_t>((target + blocks - 1) / blocks, (a.max_k + 511) / 512);
     if (want > 1) {
       g.split_keys = (int)((a.max_k + want - 1) / want + 127) / 128 * 128;
       g.splits = (int)((a.max_k + g.split_keys - 1) / g.split_keys);
@@ -382,6 +432,16 @@ recis_status fill(const recis_attend_args* a, AttendParams* p, const AttendPlan&
   return RECIS_OK;
 }
 
+template <typename T, int DP>
+cudaError_t few_launch(const AttendParams& p, const CUtensorMap& mk, const CUtensorMap& mv, int64_t grid,
+                       cudaStream_t s) {
+  auto kernel = few_kernel<T, DP>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, FewCfg<DP>::kTotal);
+  if (e != cudaSuccess) return e;
+  kernel<<<(unsigned)grid, kFewWarps * 32 + 32, FewCfg<DP>::kTotal, s>>>(p, mk, mv, spin_limit());
+  return cudaGetLastError();
+}
+
 template <typename T>
 recis_status forward(const AttendParams& p, cudaStream_t s) {
   const bool few = p.max_q * p.G <= kFewRows;
@@ -396,12 +456,17 @@ recis_status forward(const AttendParams& p, cudaStream_t s) {
     if (st != RECIS_OK) return st;
   } else {
     LaunchScope ls("attend_few", s);
-    if (p.D <= 32) few_kernel<T, 32><<<(unsigned)grid, kFewWarps * 32, 0, s>>>(p);
-    else if (p.D <= 64) few_kernel<T, 64><<<(unsigned)grid, kFewWarps * 32, 0, s>>>(p);
-    else few_kernel<T, 128><<<(unsigned)grid, kFewWarps * 32, 0, s>>>(p);
+    constexpr bool bf16 = std::is_same<T, __nv_bfloat16>::value;
+    CUtensorMap mk = {}, mv = {};
+    if (p.Tk > 0 && (!rows_map(&mk, p.k, bf16, p.D, p.Hkv, p.Tk, p.ks, p.kh, 1, kFewKeys) ||
+                     !rows_map(&mv, p.v, bf16, p.D, p.Hkv, p.Tk, p.vs, p.vh, 1, kFewKeys))) {
+      set_error("attend: the driver refused a tensor map");
+      return RECIS_ERR_CUDA;
+    }
+    const cudaError_t e = p.D <= 64 ? few_launch<T, 64>(p, mk, mv, grid, s) : few_launch<T, 128>(p, mk, mv, grid, s);
+    if (e != cudaSuccess) return cuda_fail(e, "attend launch");
   }
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return cuda_fail(e, "attend launch");
+  cudaError_t e;
   if (p.splits > 1) {
     LaunchScope ls("attend_join", s);
     join_kernel<T><<<(unsigned)jgrid, 128, 0, s>>>(p);

@@ -44,6 +44,11 @@ __device__ __forceinline__ Bag load_bag(const AttendParams& p, int b) {
 
 // more rows (queries times heads of a group) than this in a bag: tensor-core tiles
 constexpr int kFewRows = 16;
+// at most this many rows in a bag: the backward takes them all at once, in one pass over the keys
+constexpr int kFewBackRows = 64;
+// blocks of that pass an SM holds
+inline int few_back_per_sm(int D, int64_t rows) { return D <= 64 && rows <= 32 ? 2 : 1; }
+recis_status launch_attend_back_few(const AttendParams& p, bool bf16, cudaStream_t s);
 recis_status launch_attend_tc(const AttendParams& p, bool bf16, cudaStream_t s);
 recis_status launch_attend_back(const AttendParams& p, bool bf16, cudaStream_t s);
 

@@ -413,14 +413,33 @@ cudaError_t back_launch(const AttendParams& p, const BackMaps& m, int64_t grid, 
   return cudaGetLastError();
 }
 
+// joins the parts of grad_q
+template <typename T>
+recis_status join_q(const AttendParams& p, cudaStream_t s) {
+  if (p.splits == 1 || p.Tq == 0) return RECIS_OK;
+  const int64_t grid = (int64_t)p.B * (((int64_t)p.max_q * p.Hq + 3) / 4);
+  if (grid >= ((int64_t)1 << 31)) {
+    set_error("attend_backward: too many blocks (bags times longest bag times heads)");
+    return RECIS_ERR_INVALID_ARG;
+  }
+  LaunchScope ls("attend_join_q", s);
+  join_q_kernel<T><<<(unsigned)grid, 128, 0, s>>>(p);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? RECIS_OK : cuda_fail(e, "attend_join_q launch");
+}
+
 template <typename T>
 recis_status back(const AttendParams& p, cudaStream_t s) {
   constexpr bool bf16 = std::is_same<T, __nv_bfloat16>::value;
+  if (p.max_q * p.G <= kFewBackRows) {
+    const recis_status st = launch_attend_back_few(p, bf16, s);
+    return st == RECIS_OK ? join_q<T>(p, s) : st;
+  }
   const int TQ = kX / p.G, gc = std::min(p.G, kY), tq = kY / gc;
   const int64_t kgrid = (int64_t)p.B * p.Hkv * (((int64_t)p.max_k + kX - 1) / kX);
   const int64_t qgrid = (int64_t)p.B * p.splits * p.Hkv * (((int64_t)p.max_q + TQ - 1) / TQ);
-  const int64_t dgrid = (p.Tq * p.Hq + 7) / 8, jgrid = (int64_t)p.B * (((int64_t)p.max_q * p.Hq + 3) / 4);
-  for (int64_t g : {kgrid, qgrid, dgrid, jgrid})
+  const int64_t dgrid = (p.Tq * p.Hq + 7) / 8;
+  for (int64_t g : {kgrid, qgrid, dgrid})
     if (g >= ((int64_t)1 << 31)) {
       set_error("attend_backward: too many blocks (bags times longest bag times heads)");
       return RECIS_ERR_INVALID_ARG;
@@ -457,13 +476,8 @@ recis_status back(const AttendParams& p, cudaStream_t s) {
     LaunchScope ls("attend_back_queries", s);
     e = p.D <= 64 ? back_launch<T, 64, false>(p, mq, qgrid, s) : back_launch<T, 128, false>(p, mq, qgrid, s);
     if (e != cudaSuccess) return cuda_fail(e, "attend_back_queries launch");
-    if (p.splits > 1) {
-      LaunchScope lj("attend_join_q", s);
-      join_q_kernel<T><<<(unsigned)jgrid, 128, 0, s>>>(p);
-      if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "attend_join_q launch");
-    }
   }
-  return RECIS_OK;
+  return join_q<T>(p, s);
 }
 
 }  // namespace

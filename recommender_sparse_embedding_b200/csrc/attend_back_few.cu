@@ -1,0 +1,377 @@
+// attend_back_few.cu -- attention backward when a bag has few query rows
+// (queries times heads of a group <= 64): one pass over the keys.
+//
+//   p = exp(s - lse), dp = dO V^T, ds = p (dp - delta), delta = sum(dO * O),
+//   dV = p^T dO,  dK = scale ds^T Q,  dQ = scale ds K.
+//
+// With all the bag's rows in one tile, a key tile's dK and dV need no sum over
+// query tiles, and the scores are computed once: K and V are read once, dK and
+// dV written once, which is what bounds this pass.  A block takes the rows of
+// one key head and a part of the bag's keys, 128 keys a step:
+//
+//   S^T = K Q^T, dP^T = V dO^T      (128 keys x NR rows, tensor memory)
+//   P^T, dS^T as 16-bit values over them; dS also to shared memory
+//   dV = P^T dO, dK = dS^T Q        (128 keys x D), stored
+//   dQ += dS K                      (NR rows x D, kept in tensor memory)
+//
+// While the compute warps store dV and dK of one tile, the scores of the next
+// are made; the copies run further ahead.  Parts of dQ (several blocks a bag)
+// are joined in order by join_q_kernel.
+#include <algorithm>
+#include <type_traits>
+
+#include "attend.cuh"
+#include "tc.cuh"
+
+namespace recis {
+
+namespace {
+
+constexpr int kKeys = 128;
+constexpr int kCompute = 256;
+constexpr int kThreads = kCompute + 64;
+
+template <int DP, int NR>
+struct FewBackCfg {
+  static constexpr bool kTwo = DP == 64 && NR <= 32;   // two blocks an SM
+  static constexpr int kBlocks = DP / 64;
+  static constexpr int kTile = kBlocks * kKeys * 128;  // K or V
+  static constexpr int kRows = kBlocks * NR * 128;     // Q or dO
+  static constexpr int kStages = DP == 64 && !kTwo ? 4 : 2;
+  static constexpr uint32_t kDp = kTwo ? 32 : 64, kDv = 2 * kDp, kDk = kDv + DP, kDq = kDk + DP;
+  static constexpr uint32_t kCols = kTwo ? 256 : 512;
+  // K and V stages, dS [128 rows][128 keys], Q, dO, alignment, barriers, lse, delta
+  static constexpr int kTotal = 2 * kStages * kTile + 2 * 16384 + 2 * kRows + 1024 + 128 + 2 * NR * 4;
+};
+
+template <typename T, int DP, int NR>
+__global__ void __launch_bounds__(kThreads, FewBackCfg<DP, NR>::kTwo ? 2 : 1)
+    attend_back_few_kernel(const __grid_constant__ AttendParams p, const __grid_constant__ CUtensorMap mq,
+                           const __grid_constant__ CUtensorMap mo, const __grid_constant__ CUtensorMap mk,
+                           const __grid_constant__ CUtensorMap mv, int spin_max) {
+  using C = FewBackCfg<DP, NR>;
+  constexpr int NS = C::kStages, H = NR / 2;  // H: columns a compute warpgroup takes
+  extern __shared__ uint8_t s_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(s_raw) + 1023) & ~(uintptr_t)1023);
+  uint8_t *skv = base, *sds = skv + 2 * NS * C::kTile, *sq = sds + 2 * 16384, *so = sq + C::kRows;
+  uint64_t* bar = reinterpret_cast<uint64_t*>(so + C::kRows);
+  uint64_t *q_raw = bar, *q_full = bar + 1, *s_full = bar + 2, *e_full = bar + 3, *o_full = bar + 4;
+  uint64_t *kv_full = bar + 5, *kv_empty = kv_full + NS;
+  float* s_lse = reinterpret_cast<float*>(so + C::kRows + 128);  // [NR] lse * log2(e)
+  float* s_delta = s_lse + NR;
+  __shared__ uint32_t s_tmem;
+
+  unsigned id = blockIdx.x;
+  const int h = id % p.Hkv;
+  id /= p.Hkv;
+  const int sp = id % p.splits, b = id / p.splits;
+  const Bag bag = load_bag(p, b);
+  const int rows = bag.nq * p.G;  // <= NR
+  const int ks = sp * p.split_keys, ke = min(ks + p.split_keys, bag.nk);
+  if (sp > 0 && ks >= bag.nk) return;
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  if (rows == 0) {  // keys without queries: zero gradients
+    const int per = p.D / 8;
+    for (int i = tid; i < (ke - ks) * per; i += kThreads) {
+      const int64_t t = bag.k0 + ks + i / per;
+      const int d = i % per * 8;
+      *reinterpret_cast<uint4*>(static_cast<T*>(p.gk) + t * p.gks + h * p.gkh + d) = make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4*>(static_cast<T*>(p.gv) + t * p.gvs + h * p.gvh + d) = make_uint4(0, 0, 0, 0);
+    }
+    return;
+  }
+  const int n = ke > ks ? (ke - ks + kKeys - 1) / kKeys : 0;
+
+  constexpr int kLoader = kCompute / 32, kIssuer = kLoader + 1;
+  if (w == kIssuer) tmem_alloc(&s_tmem, C::kCols);
+  if (tid == kLoader * 32) {
+    mbar_init(q_raw, 1);
+    mbar_init(q_full, 1);
+    mbar_init(s_full, 1);
+    mbar_init(e_full, kCompute);
+    mbar_init(o_full, 1);
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(kv_full + i, 1);
+      mbar_init(kv_empty + i, 1);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  bool ok = true;  // false: a wait gave up
+
+  if (w == kLoader) {
+    if (n > 0) {
+      int asked = 0;
+      auto ask = [&](int j) {
+        const int st = j % NS, row = (int)(bag.k0 + ks + j * kKeys);
+        uint8_t* at = skv + 2 * st * C::kTile;
+        mbar_arrive_expect(kv_full + st, 2 * C::kTile);
+        for (int i = 0; i < C::kBlocks; ++i) {
+          tma_load3(at + i * kKeys * 128, &mk, 64 * i, h, row, kv_full + st);
+          tma_load3(at + C::kTile + i * kKeys * 128, &mv, 64 * i, h, row, kv_full + st);
+        }
+        asked = j + 1;
+      };
+      if (lane == 0) {
+        mbar_arrive_expect(q_raw, (unsigned)(2 * C::kBlocks * p.max_q * p.G * 128));
+        for (int i = 0; i < C::kBlocks; ++i) {
+          tma_load3(sq + i * NR * 128, &mq, 64 * i, h * p.G, (int)bag.q0, q_raw);
+          tma_load3(so + i * NR * 128, &mo, 64 * i, h * p.G, (int)bag.q0, q_raw);
+        }
+        for (int j = 0; j < min(n, NS); ++j) ask(j);
+      }
+      ok = mbar_wait(q_raw, 0, spin_max);
+      for (int r = rows + lane; r < NR; r += 32)  // rows of other bags, or of none
+        for (int i = 0; i < C::kBlocks; ++i)
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            reinterpret_cast<uint4*>(sq + (i * NR + r) * 128)[u] = make_uint4(0, 0, 0, 0);
+            reinterpret_cast<uint4*>(so + (i * NR + r) * 128)[u] = make_uint4(0, 0, 0, 0);
+          }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(q_full);
+        for (int j = NS; j < n && ok; ++j) {
+          if (!(ok = mbar_wait(kv_empty + j % NS, ((j / NS) & 1) ^ 1, spin_max))) break;
+          ask(j);
+        }
+        // copies in flight end before the block does
+        for (int j = max(asked - NS, 0); j < asked; ++j) ok = mbar_wait(kv_full + j % NS, (j / NS) & 1, spin_max) && ok;
+      }
+      __syncwarp();
+    }
+  } else if (w == kIssuer) {
+    if (lane == 0 && n > 0) {
+      constexpr uint32_t id_s = mma_desc<T>(kKeys, NR, false, false), id_o = mma_desc<T>(kKeys, DP, false, true);
+      const uint32_t aq = smem_u32(sq), ao = smem_u32(so), ads = smem_u32(sds), akv = smem_u32(skv);
+      auto scores = [&](int j) {
+        const int st = j % NS;
+        if (!mbar_wait(kv_full + st, (j / NS) & 1, spin_max)) return false;
+        tc_fence_after();
+        const uint32_t ak = akv + 2 * st * C::kTile, av = ak + C::kTile;
+#pragma unroll
+        for (int k = 0; k < DP / 16; ++k) {
+          const uint32_t xo = (k >> 2) * kKeys * 128 + (k & 3) * 32, yo = (k >> 2) * NR * 128 + (k & 3) * 32;
+          mma_ss(tmem, smem_desc(ak + xo, 16), smem_desc(aq + yo, 16), id_s, k > 0);
+        }
+#pragma unroll
+        for (int k = 0; k < DP / 16; ++k) {
+          const uint32_t xo = (k >> 2) * kKeys * 128 + (k & 3) * 32, yo = (k >> 2) * NR * 128 + (k & 3) * 32;
+          mma_ss(tmem + C::kDp, smem_desc(av + xo, 16), smem_desc(ao + yo, 16), id_s, k > 0);
+        }
+        mma_commit(s_full);
+        return true;
+      };
+      ok = mbar_wait(q_full, 0, spin_max) && scores(0);
+      for (int j = 0; j < n && ok; ++j) {
+        const uint32_t ak = akv + 2 * (j % NS) * C::kTile;
+        if (!(ok = mbar_wait(e_full, j & 1, spin_max))) break;
+        tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < NR / 16; ++k)
+          mma_ts(tmem + C::kDv, tmem + 8 * k, smem_desc(ao + k * 2048, NR * 128), id_o, k > 0);
+#pragma unroll
+        for (int k = 0; k < NR / 16; ++k)
+          mma_ts(tmem + C::kDk, tmem + C::kDp + 8 * k, smem_desc(aq + k * 2048, NR * 128), id_o, k > 0);
+#pragma unroll
+        for (int k = 0; k < kKeys / 16; ++k)
+          mma_ss(tmem + C::kDq, smem_desc(ads + (k >> 2) * 16384 + (k & 3) * 32, 16),
+                 smem_desc(ak + k * 2048, kKeys * 128), id_o, j > 0 || k > 0);
+        mma_commit(o_full);
+        mma_commit(kv_empty + j % NS);
+        if (j + 1 < n) ok = scores(j + 1);
+      }
+    }
+    __syncwarp();
+  } else {
+    const int wg = w >> 2, key = tid & 127;
+    const uint32_t mine = tmem + ((uint32_t)(w & 3) << 21);
+    // the rows' lse and delta
+    for (int r = w; r < NR; r += kCompute / 32) {
+      float lse = INFINITY, s = 0.f;
+      if (r < rows) {
+        const int64_t t = bag.q0 + r / p.G;
+        const int hq = h * p.G + r % p.G, d = lane * 4;
+        if (d < p.D) {
+          const uint2 x = *reinterpret_cast<const uint2*>(static_cast<const T*>(p.out) + t * p.os + hq * p.oh + d);
+          const uint2 y = *reinterpret_cast<const uint2*>(static_cast<const T*>(p.go) + t * p.gos + hq * p.goh + d);
+          const float2 x0 = unpack2<T>(x.x), x1 = unpack2<T>(x.y), y0 = unpack2<T>(y.x), y1 = unpack2<T>(y.y);
+          s = x0.x * y0.x + x0.y * y0.y + x1.x * y1.x + x1.y * y1.y;
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+        lse = p.lse[t * p.Hq + hq] * 1.4426950408889634f;
+        if (lse == -INFINITY) lse = INFINITY;  // a row without keys: p = 0
+      }
+      if (lane == 0) {
+        s_lse[r] = lse;
+        s_delta[r] = s;
+      }
+    }
+    asm volatile("bar.sync 5, 256;" ::: "memory");
+    const float c = p.scale_log2;
+    // where the thread's key lies in dS's rows: its 16-byte chunk is swizzled by the row
+    uint8_t* ds_at = sds + (key >> 6) * 16384 + (key & 7) * 2;
+    const int chunk = (key & 63) >> 3;
+    for (int j = 0; j < n; ++j) {
+      const int k0 = ks + j * kKeys;
+      const int64_t t = bag.k0 + k0 + key;
+      const bool in = k0 + key < ke, takes = in && (!p.mask || p.mask[t]);
+      ok = mbar_wait(s_full, j & 1, spin_max);
+      if (!__all_sync(0xffffffffu, ok)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      uint32_t s[H], d[H], pk[H / 2], dk[H / 2];
+      tmem_ld(mine + wg * H, s);
+      tmem_ld(mine + C::kDp + wg * H, d);
+      tmem_wait_ld();
+      // both warps of these lanes have read: P and dS go over S and dP
+      asm volatile("bar.sync %0, 64;" ::"r"(1 + (w & 3)) : "memory");
+#pragma unroll
+      for (int i = 0; i < H; i += 4) {
+        const float4 ls = *reinterpret_cast<const float4*>(s_lse + wg * H + i);
+        const float4 de = *reinterpret_cast<const float4*>(s_delta + wg * H + i);
+        float e[4], f[4];
+        e[0] = ex2(fmaf(__uint_as_float(s[i]), c, -ls.x));
+        e[1] = ex2(fmaf(__uint_as_float(s[i + 1]), c, -ls.y));
+        e[2] = ex2(fmaf(__uint_as_float(s[i + 2]), c, -ls.z));
+        e[3] = ex2(fmaf(__uint_as_float(s[i + 3]), c, -ls.w));
+        f[0] = takes ? e[0] * (__uint_as_float(d[i]) - de.x) : 0.f;
+        f[1] = takes ? e[1] * (__uint_as_float(d[i + 1]) - de.y) : 0.f;
+        f[2] = takes ? e[2] * (__uint_as_float(d[i + 2]) - de.z) : 0.f;
+        f[3] = takes ? e[3] * (__uint_as_float(d[i + 3]) - de.w) : 0.f;
+        pk[i / 2] = pack2<T>(e[0], e[1]);
+        pk[i / 2 + 1] = pack2<T>(e[2], e[3]);
+        dk[i / 2] = pack2<T>(f[0], f[1]);
+        dk[i / 2 + 1] = pack2<T>(f[2], f[3]);
+      }
+      tmem_st(mine + wg * (H / 2), pk);
+      tmem_st(mine + C::kDp + wg * (H / 2), dk);
+#pragma unroll
+      for (int i = 0; i < H; ++i) {
+        const int r = wg * H + i;
+        *reinterpret_cast<uint16_t*>(ds_at + r * 128 + ((chunk ^ (r & 7)) << 4)) =
+            (uint16_t)(i & 1 ? dk[i / 2] >> 16 : dk[i / 2]);
+      }
+      if (wg == 0 && !takes)  // a row of K that another bag or a masked key holds: 0 * NaN is NaN
+        for (int i = 0; i < C::kBlocks; ++i) {
+          uint4* row = reinterpret_cast<uint4*>(skv + 2 * (j % NS) * C::kTile + (i * kKeys + key) * 128);
+#pragma unroll
+          for (int u = 0; u < 8; ++u) row[u] = make_uint4(0, 0, 0, 0);
+        }
+      fence_async_smem();
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(e_full);
+      ok = mbar_wait(o_full, j & 1, spin_max);
+      if (!__all_sync(0xffffffffu, ok)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      // warpgroup 0 stores dV, warpgroup 1 dK
+      T* out = wg == 0 ? static_cast<T*>(p.gv) + t * p.gvs + h * p.gvh : static_cast<T*>(p.gk) + t * p.gks + h * p.gkh;
+      const float mul = wg == 0 ? 1.0f : p.scale;
+#pragma unroll
+      for (int q = 0; q < DP / 32; ++q) {
+        uint32_t r[32];
+        tmem_ld(mine + (wg == 0 ? C::kDv : C::kDk) + 32 * q, r);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float f[8];
+#pragma unroll
+          for (int u = 0; u < 8; ++u) f[u] = takes ? __uint_as_float(r[8 * i + u]) * mul : 0.f;
+          if (in && 32 * q + 8 * i < p.D) store_vec(out + 32 * q + 8 * i, f);
+        }
+      }
+      tc_fence_before();
+    }
+    // dQ: lane r of tensor memory is row r
+    const int row = tid & 127;
+    if (wg == 0 && (w & 3) * 32 < NR) {
+      tc_fence_after();
+      const int64_t t = bag.q0 + row / p.G;
+      const int hq = h * p.G + row % p.G;
+      const bool have = n > 0 && ok;
+#pragma unroll
+      for (int q = 0; q < DP / 32; ++q) {
+        uint32_t r[32];
+        if (have) {
+          tmem_ld(mine + C::kDq + 32 * q, r);
+          tmem_wait_ld();
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int d = 32 * q + 8 * i;
+          float f[8];
+#pragma unroll
+          for (int u = 0; u < 8; ++u) f[u] = have ? __uint_as_float(r[8 * i + u]) * p.scale : 0.f;
+          if (row < rows && d < p.D) {
+            if (p.splits == 1) store_vec(static_cast<T*>(p.gq) + t * p.gqs + hq * p.gqh + d, f);
+            else store_vec(p.po + (((int64_t)sp * p.Tq + t) * p.Hq + hq) * p.D + d, f);
+          }
+        }
+      }
+    }
+  }
+  if (!ok) atomicOr(p.status, kErrTimeout);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (w == kIssuer) tmem_free(tmem, C::kCols);
+}
+
+template <typename T, int DP, int NR>
+cudaError_t few_back_launch(const AttendParams& p, const CUtensorMap (&m)[4], int64_t grid, cudaStream_t s) {
+  using C = FewBackCfg<DP, NR>;
+  auto kernel = attend_back_few_kernel<T, DP, NR>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kTotal);
+  if (e != cudaSuccess) return e;
+  kernel<<<(unsigned)grid, kThreads, C::kTotal, s>>>(p, m[0], m[1], m[2], m[3], spin_limit());
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+recis_status launch_attend_back_few(const AttendParams& p, bool bf16, cudaStream_t s) {
+  const int64_t grid = (int64_t)p.B * p.splits * p.Hkv;
+  if (grid >= ((int64_t)1 << 31)) {
+    set_error("attend_backward: too many blocks (bags times longest bag times heads)");
+    return RECIS_ERR_INVALID_ARG;
+  }
+  CUtensorMap m[4] = {};
+  // a map is made only where its array has rows; without rows no block uses it
+  bool ok = true;
+  if (p.Tq > 0)
+    ok = rows_map(&m[0], p.q, bf16, p.D, p.Hq, p.Tq, p.qs, p.qh, p.G, p.max_q) &&
+         rows_map(&m[1], p.go, bf16, p.D, p.Hq, p.Tq, p.gos, p.goh, p.G, p.max_q);
+  if (p.Tk > 0)
+    ok = ok && rows_map(&m[2], p.k, bf16, p.D, p.Hkv, p.Tk, p.ks, p.kh, 1, kKeys) &&
+         rows_map(&m[3], p.v, bf16, p.D, p.Hkv, p.Tk, p.vs, p.vh, 1, kKeys);
+  if (!ok) {
+    set_error("attend_backward: the driver refused a tensor map");
+    return RECIS_ERR_CUDA;
+  }
+  const int rows = p.max_q * p.G;
+  LaunchScope ls("attend_back_few", s);
+  auto go = [&](auto t) {
+    using T = decltype(t);
+    if (p.D <= 64)
+      return rows <= 16   ? few_back_launch<T, 64, 16>(p, m, grid, s)
+             : rows <= 32 ? few_back_launch<T, 64, 32>(p, m, grid, s)
+                          : few_back_launch<T, 64, 64>(p, m, grid, s);
+    return rows <= 16   ? few_back_launch<T, 128, 16>(p, m, grid, s)
+           : rows <= 32 ? few_back_launch<T, 128, 32>(p, m, grid, s)
+                        : few_back_launch<T, 128, 64>(p, m, grid, s);
+  };
+  const cudaError_t e = bf16 ? go(__nv_bfloat16()) : go(__half());
+  return e == cudaSuccess ? RECIS_OK : cuda_fail(e, "attend_back_few launch");
+}
+
+}  // namespace recis

@@ -108,7 +108,7 @@ def test_attend_backward_refuses(R, kw):
 
 def test_attend_workspace_is_asked_for(R):
     L, nb = R.load(), ctypes.c_int64()
-    a = _attend_args()
+    a = _attend_args(Tq=40, max_q=40)  # more rows than one tile: the backward keeps sums for them
     assert L.recis_attend_workspace(ctypes.byref(a), 1, ctypes.byref(nb)) == R.OK and nb.value > 0
     assert L.recis_attend_backward(ctypes.byref(a), P, nb.value - 1, None) == R.ERR_INVALID_ARG
     assert L.recis_attend_backward(ctypes.byref(a), P + 16, nb.value, None) == R.ERR_INVALID_ARG
