@@ -436,7 +436,8 @@ template <typename T, int DP>
 cudaError_t few_launch(const AttendParams& p, const CUtensorMap& mk, const CUtensorMap& mv, int64_t grid,
                        cudaStream_t s) {
   auto kernel = few_kernel<T, DP>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, FewCfg<DP>::kTotal);
+  static std::atomic<uint64_t> done[2];
+  const cudaError_t e = allow_smem(kernel, FewCfg<DP>::kTotal, done);
   if (e != cudaSuccess) return e;
   kernel<<<(unsigned)grid, kFewWarps * 32 + 32, FewCfg<DP>::kTotal, s>>>(p, mk, mv, spin_limit());
   return cudaGetLastError();

@@ -407,7 +407,8 @@ template <typename T, int DP, bool KEYS>
 cudaError_t back_launch(const AttendParams& p, const BackMaps& m, int64_t grid, cudaStream_t s) {
   using C = BackCfg<DP>;
   auto kernel = attend_back_kernel<T, DP, KEYS>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kTotal);
+  static std::atomic<uint64_t> done[2];
+  const cudaError_t e = allow_smem(kernel, C::kTotal, done);
   if (e != cudaSuccess) return e;
   kernel<<<(unsigned)grid, C::kThreads, C::kTotal, s>>>(p, m, spin_limit());
   return cudaGetLastError();

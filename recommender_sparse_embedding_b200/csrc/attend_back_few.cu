@@ -331,7 +331,8 @@ template <typename T, int DP, int NR>
 cudaError_t few_back_launch(const AttendParams& p, const CUtensorMap (&m)[4], int64_t grid, cudaStream_t s) {
   using C = FewBackCfg<DP, NR>;
   auto kernel = attend_back_few_kernel<T, DP, NR>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kTotal);
+  static std::atomic<uint64_t> done[2];
+  const cudaError_t e = allow_smem(kernel, C::kTotal, done);
   if (e != cudaSuccess) return e;
   kernel<<<(unsigned)grid, kThreads, C::kTotal, s>>>(p, m[0], m[1], m[2], m[3], spin_limit());
   return cudaGetLastError();

@@ -306,8 +306,9 @@ template <typename T, int DP>
 static cudaError_t tc_launch(const AttendParams& p, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
                              int64_t grid, cudaStream_t s) {
   auto kernel = attend_tc_kernel<T, DP>;
+  static std::atomic<uint64_t> done[2];
   const cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, FwdSmem<DP>::kTotal);
+      allow_smem(kernel, FwdSmem<DP>::kTotal, done);
   if (e != cudaSuccess) return e;
   kernel<<<(unsigned)grid, kTcThreads, FwdSmem<DP>::kTotal, s>>>(p, mq, mk, mv, spin_limit());
   return cudaGetLastError();

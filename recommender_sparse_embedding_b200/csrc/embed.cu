@@ -7,13 +7,13 @@
 // gradient reads N rows of dout and writes the V rows of dW.
 //
 // The gradient sorts (token, position) by a stable radix sort, so that a row's
-// terms are added in occurrence order whatever the scheduling.  The sorted
-// positions are cut into spans; a group of lanes walks one span, 8 columns a
-// lane, and adds the rows of equal tokens in fp32 (at most kSpan terms).  A
-// run of one token inside a span is finished there; a run cut by span ends
-// leaves one fp32 partial per span, and a second kernel adds those in span
-// order, in fp64 -- a hot token's thousands of rows are summed by as many
-// groups, and no float atomic is used.
+// terms are added in occurrence order whatever the scheduling.  The sort moves
+// little and is bound by latency; its kernels carry extra blocks that write
+// the zeros of dW beside it.  The sorted positions are cut into spans; a group
+// of lanes walks one span, 8 columns a lane, adds the rows of equal tokens in
+// fp32, and goes on into the next span to finish a run that ends there.  A
+// longer run (a hot token) leaves one fp32 partial per span, and a second
+// kernel adds those in span order in fp64: no float atomic is used.
 #include <algorithm>
 
 #include "seqops.cuh"
@@ -110,6 +110,19 @@ __device__ __forceinline__ uint32_t sort_key(int64_t t, int64_t V, int64_t paddi
   return (uint32_t)t;
 }
 
+// Zeros written by the blocks behind a kernel's own: [at, at + bytes), 16-byte
+// aligned, kZeroBytes a block.
+constexpr int kZeroBytes = 64 * 1024;
+struct ZeroSlice {
+  char* at;
+  int64_t bytes;
+};
+__device__ __forceinline__ void zero_block(const ZeroSlice& z, int64_t block) {
+  const int64_t lo = block * kZeroBytes, hi = lo + kZeroBytes < z.bytes ? lo + kZeroBytes : z.bytes;
+  for (int64_t i = lo + (int64_t)threadIdx.x * 16; i < hi; i += (int64_t)blockDim.x * 16)
+    *reinterpret_cast<uint4*>(z.at + i) = make_uint4(0, 0, 0, 0);
+}
+
 struct PassParams {
   const int64_t* tok;       // first pass: the tokens; later passes read `in`
   const uint2* in;          // {key, position}
@@ -119,7 +132,9 @@ struct PassParams {
   int tiles;
   uint32_t* hist;           // [tiles][bins]: counts, then exclusive prefixes over tiles
   uint32_t* total;          // [bins]
+  int* listed;              // runs listed for the join: cleared by the first pass
   int* status;
+  ZeroSlice zero[3];        // beside the count, the scan and the scatter
 };
 
 template <int ITEMS>
@@ -134,6 +149,11 @@ __global__ void __launch_bounds__(kSortThreads) grad_count_kernel(const __grid_c
   __shared__ uint32_t s_h[1 << kMaxDigit];
   const int bins = 1 << p.bits;
   pdl_wait();
+  if ((int)blockIdx.x >= p.tiles) {
+    zero_block(p.zero[0], blockIdx.x - p.tiles);
+    return;
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0 && !p.in) *p.listed = 0;
   for (int b = threadIdx.x; b < bins; b += kSortThreads) s_h[b] = 0;
   __syncthreads();
   const int64_t base = (int64_t)blockIdx.x * (kSortThreads * ITEMS);
@@ -156,6 +176,10 @@ __global__ void __launch_bounds__(1024) grad_scan_kernel(const __grid_constant__
   const int per = (p.tiles + 31) / 32;
   const int t0 = min(w * per, p.tiles), t1 = min(t0 + per, p.tiles);
   pdl_wait();
+  if (blockIdx.x * 32 >= bins) {
+    zero_block(p.zero[1], blockIdx.x - (bins + 31) / 32);
+    return;
+  }
   uint32_t sum = 0;
   if (b < bins)
     for (int t = t0; t < t1; ++t) sum += p.hist[(size_t)t * bins + b];
@@ -183,8 +207,13 @@ __global__ void __launch_bounds__(kSortThreads) grad_scatter_kernel(const __grid
   __shared__ uint32_t s_w[kWarps];
   const int bins = 1 << p.bits, tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   uint32_t* s_base = s_cnt + kWarps * bins;
-  for (int b = tid; b < kWarps * bins; b += kSortThreads) s_cnt[b] = 0;
+  if ((int)blockIdx.x < p.tiles)
+    for (int b = tid; b < kWarps * bins; b += kSortThreads) s_cnt[b] = 0;
   pdl_wait();
+  if ((int)blockIdx.x >= p.tiles) {
+    zero_block(p.zero[2], blockIdx.x - p.tiles);
+    return;
+  }
   // exclusive scan of the digit totals: 4 (at most) consecutive bins a thread
   const int per = (bins + kSortThreads - 1) / kSortThreads;
   uint32_t mine = 0;
@@ -250,7 +279,9 @@ struct SumParams {
   const int64_t* tok;   // small path: the tokens
   const void* g;
   void* dw;
-  float* partial;       // [spans][2][D]: 0 a run begun in an earlier span, 1 the run that goes on into the next
+  float* partial;       // [spans][2][D]: parts of runs that the join adds up, 0 begun before the span, 1 in it
+  int2* list;           // those runs' first spans and tokens, *listed of them
+  int* listed;
   int64_t N, V, g_stride, padding;
   int D, units, lanes;
   int accumulate;
@@ -277,7 +308,10 @@ __device__ __forceinline__ void grad_store(const SumParams& p, int64_t row, int 
 }
 
 // One group of `lanes` lanes (at most a warp) walks one span; blockIdx.y picks
-// the group's columns.  Rows are loaded 8 at a time, all in flight.
+// the group's columns.  Rows are loaded 8 at a time, all in flight.  A run
+// belongs to the span it begins in; one that ends in the next span is finished
+// by its owner (the next span's group passes over it), one that goes on further
+// is listed and left in parts.
 template <typename TG, typename TO, int VEC>
 __global__ void __launch_bounds__(256) grad_span_kernel(const __grid_constant__ SumParams p) {
   constexpr int U = 8;
@@ -287,40 +321,60 @@ __global__ void __launch_bounds__(256) grad_span_kernel(const __grid_constant__ 
   const int c = blockIdx.y * p.lanes + lane;
   pdl_wait();
   if (p0 >= p.N) return;
-  const int64_t p1 = p0 + kSpan < p.N ? p0 + kSpan : p.N;
+  const int64_t p1 = p0 + kSpan < p.N ? p0 + kSpan : p.N, p2 = p1 + kSpan < p.N ? p1 + kSpan : p.N;
   const bool in = c < p.units;
+  const uint32_t none = (uint32_t)p.V;  // key of positions without a row
+  // the keys around the span's ends
+  const uint32_t first = p.pairs[p0].x, last = p.pairs[p1 - 1].x;
+  const uint32_t before = p0 > 0 ? p.pairs[p0 - 1].x : none, after = p1 < p.N ? p.pairs[p1].x : none;
+  const uint32_t after2 = p2 < p.N ? p.pairs[p2].x : none;
+  const uint32_t before2 = p0 > kSpan ? p.pairs[p0 - kSpan - 1].x : none;
+  // a run begun before the span: finished by its owner if that is the span
+  // before and the run ends in this one; else this span's part of it
+  const bool head = before == first && first < none;
+  const bool head_part = head && (after == first || before2 == first);
+  // the run that goes on past the span (begun in it, or before: then the span
+  // is all one run): finished here if it ends in the next span, else in parts
+  const bool tail = after == last && last < none;
+  const bool tail_mine = tail && !(head && last == first);
+  const bool tail_part = tail_mine && after2 == last;
+  const int64_t end = tail_mine && !tail_part ? p2 : p1;
   float acc[VEC];
 #pragma unroll
   for (int j = 0; j < VEC; ++j) acc[j] = 0.f;
-  uint32_t cur = p.pairs[p0].x;
-  bool begun_before = p0 > 0 && p.pairs[p0 - 1].x == cur;
-  for (int64_t q = p0; q < p1; q += U) {
+  uint32_t cur = first;
+  bool in_head = head;
+  bool done = false;  // past p1, beyond the run's end
+  for (int64_t q = p0; q < end && !done; q += U) {
     uint2 e[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) e[u] = q + u < p1 ? __ldg(p.pairs + q + u) : make_uint2((uint32_t)p.V, 0);
+    for (int u = 0; u < U; ++u) e[u] = q + u < end ? __ldg(p.pairs + q + u) : make_uint2(none, 0);
     RawVec<TG, VEC> r[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (e[u].x < (uint32_t)p.V && in)
-        r[u].load(static_cast<const TG*>(p.g) + (int64_t)e[u].y * p.g_stride + (int64_t)c * VEC);
+    for (int u = 0; u < U; ++u) {
+      const bool use = e[u].x < none && (q + u < p1 || e[u].x == last) && !(head && !head_part && e[u].x == first);
+      if (!use) e[u].x = e[u].x == first && head ? first : (q + u < p1 ? e[u].x : none);
+      if (use && in) r[u].load(static_cast<const TG*>(p.g) + (int64_t)e[u].y * p.g_stride + (int64_t)c * VEC);
+    }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (q + u >= p1) break;
-      if (e[u].x != cur) {  // the run of `cur` ends in this span
-        if (in && cur < (uint32_t)p.V) {
-          if (begun_before) {
-            float* at = p.partial + (span * 2) * (int64_t)p.D + (int64_t)c * VEC;
-            store_vec(at, acc);
-          } else {
-            grad_store<TO, VEC>(p, cur, c, acc);
-          }
+      if (q + u >= end) break;
+      if (e[u].x != cur) {  // the run of `cur` ends
+        if (in && cur < none) {
+          if (!in_head) grad_store<TO, VEC>(p, cur, c, acc);
+          else if (head_part) store_vec(p.partial + span * 2 * p.D + (int64_t)c * VEC, acc);
         }
-        begun_before = false;
+        in_head = false;
         cur = e[u].x;
+        if (q + u >= p1) {
+          done = true;
+          cur = none;
+          break;
+        }
 #pragma unroll
         for (int j = 0; j < VEC; ++j) acc[j] = 0.f;
       }
-      if (e[u].x < (uint32_t)p.V && in) {
+      if (e[u].x < none && in && !(in_head && !head_part)) {
         float f[VEC];
         r[u].unpack(f);
 #pragma unroll
@@ -328,56 +382,53 @@ __global__ void __launch_bounds__(256) grad_span_kernel(const __grid_constant__ 
       }
     }
   }
-  if (!in || cur >= (uint32_t)p.V) return;
-  const bool goes_on = p1 < p.N && p.pairs[p1].x == cur;
-  if (begun_before || goes_on) {
-    float* at = p.partial + (span * 2 + (begun_before ? 0 : 1)) * (int64_t)p.D + (int64_t)c * VEC;
-    store_vec(at, acc);
-  } else {
+  if (cur >= none) return;
+  if (tail_part || (in_head && head_part)) {
+    if (in) store_vec(p.partial + (span * 2 + (tail_part ? 1 : 0)) * p.D + (int64_t)c * VEC, acc);
+    if (tail_part && c == 0) p.list[atomicAdd(p.listed, 1)] = make_int2((int)span, (int)cur);
+  } else if (in && !in_head) {
     grad_store<TO, VEC>(p, cur, c, acc);
   }
 }
 
-// Joins the runs cut by span ends: the block of the span in which such a run
-// begins adds the spans' partials, `256 / lanes` strided groups in fp64, then
-// the groups' sums in group order.
+// Adds the parts of the listed runs: a block takes a run, `512 / lanes` strided
+// groups of lanes add its spans' parts in fp64, four loads in flight, then the
+// groups' sums are added in group order.  The list's order, the only thing that
+// scheduling decides, does not enter the sums.
+constexpr int kJoinThreads = 512;
 template <typename TO, int VEC>
-__global__ void __launch_bounds__(256) grad_join_kernel(const __grid_constant__ SumParams p) {
-  __shared__ double s_sum[256][VEC];
-  __shared__ int64_t s_last;
+__global__ void __launch_bounds__(kJoinThreads) grad_join_kernel(const __grid_constant__ SumParams p) {
+  __shared__ double s_sum[kJoinThreads][VEC];
   const int64_t spans = (p.N + kSpan - 1) / kSpan;
-  const int lane = threadIdx.x & (p.lanes - 1), group = threadIdx.x / p.lanes, groups = 256 / p.lanes;
+  const int lane = threadIdx.x & (p.lanes - 1), group = threadIdx.x / p.lanes, groups = kJoinThreads / p.lanes;
   const int c = blockIdx.y * p.lanes + lane;
   pdl_wait();
-  for (int64_t span = blockIdx.x; span + 1 < spans; span += gridDim.x) {
-    const int64_t p0 = span * kSpan, p1 = p0 + kSpan;
-    const uint32_t key = p.pairs[p1 - 1].x;
-    if (key >= (uint32_t)p.V || p.pairs[p1].x != key) continue;       // nothing goes on
-    if (p.pairs[p0].x == key && p0 > 0 && p.pairs[p0 - 1].x == key) continue;  // begun in an earlier span
-    if (threadIdx.x < 32) {  // the span the run ends in: 32 span ends a step
-      int64_t last = span;
-      for (int64_t t = span + 1;; t += 32) {
-        const int64_t mine = t + threadIdx.x, end = mine * kSpan + kSpan;
-        const bool whole = mine < spans && end < p.N && p.pairs[end].x == key;  // the run goes past span `mine`
-        const unsigned m = __ballot_sync(0xffffffffu, whole);
-        const int run = __ffs(~m) - 1;  // spans passed from t on (-1: all 32)
-        if (run >= 0) {
-          last = t + run;
-          break;
-        }
-      }
-      if (threadIdx.x == 0) s_last = last;
+  const int n = *p.listed;
+  for (int item = blockIdx.x; item < n; item += gridDim.x) {
+    const int64_t span = p.list[item].x;
+    const uint32_t key = (uint32_t)p.list[item].y;
+    // the span the run ends in: the first whose end the run does not pass; each
+    // round every thread tests one of kJoinThreads evenly spaced spans
+    int64_t lo = span + 1, hi = spans - 1;  // the answer lies in [lo, hi]
+    while (lo < hi) {
+      const int64_t stride = (hi - lo + kJoinThreads - 1) / kJoinThreads;
+      const int64_t at = lo + (int64_t)threadIdx.x * stride;
+      const bool passes = at < hi && p.pairs[(at + 1) * kSpan].x == key;
+      const int k = __syncthreads_count(passes);  // a run passes a prefix of the spans tested
+      if (k == 0) break;
+      const int64_t base = lo + (int64_t)(k - 1) * stride;
+      hi = hi < base + stride ? hi : base + stride;
+      lo = base + 1;
     }
-    __syncthreads();
-    const int64_t last = s_last;
+    const int64_t last = lo;
     double sum[VEC];
 #pragma unroll
     for (int j = 0; j < VEC; ++j) sum[j] = 0.0;
     if (c < p.units) {
+#pragma unroll 4
       for (int64_t t = span + group; t <= last; t += groups) {
-        const float* at = p.partial + (t * 2 + (t == span ? 1 : 0)) * (int64_t)p.D + (int64_t)c * VEC;
         RawVec<float, VEC> r;
-        r.load(at);
+        r.load(p.partial + (t * 2 + (t == span ? 1 : 0)) * p.D + (int64_t)c * VEC);
         float f[VEC];
         r.unpack(f);
 #pragma unroll
@@ -473,7 +524,7 @@ __global__ void __launch_bounds__(256) grad_small_kernel(const __grid_constant__
 // ---------------------------------------------------------------- gradient: host
 struct GradPlan {
   int items, tiles, passes, bits;  // the sort
-  int64_t pairs_bytes, hist_bytes, total_bytes, partial_bytes;
+  int64_t pairs_bytes, hist_bytes, total_bytes, partial_bytes, list_bytes;
   int64_t bytes;
 };
 
@@ -485,17 +536,21 @@ GradPlan grad_plan(int64_t N, int64_t V, int D) {
   g.passes = (bits + kMaxDigit - 1) / kMaxDigit;
   g.bits = (bits + g.passes - 1) / g.passes;
   if (g.bits < 5) g.bits = 5;  // the scan takes 32 bins at a time
-  // 16 keys a thread once there are tiles for every SM, 4 below
-  g.items = N >= (int64_t)kSMs * kSortThreads * 16 ? 16 : 4;
+  // 8 keys a thread once there are tiles for every SM, 4 below
+  g.items = N >= (int64_t)kSMs * kSortThreads * 8 ? 8 : 4;
   const int64_t tile = (int64_t)kSortThreads * g.items;
   g.tiles = (int)((N + tile - 1) / tile);
   g.pairs_bytes = align256(N * 8);
   g.hist_bytes = align256(((int64_t)g.tiles << g.bits) * 4);
-  g.total_bytes = align256(((int64_t)1 << g.bits) * 4);
-  g.partial_bytes = align256((N + kSpan - 1) / kSpan * 2 * D * 4);
-  g.bytes = 2 * g.pairs_bytes + g.hist_bytes + g.total_bytes + g.partial_bytes;
+  g.total_bytes = align256(((int64_t)1 << g.bits) * 4 + 4);  // and the number of listed runs
+  const int64_t spans = (N + kSpan - 1) / kSpan;
+  g.partial_bytes = align256(spans * 2 * D * 4);
+  g.list_bytes = align256(spans * 8);
+  g.bytes = 2 * g.pairs_bytes + g.hist_bytes + g.total_bytes + g.partial_bytes + g.list_bytes;
   return g;
 }
+
+unsigned zero_blocks(const ZeroSlice& z) { return (unsigned)((z.bytes + kZeroBytes - 1) / kZeroBytes); }
 
 template <int ITEMS>
 cudaError_t sort_pass_launch(const PassParams& pp, cudaStream_t s) {
@@ -503,15 +558,16 @@ cudaError_t sort_pass_launch(const PassParams& pp, cudaStream_t s) {
   cudaError_t e;
   {
     LaunchScope ls("embed_grad_count", s);
-    if ((e = launch_pdl(grad_count_kernel<ITEMS>, (unsigned)pp.tiles, kSortThreads, 0, s, pp)) != cudaSuccess)
-      return e;
+    e = launch_pdl(grad_count_kernel<ITEMS>, (unsigned)pp.tiles + zero_blocks(pp.zero[0]), kSortThreads, 0, s, pp);
+    if (e != cudaSuccess) return e;
   }
   {
     LaunchScope ls("embed_grad_scan", s);
-    if ((e = launch_pdl(grad_scan_kernel, (unsigned)((bins + 31) / 32), 1024, 0, s, pp)) != cudaSuccess) return e;
+    e = launch_pdl(grad_scan_kernel, (unsigned)((bins + 31) / 32) + zero_blocks(pp.zero[1]), 1024, 0, s, pp);
+    if (e != cudaSuccess) return e;
   }
   LaunchScope ls("embed_grad_scatter", s);
-  return launch_pdl(grad_scatter_kernel<ITEMS>, (unsigned)pp.tiles, kSortThreads,
+  return launch_pdl(grad_scatter_kernel<ITEMS>, (unsigned)pp.tiles + zero_blocks(pp.zero[2]), kSortThreads,
                     (size_t)(kSortThreads / 32 + 1) * bins * 4, s, pp);
 }
 
@@ -521,9 +577,11 @@ cudaError_t grad_launch(SumParams p, const int64_t* tok, char* ws, cudaStream_t 
   p.lanes = 1;
   while (p.lanes < p.units && p.lanes < 32) p.lanes *= 2;
   cudaError_t e;
-  if (!p.accumulate) {
-    e = cudaMemsetAsync(p.dw, 0, (size_t)p.V * p.D * sizeof(TO), s);
-    if (e != cudaSuccess) return e;
+  const int64_t dw_bytes = (int64_t)p.V * p.D * sizeof(TO);
+  // the sort's kernels write the zeros where it runs and 16-byte stores fit
+  const bool beside = p.N > kSmallN && dw_bytes % 16 == 0 && !misaligned(p.dw, 16);
+  if (!p.accumulate && !beside) {
+    if ((e = cudaMemsetAsync(p.dw, 0, (size_t)dw_bytes, s)) != cudaSuccess) return e;
   }
   if (p.N == 0) return cudaSuccess;
   if (p.N <= kSmallN) {
@@ -533,6 +591,7 @@ cudaError_t grad_launch(SumParams p, const int64_t* tok, char* ws, cudaStream_t 
   }
   const GradPlan g = grad_plan(p.N, p.V, p.D);
   uint2* pairs[2] = {reinterpret_cast<uint2*>(ws), reinterpret_cast<uint2*>(ws + g.pairs_bytes)};
+  char* at = ws + 2 * g.pairs_bytes;
   PassParams pp = {};
   pp.tok = tok;
   pp.N = p.N;
@@ -540,34 +599,51 @@ cudaError_t grad_launch(SumParams p, const int64_t* tok, char* ws, cudaStream_t 
   pp.padding = p.padding;
   pp.bits = g.bits;
   pp.tiles = g.tiles;
-  pp.hist = reinterpret_cast<uint32_t*>(ws + 2 * g.pairs_bytes);
-  pp.total = reinterpret_cast<uint32_t*>(ws + 2 * g.pairs_bytes + g.hist_bytes);
+  pp.hist = reinterpret_cast<uint32_t*>(at);
+  at += g.hist_bytes;
+  pp.total = reinterpret_cast<uint32_t*>(at);
+  pp.listed = reinterpret_cast<int*>(pp.total + ((int64_t)1 << g.bits));
+  at += g.total_bytes;
   pp.status = p.status;
+  // the zeros in equal slices, one a kernel of the sort
+  const int slices = 3 * g.passes;
+  const int64_t slice = (dw_bytes / slices + 16) / 16 * 16;
+  int64_t done = 0;
   for (int i = 0; i < g.passes; ++i) {
     pp.shift = i * g.bits;
     pp.in = i == 0 ? nullptr : pairs[(i + 1) & 1];
     pp.out = pairs[i & 1];
-    e = g.items == 16 ? sort_pass_launch<16>(pp, s) : sort_pass_launch<4>(pp, s);
+    for (ZeroSlice& z : pp.zero) {
+      z.at = static_cast<char*>(p.dw) + done;
+      z.bytes = beside && !p.accumulate ? std::min(slice, dw_bytes - done) : 0;
+      done += z.bytes;
+    }
+    e = g.items == 8 ? sort_pass_launch<8>(pp, s) : sort_pass_launch<4>(pp, s);
     if (e != cudaSuccess) return e;
   }
   p.pairs = pairs[(g.passes - 1) & 1];
-  p.partial = reinterpret_cast<float*>(ws + 2 * g.pairs_bytes + g.hist_bytes + g.total_bytes);
+  p.partial = reinterpret_cast<float*>(at);
+  p.list = reinterpret_cast<int2*>(at + g.partial_bytes);
+  p.listed = pp.listed;
   const int64_t spans = (p.N + kSpan - 1) / kSpan;
   const int cols = (p.units + p.lanes - 1) / p.lanes;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute pdl[1];
+  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  pdl[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = pdl;
+  cfg.numAttrs = 1;
+  cfg.stream = s;
   {
     LaunchScope ls("embed_grad_span", s);
-    cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((spans * p.lanes + 255) / 256), (unsigned)cols);
     cfg.blockDim = dim3(256);
-    cfg.stream = s;
     if ((e = cudaLaunchKernelEx(&cfg, grad_span_kernel<TG, TO, VEC>, p)) != cudaSuccess) return e;
   }
-  if (spans > 1) {
+  if (spans > 2) {
     LaunchScope ls("embed_grad_join", s);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)std::min<int64_t>(spans - 1, kSMs * 8), (unsigned)cols);
-    cfg.blockDim = dim3(256);
-    cfg.stream = s;
+    cfg.gridDim = dim3((unsigned)std::min<int64_t>(spans / 2, kSMs * 2), (unsigned)cols);
+    cfg.blockDim = dim3(kJoinThreads);
     if ((e = cudaLaunchKernelEx(&cfg, grad_join_kernel<TO, VEC>, p)) != cudaSuccess) return e;
   }
   return cudaGetLastError();

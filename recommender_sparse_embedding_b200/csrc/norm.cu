@@ -43,6 +43,41 @@ __device__ __forceinline__ float param_at(const void* p, int type, int i) {
   return to_f32(static_cast<const __half*>(p)[i]);
 }
 
+template <int VEC>
+__device__ __forceinline__ void param_vec(const void* p, int type, int c, float (&f)[VEC]) {
+  if constexpr (VEC == 8) {
+    if (type == RECIS_F32) {
+      RawVec<float, 8> r;
+      r.load(static_cast<const float*>(p) + c);
+      r.unpack(f);
+    } else if (type == RECIS_BF16) {
+      RawVec<__nv_bfloat16, 8> r;
+      r.load(static_cast<const __nv_bfloat16*>(p) + c);
+      r.unpack(f);
+    } else {
+      RawVec<__half, 8> r;
+      r.load(static_cast<const __half*>(p) + c);
+      r.unpack(f);
+    }
+  }
+}
+
+// VEC parameters from column c on (`none` where the array is NULL)
+template <int VEC>
+__device__ __forceinline__ void load_params(const void* p, int type, int c, float none, float (&f)[VEC]) {
+  if (!p) {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) f[j] = none;
+    return;
+  }
+  if (VEC == 8 && ((uintptr_t)p & 15) == 0) {
+    param_vec(p, type, c, f);
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) f[j] = param_at(p, type, c + j);
+}
+
 // Sum of v over the tpr threads of the caller's row; every thread gets it.
 // tpr <= 32: shuffles within the warp; more: tpr is a multiple of 32, and every
 // thread of the block calls (`s` alternates between calls, so one barrier a
@@ -70,67 +105,80 @@ __device__ __forceinline__ void row_sum(float (&v)[K], int tpr, float (*s)[32]) 
   }
 }
 
-// UPT vectors of VEC columns a thread: columns (lane + k * tpr) * VEC.
+// UPT vectors of VEC columns a thread: columns (lane + k * tpr) * VEC.  The
+// blocks are persistent: a thread keeps its columns' weight and bias in
+// registers through all its rows, and a row's loads are issued before the row
+// before it is worked on.
 template <typename TX, typename TY, int VEC, int UPT>
 __global__ void __launch_bounds__(kMaxRowThreads) norm_kernel(const __grid_constant__ NormParams p) {
   __shared__ float s_red[2][1][32];
   const int rows = blockDim.x / p.tpr;  // rows a block takes at once
-  const int lane = threadIdx.x % p.tpr;
-  const int64_t i = (int64_t)blockIdx.x * rows + threadIdx.x / p.tpr;
-  const bool live = i < p.M;  // a warp may hold several rows: all its lanes take part in the sums
-  const TX* x = static_cast<const TX*>(p.x) + i * p.x_stride;
-  float v[UPT][VEC];
-  float s[1] = {0.f};
-  {
-    RawVec<TX, VEC> raw[UPT];
-#pragma unroll
-    for (int k = 0; k < UPT; ++k) {
-      const int c = lane + k * p.tpr;
-      if (live && c < p.units) raw[k].load(x + (int64_t)c * VEC);
-    }
-#pragma unroll
-    for (int k = 0; k < UPT; ++k) {
-      const int c = lane + k * p.tpr;
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) v[k][j] = 0.f;
-      if (live && c < p.units) raw[k].unpack(v[k]);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) s[0] += v[k][j];
-    }
-  }
-  const float inv = 1.0f / (float)p.D;
-  row_sum<1>(s, p.tpr, s_red[0]);
-  const float mu = s[0] * inv;
-  s[0] = 0.f;
-#pragma unroll
-  for (int k = 0; k < UPT; ++k) {
-    if (lane + k * p.tpr >= p.units) break;
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      v[k][j] -= mu;
-      s[0] = fmaf(v[k][j], v[k][j], s[0]);
-    }
-  }
-  row_sum<1>(s, p.tpr, s_red[1]);
-  const float r = 1.0f / sqrtf(fmaf(s[0], inv, p.eps));
-  if (!live) return;
-  if (lane == 0) {
-    if (p.mean) p.mean[i] = mu;
-    if (p.rstd) p.rstd[i] = r;
-  }
-  TY* y = static_cast<TY*>(p.y) + i * p.y_stride;
+  const int row = threadIdx.x / p.tpr, lane = threadIdx.x % p.tpr;
+  float w[UPT][VEC], b[UPT][VEC];
 #pragma unroll
   for (int k = 0; k < UPT; ++k) {
     const int c = lane + k * p.tpr;
-    if (c >= p.units) break;
-    float f[VEC];
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      const float w = p.w ? param_at(p.w, p.w_type, c * VEC + j) : 1.0f;
-      const float b = p.b ? param_at(p.b, p.w_type, c * VEC + j) : 0.0f;
-      f[j] = fmaf(v[k][j] * r, w, b);
+    if (c < p.units) {
+      load_params(p.w, p.w_type, c * VEC, 1.0f, w[k]);
+      load_params(p.b, p.w_type, c * VEC, 0.0f, b[k]);
     }
-    store_vec(y + (int64_t)c * VEC, f);
+  }
+  const float inv = 1.0f / (float)p.D;
+  const int64_t step = (int64_t)gridDim.x * rows;
+  RawVec<TX, VEC> raw[UPT];
+  auto fetch = [&](int64_t i) {
+#pragma unroll
+    for (int k = 0; k < UPT; ++k) {
+      const int c = lane + k * p.tpr;
+      if (i < p.M && c < p.units) raw[k].load(static_cast<const TX*>(p.x) + i * p.x_stride + (int64_t)c * VEC);
+    }
+  };
+  fetch((int64_t)blockIdx.x * rows + row);
+  // every thread of the block goes through the same number of steps (a warp may
+  // hold several rows, and all its lanes take part in the sums)
+  for (int64_t i0 = (int64_t)blockIdx.x * rows; i0 < p.M; i0 += step) {
+    const int64_t i = i0 + row;
+    const bool live = i < p.M;
+    float v[UPT][VEC];
+    float s[1] = {0.f};
+#pragma unroll
+    for (int k = 0; k < UPT; ++k) {
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) v[k][j] = 0.f;
+      if (live && lane + k * p.tpr < p.units) raw[k].unpack(v[k]);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) s[0] += v[k][j];
+    }
+    fetch(i + step);
+    row_sum<1>(s, p.tpr, s_red[0]);
+    const float mu = s[0] * inv;
+    s[0] = 0.f;
+#pragma unroll
+    for (int k = 0; k < UPT; ++k) {
+      if (lane + k * p.tpr >= p.units) break;
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        v[k][j] -= mu;
+        s[0] = fmaf(v[k][j], v[k][j], s[0]);
+      }
+    }
+    row_sum<1>(s, p.tpr, s_red[1]);
+    const float r = 1.0f / sqrtf(fmaf(s[0], inv, p.eps));
+    if (!live) continue;
+    if (lane == 0) {
+      if (p.mean) p.mean[i] = mu;
+      if (p.rstd) p.rstd[i] = r;
+    }
+    TY* y = static_cast<TY*>(p.y) + i * p.y_stride;
+#pragma unroll
+    for (int k = 0; k < UPT; ++k) {
+      const int c = lane + k * p.tpr;
+      if (c >= p.units) break;
+      float f[VEC];
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) f[j] = fmaf(v[k][j] * r, w[k][j], b[k][j]);
+      store_vec(y + (int64_t)c * VEC, f);
+    }
   }
 }
 
@@ -171,29 +219,34 @@ __global__ void __launch_bounds__(kMaxRowThreads) norm_back_kernel(const __grid_
   for (int k = 0; k < UPT; ++k) {
     const int c = lane + k * p.tpr;
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      w[k][j] = c < p.units ? (p.w ? param_at(p.w, p.w_type, c * VEC + j) : 1.0f) : 0.f;
-      dw[k][j] = db[k][j] = 0.f;
-    }
+    for (int j = 0; j < VEC; ++j) w[k][j] = dw[k][j] = db[k][j] = 0.f;
+    if (c < p.units) load_params(p.w, p.w_type, c * VEC, 1.0f, w[k]);
   }
   const float inv = 1.0f / (float)p.D;
   const int64_t step = (int64_t)gridDim.x * rows;
   int flip = 0;
-  // every thread of the block goes through the same number of steps
-  for (int64_t i0 = (int64_t)blockIdx.x * rows; i0 < p.M; i0 += step, flip ^= 1) {
-    const int64_t i = i0 + row;
-    const bool live = i < p.M;
-    RawVec<TX, VEC> rx[UPT];
-    RawVec<TY, VEC> rg[UPT];
+  RawVec<TX, VEC> rx[UPT];
+  RawVec<TY, VEC> rg[UPT];
+  float mu_next = 0.f, r_next = 0.f;
+  auto fetch = [&](int64_t i) {
+    if (i >= p.M) return;
 #pragma unroll
     for (int k = 0; k < UPT; ++k) {
       const int c = lane + k * p.tpr;
-      if (live && c < p.units) {
+      if (c < p.units) {
         rx[k].load(static_cast<const TX*>(p.x) + i * p.x_stride + (int64_t)c * VEC);
         rg[k].load(static_cast<const TY*>(p.gy) + i * p.gy_stride + (int64_t)c * VEC);
       }
     }
-    const float mu = live ? __ldg(p.mean + i) : 0.f, r = live ? __ldg(p.rstd + i) : 0.f;
+    mu_next = __ldg(p.mean + i);
+    r_next = __ldg(p.rstd + i);
+  };
+  fetch((int64_t)blockIdx.x * rows + row);
+  // every thread of the block goes through the same number of steps
+  for (int64_t i0 = (int64_t)blockIdx.x * rows; i0 < p.M; i0 += step, flip ^= 1) {
+    const int64_t i = i0 + row;
+    const bool live = i < p.M;
+    const float mu = live ? mu_next : 0.f, r = live ? r_next : 0.f;
     float xh[UPT][VEC], g[UPT][VEC];
     float s[2] = {0.f, 0.f};
 #pragma unroll
@@ -215,6 +268,7 @@ __global__ void __launch_bounds__(kMaxRowThreads) norm_back_kernel(const __grid_
         }
       }
     }
+    fetch(i + step);
     if (!p.y) continue;
     row_sum<2>(s, p.tpr, s_red[flip]);
     const float m0 = s[0] * inv, m1 = s[1] * inv;
@@ -300,8 +354,11 @@ __global__ void __launch_bounds__(1024) norm_join_kernel(const float* partial, i
   const int c = blockIdx.x * 32 + lane;  // columns of [dw | db]
   double t = 0.0;
   const int per = (blocks + 31) / 32;
-  if (c < 2 * D)
-    for (int q = k * per; q < min((k + 1) * per, blocks); ++q) t += (double)partial[(int64_t)q * 2 * D + c];
+  if (c < 2 * D) {
+    const int q1 = min((k + 1) * per, blocks);
+#pragma unroll 8
+    for (int q = k * per; q < q1; ++q) t += (double)__ldg(partial + (int64_t)q * 2 * D + c);
+  }
   s[k][lane] = t;
   __syncthreads();
   if (k != 0 || c >= 2 * D) return;
@@ -323,22 +380,31 @@ int row_threads(int units, int upt) {
   return t <= kMaxRowThreads ? t : 0;
 }
 
+// persistent blocks: as many as the SMs hold at `threads` threads an SM
+int persistent_blocks(int64_t M, int rows, int block, int threads) {
+  return (int)std::min<int64_t>((M + rows - 1) / rows, (int64_t)kSMs * std::max(1, threads / block));
+}
+
 template <typename TX, typename TY, int VEC>
 cudaError_t norm_launch(NormParams p, cudaStream_t s) {
   p.units = p.D / VEC;
   LaunchScope ls("layer_norm", s);
-  // a warp's width of threads first, then up to four vectors a thread, then more threads
-  int upt = p.units <= 32 ? 1 : p.units <= 64 ? 2 : 4;
+  // a warp's width of threads first, then up to 16 columns a thread, then more
+  // threads, then up to 32 (single columns: 8) a thread
+  const int most = VEC == 8 ? 4 : 8;
+  int upt = p.units <= 32 ? 1 : 2;
+  if (VEC == 1 && p.units > 64) upt = 8;
   p.tpr = row_threads(p.units, upt);
+  if (!p.tpr) p.tpr = row_threads(p.units, upt = most);
   if (!p.tpr) {
     norm_wide_kernel<TX, TY><<<(unsigned)p.M, kWideThreads, 0, s>>>(p);
     return cudaGetLastError();
   }
   const int block = std::max(p.tpr, 128), rows = block / p.tpr;
-  const unsigned grid = (unsigned)((p.M + rows - 1) / rows);
+  const int grid = persistent_blocks(p.M, rows, block, upt == 1 ? 1536 : 1024);
   if (upt == 1) norm_kernel<TX, TY, VEC, 1><<<grid, block, 0, s>>>(p);
   else if (upt == 2) norm_kernel<TX, TY, VEC, 2><<<grid, block, 0, s>>>(p);
-  else norm_kernel<TX, TY, VEC, 4><<<grid, block, 0, s>>>(p);
+  else norm_kernel<TX, TY, VEC, VEC == 8 ? 4 : 8><<<grid, block, 0, s>>>(p);
   return cudaGetLastError();
 }
 
@@ -349,7 +415,7 @@ template <typename TX, typename TY, int VEC>
 cudaError_t back_launch(NormParams p, cudaStream_t s, int* blocks_out) {
   p.units = p.D / VEC;
   LaunchScope ls("layer_norm_backward", s);
-  const int upt = p.units <= 32 ? 1 : 2;
+  const int upt = p.units <= 32 ? 1 : VEC == 1 && p.units > 64 ? 8 : 2;
   p.tpr = row_threads(p.units, upt);
   int blocks = back_blocks(p.M);
   if (!p.tpr) {
@@ -358,7 +424,7 @@ cudaError_t back_launch(NormParams p, cudaStream_t s, int* blocks_out) {
     return cudaGetLastError();
   }
   const int block = std::max(p.tpr, 256), rows = block / p.tpr;
-  blocks = (int)std::min<int64_t>(blocks, (p.M + rows - 1) / rows);
+  blocks = std::min(blocks, persistent_blocks(p.M, rows, block, 1024));
   *blocks_out = blocks;
   const size_t smem = p.partial ? (size_t)2 * p.tpr * upt * VEC * 4 : 0;
   auto go = [&](auto kernel) {
@@ -369,7 +435,9 @@ cudaError_t back_launch(NormParams p, cudaStream_t s, int* blocks_out) {
     kernel<<<blocks, block, smem, s>>>(p);
     return cudaGetLastError();
   };
-  return upt == 1 ? go(norm_back_kernel<TX, TY, VEC, 1>) : go(norm_back_kernel<TX, TY, VEC, 2>);
+  if (upt == 1) return go(norm_back_kernel<TX, TY, VEC, 1>);
+  if (upt == 2) return go(norm_back_kernel<TX, TY, VEC, 2>);
+  return go(norm_back_kernel<TX, TY, VEC, VEC == 1 ? 8 : 2>);
 }
 
 bool norm_sizes_ok(int64_t M, int32_t D) { return M >= 0 && M <= INT32_MAX && D >= 1 && D <= 65536; }

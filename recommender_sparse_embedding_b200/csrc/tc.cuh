@@ -9,6 +9,7 @@
 #pragma once
 #include <cuda.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "seqops.cuh"
@@ -130,6 +131,20 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// Allows `kernel` its dynamic shared memory, once a device; `done` is the
+// kernel's own (a bit a device).
+template <typename K>
+cudaError_t allow_smem(K kernel, int bytes, std::atomic<uint64_t> (&done)[2]) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || dev < 0 || dev >= 128) return e == cudaSuccess ? cudaErrorInvalidDevice : e;
+  const uint64_t bit = 1ULL << (dev & 63);
+  if (done[dev >> 6].load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done[dev >> 6].fetch_or(bit, std::memory_order_release);
+  return e;
 }
 
 // Tensor map of rows of heads of D 16-bit elements at p (row and head strides

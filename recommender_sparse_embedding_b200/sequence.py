@@ -13,7 +13,6 @@ token out of range, malformed offsets) are raised by sequence_status_sync.
 from __future__ import annotations
 
 import ctypes
-from contextlib import contextmanager
 from typing import Optional
 
 import torch
@@ -39,28 +38,34 @@ class AttendArgs(ctypes.Structure):
                                                  "grad_k_head_stride", "grad_v_stride", "grad_v_head_stride")])
 
 
-@contextmanager
-def _on(stream, *tensors):
-    """The tensors' device and the call's stream made current; yields the raw
-    stream.  Every tensor (None: left out) is on the first one's device."""
-    dev = tensors[0].device
+def _elsewhere(stream, *tensors) -> bool:
+    """Whether the call runs on another device or stream than the current one.
+    Every tensor (None: left out) is on the first one's device."""
+    index = tensors[0].get_device()  # -1: not a GPU's
     for t in tensors:
-        if t is not None and (not t.is_cuda or t.device != dev):
-            raise ValueError(f"expected CUDA tensors on one device, got {t.device} beside {dev}")
-    if stream is not None and stream.device != dev:
-        raise ValueError(f"the stream belongs to {stream.device}, the tensors to {dev}")
-    with torch.cuda.device(dev):
-        if stream is None:
-            yield torch.cuda.current_stream(dev).cuda_stream
-        else:
-            with torch.cuda.stream(stream):
-                yield stream.cuda_stream
+        if t is not None and (t.get_device() != index or index < 0):
+            raise ValueError(f"expected CUDA tensors on one device, got {t.device} beside {tensors[0].device}")
+    if stream is None:
+        return index != torch.cuda.current_device()
+    if stream.device != tensors[0].device:
+        raise ValueError(f"the stream belongs to {stream.device}, the tensors to {tensors[0].device}")
+    return True
+
+
+def _on(stream, t: torch.Tensor):
+    """The context that makes the call's stream, and with it its device, current."""
+    return torch.cuda.stream(torch.cuda.current_stream(t.device) if stream is None else stream)
+
+
+def _raw(dev: torch.device) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
 def _type(t: torch.Tensor, name: str, types=TYPES) -> int:
-    if t.dtype not in types:
+    code = types.get(t.dtype)
+    if code is None:
         raise TypeError(f"{name}: expected one of {', '.join(str(d) for d in types)}, got {t.dtype}")
-    return types[t.dtype]
+    return code
 
 
 def _int64(t: torch.Tensor, name: str) -> torch.Tensor:
@@ -73,28 +78,40 @@ def _int64(t: torch.Tensor, name: str) -> torch.Tensor:
 
 def _rows(t: torch.Tensor, name: str, D: Optional[int] = None):
     """(rows, D, row stride) of a tensor seen as rows of its last dimension."""
-    if t.dim() < 1:
+    shape = t.shape
+    if not shape:
         raise ValueError(f"{name}: expected rows, got a scalar")
-    if D is not None and t.shape[-1] != D:
-        raise ValueError(f"{name}: expected rows of {D}, got {t.shape[-1]}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    width = shape[-1]
+    if (D is None or width == D) and width and t.is_contiguous():
+        return t.numel() // width, width, width
+    if D is not None and width != D:
+        raise ValueError(f"{name}: expected rows of {D}, got {width}")
+    n = t.numel() // width if width else 0
+    if n <= 1 or t.is_contiguous():
+        if width > 1 and t.stride(-1) != 1:
+            raise ValueError(f"{name}: the elements of a row must be contiguous")
+        return n, width, width
+    if width > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name}: the elements of a row must be contiguous")
-    n = t.numel() // max(t.shape[-1], 1)
-    if n <= 1:
-        return n, t.shape[-1], t.shape[-1]
-    try:
-        flat = t.view(n, t.shape[-1])
-    except RuntimeError:
-        raise ValueError(f"{name}: the rows must be evenly spaced") from None
-    if flat.stride(0) < t.shape[-1]:
+    step = None
+    span = 0
+    for size, stride in zip(reversed(shape[:-1]), reversed(t.stride()[:-1])):
+        if size == 1:
+            continue
+        if step is None:
+            step = stride
+        elif stride != span:
+            raise ValueError(f"{name}: the rows must be evenly spaced")
+        span = stride * size
+    if step < width:
         raise ValueError(f"{name}: rows overlap (an expanded tensor?)")
-    return n, t.shape[-1], flat.stride(0)
+    return n, width, step
 
 
 def _out(out, name, shape, dtype, device):
     if out is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    if tuple(out.shape) != tuple(shape) or out.dtype != dtype:
+    if out.shape != shape or out.dtype != dtype:
         raise ValueError(f"{name}: expected {tuple(shape)} of {dtype}, got {tuple(out.shape)} of {out.dtype}")
     return out
 
@@ -103,16 +120,15 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None or t.numel() == 0 else t.data_ptr()
 
 
-def _scratch(nbytes: int, device) -> torch.Tensor:
-    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+def _scratch(nbytes: int, device) -> Optional[torch.Tensor]:
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
 
 
 def sequence_status_sync(stream=None):
     """recis_sequence_status_sync: waits for the stream and raises what earlier
     sequence calls on its device found."""
-    dev = torch.device("cuda", torch.cuda.current_device()) if stream is None else stream.device
-    with torch.cuda.device(dev):
-        s = torch.cuda.current_stream(dev) if stream is None else stream
+    s = torch.cuda.current_stream() if stream is None else stream
+    with torch.cuda.device(s.device):
         _r._check(_r.load().recis_sequence_status_sync(s.cuda_stream), "recis_sequence_status_sync")
 
 
@@ -127,13 +143,15 @@ def embed_lookup(weight: torch.Tensor, tokens: torch.Tensor, scale: float = 1.0,
     wt = _type(weight, "weight")
     tokens = _int64(tokens, "tokens")
     V, D = weight.shape
-    with _on(stream, weight, tokens, out) as s:
-        out = _out(out, "out", (*tokens.shape, D), out_dtype or (weight.dtype if out is None else out.dtype),
-                   weight.device)
-        ot = _type(out, "out")
-        _, _, stride = _rows(out, "out", D)
-        _r._check(_r.load().recis_embed_lookup(weight.data_ptr(), wt, V, D, _ptr(tokens), tokens.numel(), scale,
-                                               padding, _ptr(out), ot, stride, s), "recis_embed_lookup")
+    if _elsewhere(stream, weight, tokens, out):
+        with _on(stream, weight):
+            return embed_lookup(weight, tokens, scale, padding, out_dtype, out)
+    dev = weight.device
+    out = _out(out, "out", (*tokens.shape, D), out_dtype or (weight.dtype if out is None else out.dtype), dev)
+    ot = _type(out, "out")
+    _, _, stride = _rows(out, "out", D)
+    _r._check(_r.load().recis_embed_lookup(weight.data_ptr(), wt, V, D, _ptr(tokens), tokens.numel(), scale, padding,
+                                           _ptr(out), ot, stride, _raw(dev)), "recis_embed_lookup")
     return out
 
 
@@ -144,31 +162,32 @@ def embed_grad(tokens: torch.Tensor, grad_out: torch.Tensor, num_rows: int, scal
     `dtype` (fp32 by default).  accumulate: added to `out`."""
     gt = _type(grad_out, "grad_out")
     tokens = _int64(tokens, "tokens")
-    if tuple(grad_out.shape[:-1]) != tuple(tokens.shape) or grad_out.dim() != tokens.dim() + 1:
+    if grad_out.shape[:-1] != tokens.shape:
         raise ValueError(f"grad_out: expected {tuple(tokens.shape)} + [D], got {tuple(grad_out.shape)}")
     if accumulate and out is None:
         raise ValueError("accumulate needs the tensor to add to (out)")
-    _, D, stride = _rows(grad_out, "grad_out")
-    L = _r.load()
-    with _on(stream, grad_out, tokens, out) as s:
-        out = _out(out, "out", (num_rows, D), dtype or (torch.float32 if out is None else out.dtype), grad_out.device)
-        ot = _type(out, "out")
-        if not out.is_contiguous():
-            raise ValueError("out: expected a contiguous tensor")
-        nb = ctypes.c_int64()
-        _r._check(L.recis_embed_grad_workspace(tokens.numel(), num_rows, D, ctypes.byref(nb)),
-                  "recis_embed_grad_workspace")
-        ws = _scratch(nb.value, grad_out.device)
-        _r._check(L.recis_embed_grad(_ptr(tokens), tokens.numel(), _ptr(grad_out), gt, stride, num_rows, D, scale,
-                                     padding, 1 if accumulate else 0, out.data_ptr(), ot, _ptr(ws), nb.value, s),
-                  "recis_embed_grad")
+    _, D, grad_stride = _rows(grad_out, "grad_out")
+    if _elsewhere(stream, grad_out, tokens, out):
+        with _on(stream, grad_out):
+            return embed_grad(tokens, grad_out, num_rows, scale, padding, dtype, out, accumulate)
+    L, dev, n = _r.load(), grad_out.device, tokens.numel()
+    out = _out(out, "out", (num_rows, D), dtype or (torch.float32 if out is None else out.dtype), dev)
+    ot = _type(out, "out")
+    if not out.is_contiguous():
+        raise ValueError("out: expected a contiguous tensor")
+    nb = ctypes.c_int64()
+    _r._check(L.recis_embed_grad_workspace(n, num_rows, D, ctypes.byref(nb)), "recis_embed_grad_workspace")
+    ws = _scratch(nb.value, dev)
+    _r._check(L.recis_embed_grad(_ptr(tokens), n, _ptr(grad_out), gt, grad_stride, num_rows, D, scale, padding,
+                                 1 if accumulate else 0, out.data_ptr(), ot, _ptr(ws), nb.value, _raw(dev)),
+              "recis_embed_grad")
     return out
 
 
 # ------------------------------------------------------------------ layer norm
 def _norm_params(weight, bias, D):
     for t, name in ((weight, "weight"), (bias, "bias")):
-        if t is not None and (tuple(t.shape) != (D,) or not t.is_contiguous()):
+        if t is not None and (t.shape != (D,) or not t.is_contiguous()):
             raise ValueError(f"{name}: expected a contiguous [{D}] tensor, got {tuple(t.shape)}")
     if weight is not None and bias is not None and weight.dtype != bias.dtype:
         raise TypeError(f"weight and bias differ in type: {weight.dtype}, {bias.dtype}")
@@ -184,14 +203,16 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
     xt = _type(x, "x")
     M, D, xs = _rows(x, "x")
     wt = _norm_params(weight, bias, D)
-    with _on(stream, x, weight, bias, out) as s:
-        y = _out(out, "out", x.shape, out_dtype or (x.dtype if out is None else out.dtype), x.device)
-        yt = _type(y, "out")
-        ys = _rows(y, "out", D)[2]
-        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-        rstd = torch.empty_like(mean)
-        _r._check(_r.load().recis_layer_norm(_ptr(x), xt, xs, M, D, _ptr(weight), _ptr(bias), wt, eps, _ptr(y), yt, ys,
-                                             _ptr(mean), _ptr(rstd), s), "recis_layer_norm")
+    if _elsewhere(stream, x, weight, bias, out):
+        with _on(stream, x):
+            return layer_norm(x, weight, bias, eps, out_dtype, out)
+    dev = x.device
+    y = _out(out, "out", x.shape, out_dtype or (x.dtype if out is None else out.dtype), dev)
+    yt = _type(y, "out")
+    ys = _rows(y, "out", D)[2]
+    mean, rstd = torch.empty((2, *x.shape[:-1]), dtype=torch.float32, device=dev).unbind(0)
+    _r._check(_r.load().recis_layer_norm(_ptr(x), xt, xs, M, D, _ptr(weight), _ptr(bias), wt, eps, _ptr(y), yt, ys,
+                                         _ptr(mean), _ptr(rstd), _raw(dev)), "recis_layer_norm")
     return y, mean, rstd
 
 
@@ -202,41 +223,46 @@ def layer_norm_backward(grad_y: torch.Tensor, x: torch.Tensor, mean: torch.Tenso
     of weight's and bias's type, None where weight or bias is None."""
     xt, yt = _type(x, "x"), _type(grad_y, "grad_y")
     M, D, xs = _rows(x, "x")
-    if tuple(grad_y.shape) != tuple(x.shape):
+    if grad_y.shape != x.shape:
         raise ValueError(f"grad_y: expected {tuple(x.shape)}, got {tuple(grad_y.shape)}")
     gs = _rows(grad_y, "grad_y")[2]
     wt = _norm_params(weight, bias, D)
     for t, name in ((mean, "mean"), (rstd, "rstd")):
-        if t.dtype != torch.float32 or tuple(t.shape) != tuple(x.shape[:-1]) or not t.is_contiguous():
+        if t.dtype != torch.float32 or t.shape != x.shape[:-1] or not t.is_contiguous():
             raise ValueError(f"{name}: expected contiguous {tuple(x.shape[:-1])} of {torch.float32}")
-    L = _r.load()
-    with _on(stream, x, grad_y, mean, rstd, weight, bias, grad_x) as s:
-        gx = _out(grad_x, "grad_x", x.shape, x.dtype, x.device)
-        gxs = _rows(gx, "grad_x", D)[2]
-        gw = None if weight is None else torch.empty_like(weight)
-        gb = None if bias is None else torch.empty_like(bias)
-        nb = ctypes.c_int64()
-        _r._check(L.recis_layer_norm_backward_workspace(M, D, ctypes.byref(nb)),
-                  "recis_layer_norm_backward_workspace")
-        ws = _scratch(nb.value, x.device)
-        _r._check(L.recis_layer_norm_backward(_ptr(grad_y), yt, gs, _ptr(x), xt, xs, M, D, _ptr(weight), wt, _ptr(mean),
-                                              _ptr(rstd), _ptr(gx), gxs, _ptr(gw), _ptr(gb), _ptr(ws), nb.value, s),
-                  "recis_layer_norm_backward")
+    if _elsewhere(stream, x, grad_y, mean, rstd, weight, bias, grad_x):
+        with _on(stream, x):
+            return layer_norm_backward(grad_y, x, mean, rstd, weight, bias, grad_x)
+    L, dev = _r.load(), x.device
+    gx = _out(grad_x, "grad_x", x.shape, x.dtype, dev)
+    gxs = _rows(gx, "grad_x", D)[2]
+    gw = None if weight is None else torch.empty_like(weight)
+    gb = None if bias is None else torch.empty_like(bias)
+    nb = ctypes.c_int64()
+    _r._check(L.recis_layer_norm_backward_workspace(M, D, ctypes.byref(nb)), "recis_layer_norm_backward_workspace")
+    ws = _scratch(nb.value, dev)
+    _r._check(L.recis_layer_norm_backward(_ptr(grad_y), yt, gs, _ptr(x), xt, xs, M, D, _ptr(weight), wt, _ptr(mean),
+                                          _ptr(rstd), _ptr(gx), gxs, _ptr(gw), _ptr(gb), _ptr(ws), nb.value,
+                                          _raw(dev)), "recis_layer_norm_backward")
     return gx, gw, gb
 
 
 # ------------------------------------------------------------------ attention
-def _heads(t: torch.Tensor, name: str, like: torch.Tensor, shape=None):
+_ATTEND_TYPES = {torch.bfloat16: 1, torch.float16: 2}
+
+
+def _heads(t: torch.Tensor, name: str, dtype, shape=None):
     """(row stride, head stride) of a [rows, heads, D] tensor."""
-    if t.dim() != 3 or (shape is not None and tuple(t.shape) != tuple(shape)):
+    if t.dim() != 3 or (shape is not None and t.shape != shape):
         raise ValueError(f"{name}: expected {'[rows, heads, D]' if shape is None else tuple(shape)}, "
                          f"got {tuple(t.shape)}")
-    if t.dtype != like.dtype:
-        raise TypeError(f"{name}: expected {like.dtype}, got {t.dtype}")
-    if t.stride(2) != 1 and t.shape[2] > 1:
-        raise ValueError(f"{name}: the elements of a head must be contiguous")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     T, H, D = t.shape
-    return (t.stride(0) if T > 1 else H * D), (t.stride(1) if H > 1 else D)
+    a, b, c = t.stride()
+    if c != 1 and D > 1:
+        raise ValueError(f"{name}: the elements of a head must be contiguous")
+    return (a if T > 1 else H * D), (b if H > 1 else D)
 
 
 def _written(t: torch.Tensor, name: str, strides):
@@ -249,25 +275,25 @@ def _written(t: torch.Tensor, name: str, strides):
 
 
 def _attend_args(q, k, v, q_offsets, k_offsets, max_q, max_k, scale, key_mask):
-    a = AttendArgs(type=_type(q, "q", {torch.bfloat16: 1, torch.float16: 2}))
-    a.q_stride, a.q_head_stride = _heads(q, "q", q)
-    a.k_stride, a.k_head_stride = _heads(k, "k", q)
-    a.v_stride, a.v_head_stride = _heads(v, "v", q, k.shape)
-    a.Tq, a.Hq, a.D = q.shape
-    a.Tk, a.Hkv, _ = k.shape
-    if k.shape[2] != a.D or a.Hkv == 0 or a.Hq % a.Hkv or a.Hq == 0:
+    dtype = q.dtype
+    kind = _type(q, "q", _ATTEND_TYPES)
+    qs, qh = _heads(q, "q", dtype)
+    ks, kh = _heads(k, "k", dtype)
+    vs, vh = _heads(v, "v", dtype, k.shape)
+    Tq, Hq, D = q.shape
+    Tk, Hkv, Dk = k.shape
+    if Dk != D or Hkv == 0 or Hq == 0 or Hq % Hkv:
         raise ValueError(f"k: heads of {tuple(k.shape)} do not fit q's {tuple(q.shape)}")
+    n = q_offsets.numel()
     for t, name in ((q_offsets, "q_offsets"), (k_offsets, "k_offsets")):
-        if _int64(t, name).dim() != 1 or t.numel() < 1 or t.numel() != q_offsets.numel():
+        if _int64(t, name).dim() != 1 or n < 1 or t.numel() != n:
             raise ValueError(f"{name}: expected [B + 1] offsets, got {tuple(t.shape)}")
-    if key_mask is not None and (key_mask.dtype not in (torch.bool, torch.uint8) or tuple(key_mask.shape) != (a.Tk,)
+    if key_mask is not None and (key_mask.dtype not in (torch.bool, torch.uint8) or key_mask.shape != (Tk,)
                                  or not key_mask.is_contiguous()):
-        raise ValueError(f"key_mask: expected a contiguous [{a.Tk}] bool tensor")
-    a.B, a.max_q, a.max_k = q_offsets.numel() - 1, max_q, max_k
-    a.scale = float(a.D) ** -0.5 if scale is None else scale
-    a.q_offsets, a.k_offsets, a.key_mask = q_offsets.data_ptr(), k_offsets.data_ptr(), _ptr(key_mask)
-    a.q, a.k, a.v = _ptr(q), _ptr(k), _ptr(v)
-    return a
+        raise ValueError(f"key_mask: expected a contiguous [{Tk}] bool tensor")
+    return AttendArgs(kind, D, Hq, Hkv, n - 1, Tq, Tk, max_q, max_k, float(D) ** -0.5 if scale is None else scale,
+                      q_offsets.data_ptr(), k_offsets.data_ptr(), _ptr(key_mask), _ptr(q), _ptr(k), _ptr(v),
+                      qs, qh, ks, kh, vs, vh)
 
 
 def attend(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_offsets: torch.Tensor, k_offsets: torch.Tensor,
@@ -279,19 +305,23 @@ def attend(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_offsets: torch.T
     default; key_mask: bool [Tk], False keys take no part.  Rows of no bag are
     left as they are in `out` and `lse` where given, undefined in new ones."""
     a = _attend_args(q, k, v, q_offsets, k_offsets, max_q, max_k, scale, key_mask)
-    L = _r.load()
-    with _on(stream, q, k, v, q_offsets, k_offsets, key_mask, out, lse) as s:
-        out = _out(out, "out", q.shape, q.dtype, q.device)
-        a.out_stride, a.out_head_stride = _heads(out, "out", q)
+    if _elsewhere(stream, q, k, v, q_offsets, k_offsets, key_mask, out, lse):
+        with _on(stream, q):
+            return attend(q, k, v, q_offsets, k_offsets, max_q, max_k, scale, key_mask, out, lse)
+    L, dev = _r.load(), q.device
+    given = out is not None
+    out = _out(out, "out", q.shape, q.dtype, dev)
+    a.out_stride, a.out_head_stride = _heads(out, "out", q.dtype)
+    if given:
         _written(out, "out", (a.out_stride, a.out_head_stride))
-        lse = _out(lse, "lse", q.shape[:2], torch.float32, q.device)
-        if not lse.is_contiguous():
-            raise ValueError("lse: expected a contiguous tensor")
-        a.out, a.lse = _ptr(out), _ptr(lse)
-        nb = ctypes.c_int64()
-        _r._check(L.recis_attend_workspace(ctypes.byref(a), 0, ctypes.byref(nb)), "recis_attend_workspace")
-        ws = _scratch(nb.value, q.device)
-        _r._check(L.recis_attend(ctypes.byref(a), _ptr(ws), nb.value, s), "recis_attend")
+    lse = _out(lse, "lse", q.shape[:2], torch.float32, dev)
+    if not lse.is_contiguous():
+        raise ValueError("lse: expected a contiguous tensor")
+    a.out, a.lse = _ptr(out), _ptr(lse)
+    nb, ref = ctypes.c_int64(), ctypes.byref(a)
+    _r._check(L.recis_attend_workspace(ref, 0, ctypes.byref(nb)), "recis_attend_workspace")
+    ws = _scratch(nb.value, dev)
+    _r._check(L.recis_attend(ref, _ptr(ws), nb.value, _raw(dev)), "recis_attend")
     return out, lse
 
 
@@ -304,26 +334,32 @@ def attend_backward(grad_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v:
     out and lse, and out's gradient.  Rows of no bag are left as they are in
     the gradients where given, undefined in new ones."""
     a = _attend_args(q, k, v, q_offsets, k_offsets, max_q, max_k, scale, key_mask)
-    a.out_stride, a.out_head_stride = _heads(out, "out", q, q.shape)
-    a.grad_out_stride, a.grad_out_head_stride = _heads(grad_out, "grad_out", q, q.shape)
-    if lse.dtype != torch.float32 or tuple(lse.shape) != tuple(q.shape[:2]) or not lse.is_contiguous():
+    dtype = q.dtype
+    a.out_stride, a.out_head_stride = _heads(out, "out", dtype, q.shape)
+    a.grad_out_stride, a.grad_out_head_stride = _heads(grad_out, "grad_out", dtype, q.shape)
+    if lse.dtype != torch.float32 or lse.shape != q.shape[:2] or not lse.is_contiguous():
         raise ValueError(f"lse: expected contiguous {tuple(q.shape[:2])} of {torch.float32}")
-    L = _r.load()
-    with _on(stream, q, k, v, out, lse, grad_out, q_offsets, k_offsets, key_mask, grad_q, grad_k, grad_v) as s:
-        grads = []
-        for t, name, like in ((grad_q, "grad_q", q), (grad_k, "grad_k", k), (grad_v, "grad_v", v)):
-            t = _out(t, name, like.shape, q.dtype, q.device)
-            strides = _heads(t, name, q)
-            _written(t, name, strides)
-            setattr(a, name + "_stride", strides[0])
-            setattr(a, name + "_head_stride", strides[1])
-            setattr(a, name, _ptr(t))
-            grads.append(t)
-        a.out, a.lse, a.grad_out = _ptr(out), _ptr(lse), _ptr(grad_out)
-        nb = ctypes.c_int64()
-        _r._check(L.recis_attend_workspace(ctypes.byref(a), 1, ctypes.byref(nb)), "recis_attend_workspace")
-        ws = _scratch(nb.value, q.device)
-        _r._check(L.recis_attend_backward(ctypes.byref(a), _ptr(ws), nb.value, s), "recis_attend_backward")
+    if _elsewhere(stream, q, k, v, out, lse, grad_out, q_offsets, k_offsets, key_mask, grad_q, grad_k, grad_v):
+        with _on(stream, q):
+            return attend_backward(grad_out, q, k, v, out, lse, q_offsets, k_offsets, max_q, max_k, scale, key_mask,
+                                   grad_q, grad_k, grad_v)
+    L, dev = _r.load(), q.device
+    grads, strides = [], []
+    for t, name, like in ((grad_q, "grad_q", q), (grad_k, "grad_k", k), (grad_v, "grad_v", v)):
+        g = _out(t, name, like.shape, dtype, dev)
+        st = _heads(g, name, dtype)
+        if t is not None:
+            _written(g, name, st)
+        grads.append(g)
+        strides.append(st)
+    a.out, a.lse, a.grad_out = _ptr(out), _ptr(lse), _ptr(grad_out)
+    a.grad_q, a.grad_k, a.grad_v = _ptr(grads[0]), _ptr(grads[1]), _ptr(grads[2])
+    ((a.grad_q_stride, a.grad_q_head_stride), (a.grad_k_stride, a.grad_k_head_stride),
+     (a.grad_v_stride, a.grad_v_head_stride)) = strides
+    nb, ref = ctypes.c_int64(), ctypes.byref(a)
+    _r._check(L.recis_attend_workspace(ref, 1, ctypes.byref(nb)), "recis_attend_workspace")
+    ws = _scratch(nb.value, dev)
+    _r._check(L.recis_attend_backward(ref, _ptr(ws), nb.value, _raw(dev)), "recis_attend_backward")
     return tuple(grads)
 
 
