@@ -27,7 +27,8 @@ __device__ int g_seq_status;
 constexpr int kSmallN = 1024;     // up to here one kernel finds and sums each token's rows
 constexpr int kSortThreads = 256;
 constexpr int kMaxDigit = 10;     // bits a pass sorts by
-constexpr int kSpan = 64;         // sorted positions a group of lanes walks
+constexpr int kMaxSpan = 64;      // sorted positions a group of lanes walks: 16, 32 or 64
+constexpr int kMaxSpans = 64;     // spans a block takes
 
 __host__ __device__ constexpr int64_t align256(int64_t b) { return (b + 255) & ~(int64_t)255; }
 
@@ -43,41 +44,44 @@ struct LookupParams {
 };
 
 // `lanes` threads walk the columns of R rows at once, so R independent row
-// loads a thread are in flight.
+// loads a thread are in flight; the next rows' tokens are read meanwhile.
 template <typename TW, typename TO, int VEC, int R>
-__global__ void __launch_bounds__(256) embed_lookup_kernel(const __grid_constant__ LookupParams p) {
+__global__ void __launch_bounds__(256, R == 1 ? 6 : 4) embed_lookup_kernel(const __grid_constant__ LookupParams p) {
   const int lane = threadIdx.x & (p.lanes - 1);
-  const int64_t group = ((int64_t)blockIdx.x * 256 + threadIdx.x) / p.lanes;
-  const int64_t groups = (int64_t)gridDim.x * 256 / p.lanes;
-  for (int64_t r0 = group * R; r0 < p.N; r0 += groups * R) {
-    int64_t t[R];
+  const int64_t step = (int64_t)gridDim.x * (256 / p.lanes) * R;
+  int64_t r0 = ((int64_t)blockIdx.x * (256 / p.lanes) + threadIdx.x / p.lanes) * R;
+  int64_t t[R];
+  auto tokens = [&](int64_t r) {
 #pragma unroll
-    for (int r = 0; r < R; ++r) t[r] = r0 + r < p.N ? __ldg(p.tok + r0 + r) : p.padding;
+    for (int i = 0; i < R; ++i) t[i] = r + i < p.N ? __ldg(p.tok + r + i) : p.padding;
+  };
+  tokens(r0);
+  for (; r0 < p.N; r0 += step) {
+    int row[R];  // -1: zeros
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      if (t[r] == p.padding) t[r] = -1;
-      else if (t[r] < 0 || t[r] >= p.V) {
-        if (lane == 0) atomicOr(p.status, kErrTagOverflow);
-        t[r] = -1;
-      }
+    for (int i = 0; i < R; ++i) {
+      row[i] = t[i] >= 0 && t[i] < p.V && t[i] != p.padding ? (int)t[i] : -1;
+      if (row[i] < 0 && t[i] != p.padding && lane == 0) atomicOr(p.status, kErrTagOverflow);
     }
+    tokens(r0 + step);
     for (int c = lane; c < p.units; c += p.lanes) {
       RawVec<TW, VEC> v[R];
 #pragma unroll
-      for (int r = 0; r < R; ++r)
-        if (t[r] >= 0) v[r].load(static_cast<const TW*>(p.w) + t[r] * p.D + (int64_t)c * VEC);
+      for (int i = 0; i < R; ++i)
+        if (row[i] >= 0) v[i].load(static_cast<const TW*>(p.w) + (int64_t)row[i] * p.D + c * VEC);
+      TO* out = static_cast<TO*>(p.out) + r0 * p.out_stride + c * VEC;
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        if (r0 + r >= p.N) break;
+      for (int i = 0; i < R; ++i) {
+        if (r0 + i >= p.N) break;
         float f[VEC];
 #pragma unroll
         for (int j = 0; j < VEC; ++j) f[j] = 0.f;
-        if (t[r] >= 0) {
-          v[r].unpack(f);
+        if (row[i] >= 0) {
+          v[i].unpack(f);
 #pragma unroll
           for (int j = 0; j < VEC; ++j) f[j] *= p.scale;
         }
-        store_vec(static_cast<TO*>(p.out) + (r0 + r) * p.out_stride + (int64_t)c * VEC, f);
+        store_vec(out + i * p.out_stride, f);
       }
     }
   }
@@ -91,7 +95,7 @@ cudaError_t lookup_launch(LookupParams p, cudaStream_t s) {
   // four rows a group once that still fills the machine; one row each below
   const bool many = p.N / 4 * p.lanes >= (int64_t)kSMs * 1024;
   const int64_t groups = many ? (p.N + 3) / 4 : p.N;
-  const int64_t blocks = std::min<int64_t>((groups * p.lanes + 255) / 256, (int64_t)1 << 30);
+  const int64_t blocks = std::min<int64_t>((groups * p.lanes + 255) / 256, kSMs * (many ? 4 : 6));
   LaunchScope ls("embed_lookup", s);
   if (many) embed_lookup_kernel<TW, TO, VEC, 4><<<(unsigned)blocks, 256, 0, s>>>(p);
   else embed_lookup_kernel<TW, TO, VEC, 1><<<(unsigned)blocks, 256, 0, s>>>(p);
@@ -139,8 +143,8 @@ struct PassParams {
 
 template <int ITEMS>
 __device__ __forceinline__ uint2 pass_item(const PassParams& p, int64_t i, bool report) {
-  if (p.in) return p.in[i];
-  return make_uint2(sort_key(p.tok[i], p.V, p.padding, p.status, report), (uint32_t)i);
+  if (p.in) return __ldg(p.in + i);
+  return make_uint2(sort_key(__ldg(p.tok + i), p.V, p.padding, p.status, report), (uint32_t)i);
 }
 
 // digit counts of each tile
@@ -157,11 +161,15 @@ __global__ void __launch_bounds__(kSortThreads) grad_count_kernel(const __grid_c
   for (int b = threadIdx.x; b < bins; b += kSortThreads) s_h[b] = 0;
   __syncthreads();
   const int64_t base = (int64_t)blockIdx.x * (kSortThreads * ITEMS);
+  uint32_t key[ITEMS];
 #pragma unroll
   for (int j = 0; j < ITEMS; ++j) {
     const int64_t i = base + j * kSortThreads + threadIdx.x;
-    if (i < p.N) atomicAdd(&s_h[(pass_item<ITEMS>(p, i, true).x >> p.shift) & (bins - 1)], 1u);
+    key[j] = i < p.N ? pass_item<ITEMS>(p, i, true).x : 0;
   }
+#pragma unroll
+  for (int j = 0; j < ITEMS; ++j)
+    if (base + j * kSortThreads + threadIdx.x < p.N) atomicAdd(&s_h[(key[j] >> p.shift) & (bins - 1)], 1u);
   __syncthreads();
   pdl_trigger();
   for (int b = threadIdx.x; b < bins; b += kSortThreads) p.hist[(size_t)blockIdx.x * bins + b] = s_h[b];
@@ -182,6 +190,7 @@ __global__ void __launch_bounds__(1024) grad_scan_kernel(const __grid_constant__
   }
   uint32_t sum = 0;
   if (b < bins)
+#pragma unroll 8
     for (int t = t0; t < t1; ++t) sum += p.hist[(size_t)t * bins + b];
   s_part[w][lane] = sum;
   __syncthreads();
@@ -214,12 +223,21 @@ __global__ void __launch_bounds__(kSortThreads) grad_scatter_kernel(const __grid
     zero_block(p.zero[2], blockIdx.x - p.tiles);
     return;
   }
+  // the tile's keys and counts, all in flight at once
+  const int64_t base = (int64_t)blockIdx.x * (kSortThreads * ITEMS) + (int64_t)w * 32 * ITEMS + lane;
+  uint2 v[ITEMS];
+#pragma unroll
+  for (int j = 0; j < ITEMS; ++j)
+    v[j] = base + j * 32 < p.N ? pass_item<ITEMS>(p, base + j * 32, false) : make_uint2(0, 0);
   // exclusive scan of the digit totals: 4 (at most) consecutive bins a thread
-  const int per = (bins + kSortThreads - 1) / kSortThreads;
-  uint32_t mine = 0;
-  for (int j = 0; j < per; ++j) {
-    const int b = tid * per + j;
-    if (b < bins) mine += p.total[b];
+  constexpr int kPer = (1 << kMaxDigit) / kSortThreads;
+  uint32_t tot[kPer], pre[kPer], mine = 0;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const int b = tid * kPer + j;
+    tot[j] = b < bins ? __ldg(p.total + b) : 0;
+    pre[j] = b < bins ? __ldg(p.hist + (size_t)blockIdx.x * bins + b) : 0;
+    mine += tot[j];
   }
   uint32_t x = mine;
 #pragma unroll
@@ -231,26 +249,25 @@ __global__ void __launch_bounds__(kSortThreads) grad_scatter_kernel(const __grid
   __syncthreads();
   uint32_t run = x - mine;
   for (int q = 0; q < w; ++q) run += s_w[q];
-  for (int j = 0; j < per; ++j) {
-    const int b = tid * per + j;
-    if (b < bins) {
-      s_base[b] = run + p.hist[(size_t)blockIdx.x * bins + b];
-      run += p.total[b];
-    }
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const int b = tid * kPer + j;
+    if (b < bins) s_base[b] = run + pre[j];
+    run += tot[j];
   }
   // ranks within the warp's keys, in order
-  const int64_t base = (int64_t)blockIdx.x * (kSortThreads * ITEMS) + (int64_t)w * 32 * ITEMS + lane;
   uint32_t* cnt = s_cnt + w * bins;
-  uint2 v[ITEMS];
   uint32_t rank[ITEMS];
-#pragma unroll
-  for (int j = 0; j < ITEMS; ++j)
-    v[j] = base + j * 32 < p.N ? pass_item<ITEMS>(p, base + j * 32, false) : make_uint2(0, 0);
 #pragma unroll
   for (int j = 0; j < ITEMS; ++j) {
     const bool ok = base + j * 32 < p.N;
     const uint32_t d = (v[j].x >> p.shift) & (bins - 1);
-    const unsigned peers = __match_any_sync(0xffffffffu, ok ? d : 0xffffffffu);
+    unsigned peers = __ballot_sync(0xffffffffu, ok);
+    for (int b = 0; b < p.bits; ++b) {
+      const unsigned m = __ballot_sync(0xffffffffu, d >> b & 1);
+      peers &= (d >> b & 1) ? m : ~m;
+    }
+    if (!ok) peers = 0;
     const uint32_t before = ok ? cnt[d] : 0;
     rank[j] = before + __popc(peers & ((1u << lane) - 1u));
     __syncwarp();
@@ -259,11 +276,13 @@ __global__ void __launch_bounds__(kSortThreads) grad_scatter_kernel(const __grid
   }
   __syncthreads();
   for (int b = tid; b < bins; b += kSortThreads) {
-    uint32_t at = s_base[b];
+    uint32_t at = s_base[b], c[kWarps];
+#pragma unroll
+    for (int q = 0; q < kWarps; ++q) c[q] = s_cnt[q * bins + b];
+#pragma unroll
     for (int q = 0; q < kWarps; ++q) {
-      const uint32_t c = s_cnt[q * bins + b];
       s_cnt[q * bins + b] = at;
-      at += c;
+      at += c[q];
     }
   }
   __syncthreads();
@@ -282,8 +301,10 @@ struct SumParams {
   float* partial;       // [spans][2][D]: parts of runs that the join adds up, 0 begun before the span, 1 in it
   int2* list;           // those runs' first spans and tokens, *listed of them
   int* listed;
+  int* run_last;        // [V]: the span each of them ends in, by token
   int64_t N, V, g_stride, padding;
   int D, units, lanes;
+  int span, spb;        // positions a span; spans a block
   int accumulate;
   float scale;
   int* status;
@@ -308,73 +329,76 @@ __device__ __forceinline__ void grad_store(const SumParams& p, int64_t row, int 
 }
 
 // One group of `lanes` lanes (at most a warp) walks one span; blockIdx.y picks
-// the group's columns.  Rows are loaded 8 at a time, all in flight.  A run
-// belongs to the span it begins in; one that ends in the next span is finished
-// by its owner (the next span's group passes over it), one that goes on further
-// is listed and left in parts.
+// the group's columns.  The block's sorted pairs are brought to shared memory
+// at once, so that a group's row loads, 8 at a time, wait for nothing else.  A
+// run belongs to the span it begins in; one that ends in the next span is
+// finished by its owner (the next span's group passes over it), one that goes
+// on further is listed and left in parts.
 template <typename TG, typename TO, int VEC>
-__global__ void __launch_bounds__(256) grad_span_kernel(const __grid_constant__ SumParams p) {
+__global__ void __launch_bounds__(256, 3) grad_span_kernel(const __grid_constant__ SumParams p) {
   constexpr int U = 8;
-  const int lane = threadIdx.x & (p.lanes - 1);
-  const int64_t span = ((int64_t)blockIdx.x * 256 + threadIdx.x) / p.lanes;
-  const int64_t p0 = span * kSpan;
-  const int c = blockIdx.y * p.lanes + lane;
-  pdl_wait();
-  if (p0 >= p.N) return;
-  const int64_t p1 = p0 + kSpan < p.N ? p0 + kSpan : p.N, p2 = p1 + kSpan < p.N ? p1 + kSpan : p.N;
-  const bool in = c < p.units;
+  // pairs from one span and a position before the block's first span to one span behind its last
+  __shared__ uint2 s_pair[(kMaxSpans + 2) * kMaxSpan + 2];
+  const int lane = threadIdx.x & (p.lanes - 1), S = p.span;
+  const int64_t b0 = (int64_t)blockIdx.x * p.spb * S, lo = b0 - S - 1;
   const uint32_t none = (uint32_t)p.V;  // key of positions without a row
+  pdl_wait();
+  for (int i = threadIdx.x; i < (p.spb + 2) * S + 2; i += blockDim.x) {
+    const int64_t at = lo + i;
+    s_pair[i] = at >= 0 && at < p.N ? __ldg(p.pairs + at) : make_uint2(none, 0);
+  }
+  __syncthreads();
+  const int64_t span = (int64_t)blockIdx.x * p.spb + threadIdx.x / p.lanes;
+  const int64_t p0 = span * S;
+  if (p0 >= p.N) return;
+  const uint2* pr = s_pair + (p0 - lo);  // pr[i]: position p0 + i, -S - 1 <= i <= 2 S
+  const int len = p.N - p0 < S ? (int)(p.N - p0) : S;
+  const int c = blockIdx.y * p.lanes + lane;
+  const bool in = c < p.units;
   // the keys around the span's ends
-  const uint32_t first = p.pairs[p0].x, last = p.pairs[p1 - 1].x;
-  const uint32_t before = p0 > 0 ? p.pairs[p0 - 1].x : none, after = p1 < p.N ? p.pairs[p1].x : none;
-  const uint32_t after2 = p2 < p.N ? p.pairs[p2].x : none;
-  const uint32_t before2 = p0 > kSpan ? p.pairs[p0 - kSpan - 1].x : none;
+  const uint32_t first = pr[0].x, last = pr[len - 1].x, before = pr[-1].x, after = pr[len].x;
   // a run begun before the span: finished by its owner if that is the span
   // before and the run ends in this one; else this span's part of it
   const bool head = before == first && first < none;
-  const bool head_part = head && (after == first || before2 == first);
-  // the run that goes on past the span (begun in it, or before: then the span
-  // is all one run): finished here if it ends in the next span, else in parts
-  const bool tail = after == last && last < none;
-  const bool tail_mine = tail && !(head && last == first);
-  const bool tail_part = tail_mine && after2 == last;
-  const int64_t end = tail_mine && !tail_part ? p2 : p1;
+  const bool head_part = head && (after == first || pr[-S - 1].x == first);
+  // the run that goes on past the span, if it is this span's: finished here if
+  // it ends in the next span, else in parts
+  const bool tail = after == last && last < none && !(head && last == first);
+  const bool tail_part = tail && pr[2 * S].x == last;
+  const int end = tail && !tail_part ? 2 * S : len;
+  int q = 0;
+  if (head && !head_part)
+    while (q < len && pr[q].x == first) ++q;
+  bool in_head = head_part;
+  const TG* g = static_cast<const TG*>(p.g) + (int64_t)c * VEC;
   float acc[VEC];
 #pragma unroll
   for (int j = 0; j < VEC; ++j) acc[j] = 0.f;
-  uint32_t cur = first;
-  bool in_head = head;
-  bool done = false;  // past p1, beyond the run's end
-  for (int64_t q = p0; q < end && !done; q += U) {
-    uint2 e[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) e[u] = q + u < end ? __ldg(p.pairs + q + u) : make_uint2(none, 0);
+  uint32_t cur = q < len ? pr[q].x : none;
+  for (; q < end && cur < none; q += U) {
     RawVec<TG, VEC> r[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const bool use = e[u].x < none && (q + u < p1 || e[u].x == last) && !(head && !head_part && e[u].x == first);
-      if (!use) e[u].x = e[u].x == first && head ? first : (q + u < p1 ? e[u].x : none);
-      if (use && in) r[u].load(static_cast<const TG*>(p.g) + (int64_t)e[u].y * p.g_stride + (int64_t)c * VEC);
+      const uint2 e = q + u < end ? pr[q + u] : make_uint2(none, 0);
+      if (in && e.x < none) r[u].load(g + (int64_t)e.y * p.g_stride);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (q + u >= end) break;
-      if (e[u].x != cur) {  // the run of `cur` ends
-        if (in && cur < none) {
+      const uint32_t key = q + u < end ? pr[q + u].x : none;
+      if (key != cur) {  // the run of `cur` ends
+        if (q + u >= end) break;
+        if (in) {
           if (!in_head) grad_store<TO, VEC>(p, cur, c, acc);
-          else if (head_part) store_vec(p.partial + span * 2 * p.D + (int64_t)c * VEC, acc);
+          else store_vec(p.partial + span * 2 * p.D + (int64_t)c * VEC, acc);
         }
         in_head = false;
-        cur = e[u].x;
-        if (q + u >= p1) {
-          done = true;
-          cur = none;
-          break;
-        }
+        // past the span only its own last run is taken; keys without a row come last
+        cur = q + u < len ? key : none;
+        if (cur >= none) break;
 #pragma unroll
         for (int j = 0; j < VEC; ++j) acc[j] = 0.f;
       }
-      if (e[u].x < none && in && !(in_head && !head_part)) {
+      if (in) {
         float f[VEC];
         r[u].unpack(f);
 #pragma unroll
@@ -382,24 +406,25 @@ __global__ void __launch_bounds__(256) grad_span_kernel(const __grid_constant__ 
       }
     }
   }
+  // (a run in parts has one last span: where its head ends)
+  if (head_part && after != first && c == 0) p.run_last[first] = (int)span;
   if (cur >= none) return;
-  if (tail_part || (in_head && head_part)) {
+  if (tail_part || in_head) {
     if (in) store_vec(p.partial + (span * 2 + (tail_part ? 1 : 0)) * p.D + (int64_t)c * VEC, acc);
     if (tail_part && c == 0) p.list[atomicAdd(p.listed, 1)] = make_int2((int)span, (int)cur);
-  } else if (in && !in_head) {
+  } else if (in) {
     grad_store<TO, VEC>(p, cur, c, acc);
   }
 }
 
-// Adds the parts of the listed runs: a block takes a run, `512 / lanes` strided
-// groups of lanes add its spans' parts in fp64, four loads in flight, then the
-// groups' sums are added in group order.  The list's order, the only thing that
+// Adds the parts of the listed runs: a block takes a run, `256 / lanes` strided
+// groups of lanes add its spans' parts in fp64, eight loads in flight, then the
+// groups' sums are added in a fixed order.  The list's order, the only thing that
 // scheduling decides, does not enter the sums.
-constexpr int kJoinThreads = 512;
+constexpr int kJoinThreads = 256;
 template <typename TO, int VEC>
 __global__ void __launch_bounds__(kJoinThreads) grad_join_kernel(const __grid_constant__ SumParams p) {
-  __shared__ double s_sum[kJoinThreads][VEC];
-  const int64_t spans = (p.N + kSpan - 1) / kSpan;
+  __shared__ double s_sum[kJoinThreads / 32][32][VEC];
   const int lane = threadIdx.x & (p.lanes - 1), group = threadIdx.x / p.lanes, groups = kJoinThreads / p.lanes;
   const int c = blockIdx.y * p.lanes + lane;
   pdl_wait();
@@ -407,43 +432,43 @@ __global__ void __launch_bounds__(kJoinThreads) grad_join_kernel(const __grid_co
   for (int item = blockIdx.x; item < n; item += gridDim.x) {
     const int64_t span = p.list[item].x;
     const uint32_t key = (uint32_t)p.list[item].y;
-    // the span the run ends in: the first whose end the run does not pass; each
-    // round every thread tests one of kJoinThreads evenly spaced spans
-    int64_t lo = span + 1, hi = spans - 1;  // the answer lies in [lo, hi]
-    while (lo < hi) {
-      const int64_t stride = (hi - lo + kJoinThreads - 1) / kJoinThreads;
-      const int64_t at = lo + (int64_t)threadIdx.x * stride;
-      const bool passes = at < hi && p.pairs[(at + 1) * kSpan].x == key;
-      const int k = __syncthreads_count(passes);  // a run passes a prefix of the spans tested
-      if (k == 0) break;
-      const int64_t base = lo + (int64_t)(k - 1) * stride;
-      hi = hi < base + stride ? hi : base + stride;
-      lo = base + 1;
-    }
-    const int64_t last = lo;
+    const int64_t last = p.run_last[key];
     double sum[VEC];
 #pragma unroll
     for (int j = 0; j < VEC; ++j) sum[j] = 0.0;
     if (c < p.units) {
-#pragma unroll 4
-      for (int64_t t = span + group; t <= last; t += groups) {
-        RawVec<float, VEC> r;
-        r.load(p.partial + (t * 2 + (t == span ? 1 : 0)) * p.D + (int64_t)c * VEC);
-        float f[VEC];
-        r.unpack(f);
+      for (int64_t t0 = span + group; t0 <= last; t0 += 8 * groups) {
+        RawVec<float, VEC> r[8];
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) sum[j] += (double)f[j];
+        for (int u = 0; u < 8; ++u) {
+          const int64_t t = t0 + u * groups;
+          if (t <= last) r[u].load(p.partial + (t * 2 + (t == span ? 1 : 0)) * p.D + (int64_t)c * VEC);
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          if (t0 + u * groups > last) break;
+          float f[VEC];
+          r[u].unpack(f);
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) sum[j] += (double)f[j];
+        }
       }
     }
+    // the groups of a warp, then the warps
+    for (int off = p.lanes; off < 32; off <<= 1)
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) s_sum[threadIdx.x][j] = sum[j];
+      for (int j = 0; j < VEC; ++j) sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], off);
+    if ((threadIdx.x & 31) < p.lanes)
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) s_sum[threadIdx.x >> 5][lane][j] = sum[j];
     __syncthreads();
-    if (group == 0 && c < p.units) {
+    if (threadIdx.x < p.lanes && c < p.units) {
       float f[VEC];
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
         double t = 0.0;
-        for (int q = 0; q < groups; ++q) t += s_sum[q * p.lanes + lane][j];
+#pragma unroll
+        for (int q = 0; q < kJoinThreads / 32; ++q) t += s_sum[q][lane][j];
         f[j] = (float)t;
       }
       grad_store<TO, VEC>(p, key, c, f);
@@ -524,7 +549,8 @@ __global__ void __launch_bounds__(256) grad_small_kernel(const __grid_constant__
 // ---------------------------------------------------------------- gradient: host
 struct GradPlan {
   int items, tiles, passes, bits;  // the sort
-  int64_t pairs_bytes, hist_bytes, total_bytes, partial_bytes, list_bytes;
+  int span;
+  int64_t pairs_bytes, hist_bytes, total_bytes, partial_bytes, list_bytes, last_bytes;
   int64_t bytes;
 };
 
@@ -533,7 +559,11 @@ GradPlan grad_plan(int64_t N, int64_t V, int D) {
   if (N <= kSmallN) return g;
   int bits = 1;
   while (((int64_t)1 << bits) <= V) ++bits;  // keys 0 .. V
-  g.passes = (bits + kMaxDigit - 1) / kMaxDigit;
+  // a pass costs a block its bins as well as its keys: digits of at most 8 bits
+  // where there are keys for many blocks (1.5M tokens of 20 bits: see sort
+  // times in the header), of 10 where launches are what counts
+  const int most = N >= 400000 ? 8 : kMaxDigit;
+  g.passes = (bits + most - 1) / most;
   g.bits = (bits + g.passes - 1) / g.passes;
   if (g.bits < 5) g.bits = 5;  // the scan takes 32 bins at a time
   // 8 keys a thread once there are tiles for every SM, 4 below
@@ -543,10 +573,15 @@ GradPlan grad_plan(int64_t N, int64_t V, int D) {
   g.pairs_bytes = align256(N * 8);
   g.hist_bytes = align256(((int64_t)g.tiles << g.bits) * 4);
   g.total_bytes = align256(((int64_t)1 << g.bits) * 4 + 4);  // and the number of listed runs
-  const int64_t spans = (N + kSpan - 1) / kSpan;
+  // long spans leave fewer parts, short ones make enough groups to fill the
+  // machine (a group takes 8 columns a lane)
+  g.span = kMaxSpan;
+  while (g.span > 16 && N / g.span * ((D + 7) / 8) < (int64_t)kSMs * 2048) g.span /= 2;
+  const int64_t spans = (N + g.span - 1) / g.span;
   g.partial_bytes = align256(spans * 2 * D * 4);
   g.list_bytes = align256(spans * 8);
-  g.bytes = 2 * g.pairs_bytes + g.hist_bytes + g.total_bytes + g.partial_bytes + g.list_bytes;
+  g.last_bytes = align256(V * 4);
+  g.bytes = 2 * g.pairs_bytes + g.hist_bytes + g.total_bytes + g.partial_bytes + g.list_bytes + g.last_bytes;
   return g;
 }
 
@@ -624,8 +659,11 @@ cudaError_t grad_launch(SumParams p, const int64_t* tok, char* ws, cudaStream_t 
   p.pairs = pairs[(g.passes - 1) & 1];
   p.partial = reinterpret_cast<float*>(at);
   p.list = reinterpret_cast<int2*>(at + g.partial_bytes);
+  p.run_last = reinterpret_cast<int*>(at + g.partial_bytes + g.list_bytes);
   p.listed = pp.listed;
-  const int64_t spans = (p.N + kSpan - 1) / kSpan;
+  p.span = g.span;
+  const int64_t spans = (p.N + p.span - 1) / p.span;
+  p.spb = std::min(256 / p.lanes, kMaxSpans);
   const int cols = (p.units + p.lanes - 1) / p.lanes;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute pdl[1];
@@ -636,13 +674,13 @@ cudaError_t grad_launch(SumParams p, const int64_t* tok, char* ws, cudaStream_t 
   cfg.stream = s;
   {
     LaunchScope ls("embed_grad_span", s);
-    cfg.gridDim = dim3((unsigned)((spans * p.lanes + 255) / 256), (unsigned)cols);
-    cfg.blockDim = dim3(256);
+    cfg.gridDim = dim3((unsigned)((spans + p.spb - 1) / p.spb), (unsigned)cols);
+    cfg.blockDim = dim3((unsigned)(p.spb * p.lanes));
     if ((e = cudaLaunchKernelEx(&cfg, grad_span_kernel<TG, TO, VEC>, p)) != cudaSuccess) return e;
   }
-  if (spans > 2) {
+  if (spans > 2) {  // a run in parts covers a whole span between two others
     LaunchScope ls("embed_grad_join", s);
-    cfg.gridDim = dim3((unsigned)std::min<int64_t>(spans / 2, kSMs * 2), (unsigned)cols);
+    cfg.gridDim = dim3((unsigned)std::min<int64_t>(spans / 2, kSMs * 8), (unsigned)cols);
     cfg.blockDim = dim3(kJoinThreads);
     if ((e = cudaLaunchKernelEx(&cfg, grad_join_kernel<TO, VEC>, p)) != cudaSuccess) return e;
   }
