@@ -422,6 +422,8 @@ recis_status fill(const recis_attend_args* a, AttendParams* p, const AttendPlan&
   p->max_q = (int)std::max<int64_t>(a->max_q, 1); p->max_k = (int)std::max<int64_t>(a->max_k, 1);
   p->scale = (float)a->scale;
   p->scale_log2 = (float)(a->scale * 1.4426950408889634);
+  // a scale of 0 makes every score 0; 1e-30 does too, and keeps the -inf of keys that take no part
+  if (p->scale_log2 == 0.f) p->scale_log2 = 1e-30f;
   p->splits = g.splits;
   p->split_keys = g.split_keys;
   char* at = static_cast<char*>(ws);

@@ -59,15 +59,14 @@ __global__ void __launch_bounds__(BackCfg<DP>::kThreads, BackCfg<DP>::kBlocksPer
     attend_back_kernel(const __grid_constant__ AttendParams p, const __grid_constant__ BackMaps maps, int spin_max) {
   using C = BackCfg<DP>;
   constexpr int NB = C::kBuf, WG = C::kWG;
-  constexpr int kDelay = NB == 2 ? kNS - 2 : kNS - 1;  // tiles asked for ahead of the one that is finished
   extern __shared__ uint8_t s_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(s_raw) + 1023) & ~(uintptr_t)1023);
   uint8_t *x1 = base, *x2 = x1 + C::kXBytes, *y1 = x2 + C::kXBytes, *y2 = y1 + kNS * C::kYBytes;
   uint64_t* bar = reinterpret_cast<uint64_t*>(y2 + kNS * C::kYBytes);
   uint64_t *x_full = bar, *acc_full = bar + 1, *s_full = bar + 2, *e_full = s_full + NB;
   uint64_t *y_full = e_full + NB, *y_empty = y_full + kNS, *y_raw = y_empty + kNS;
-  float* s_lse = reinterpret_cast<float*>(y2 + kNS * C::kYBytes + 256);  // KEYS: [kNS][kY] lse * log2(e)
-  float* s_delta = s_lse + kNS * kY;                                     // KEYS: [kNS][kY]
+  float* s_lse = reinterpret_cast<float*>(y2 + kNS * C::kYBytes + 256);  // KEYS: [kNS][kY] -lse * log2(e)
+  float* s_delta = s_lse + kNS * kY;                                     // KEYS: [kNS][kY] -delta
   __shared__ uint32_t s_tmem;
   __shared__ uint32_t s_valid[kNS][2];  // queries: the streamed keys that take part
 
@@ -126,15 +125,58 @@ __global__ void __launch_bounds__(BackCfg<DP>::kThreads, BackCfg<DP>::kBlocksPer
         if (!KEYS) return ks + (j + 1) * kY > ke || p.mask != nullptr;
         return tq * gc < kY || (j / chunks + 1) * tq > bag.nq || (j % chunks + 1) * gc > p.G;
       };
+      // the lane's rows of a tile: lane and lane + 32
+      int rq[2], rg[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        rq[i] = (lane + 32 * i) / gc;
+        rg[i] = (lane + 32 * i) % gc;
+      }
       int asked = 0;
-      for (int j = 0; j < n + kDelay && ok; ++j) {
+      bool v[2];                     // of the tile asked for last: the lane's rows take part,
+      float lse[2], delta[2];        // and their -lse and -delta
+      // a tile is asked for, and finished one step later: its rows' lse and
+      // delta are under way meanwhile, and no tile waits for a later one's slot
+      for (int j = 0; j <= n; ++j) {
+        if (j > 0) {
+          const int f = j - 1, st = f % kNS;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if (KEYS) {
+              // a row without keys (lse -inf) or of no query: p = 0
+              s_lse[st * kY + lane + 32 * i] = v[i] && lse[i] != INFINITY ? lse[i] * 1.4426950408889634f : -INFINITY;
+              s_delta[st * kY + lane + 32 * i] = v[i] ? delta[i] : 0.f;
+            } else {
+              const unsigned bits = __ballot_sync(0xffffffffu, v[i]);
+              if (lane == 0) s_valid[st][i] = bits;
+            }
+          }
+          if (special(f)) {
+            ok = mbar_wait(y_raw + st, (f / kNS) & 1, spin_max);  // every tile of a stage's turn completes this phase
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              if (!v[i])
+                for (int k = 0; k < C::kBlocks; ++k) {
+                  uint4* a = reinterpret_cast<uint4*>(y1 + st * C::kYBytes + (k * kY + lane + 32 * i) * 128);
+                  uint4* c = reinterpret_cast<uint4*>(y2 + st * C::kYBytes + (k * kY + lane + 32 * i) * 128);
+#pragma unroll
+                  for (int u = 0; u < 8; ++u) a[u] = c[u] = make_uint4(0, 0, 0, 0);
+                }
+            fence_async_smem();
+          } else if (lane == 0) {
+            mbar_arrive(y_raw + st);  // keeps the stage's phases in step
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(y_full + st);
+        }
         if (j < n) {
           const int st = j % kNS;
-          if (j >= kNS) ok = mbar_wait(y_empty + st, ((j / kNS) & 1) ^ 1, spin_max);
+          if (j >= kNS) ok = mbar_wait(y_empty + st, ((j / kNS) & 1) ^ 1, spin_max) && ok;
           if (!__all_sync(0xffffffffu, ok)) {
             ok = false;
             break;
           }
+          const int jq = KEYS ? (j / chunks) * tq : 0, jg = KEYS ? (j % chunks) * gc : 0;
           if (lane == 0) {
             uint64_t* full = y_full + st;
             if (special(j)) {
@@ -143,58 +185,30 @@ __global__ void __launch_bounds__(BackCfg<DP>::kThreads, BackCfg<DP>::kBlocksPer
             }
             const int rows = KEYS ? tq * gc : kY;
             mbar_arrive_expect(full, (unsigned)(2 * C::kBlocks * rows * 128));
-            const int y = KEYS ? h * p.G + (j % chunks) * gc : h;
-            const int z = KEYS ? (int)(bag.q0 + (j / chunks) * tq) : (int)(bag.k0 + ks + j * kY);
+            const int y = KEYS ? h * p.G + jg : h;
+            const int z = KEYS ? (int)(bag.q0 + jq) : (int)(bag.k0 + ks + j * kY);
             for (int i = 0; i < C::kBlocks; ++i) {
               tma_load3(y1 + st * C::kYBytes + i * kY * 128, &maps.y1, 64 * i, y, z, full);
               tma_load3(y2 + st * C::kYBytes + i * kY * 128, &maps.y2, 64 * i, y, z, full);
             }
           }
           asked = j + 1;
-        }
-        const int f = j - kDelay;
-        if (f < 0) continue;
-        const int st = f % kNS;
-        bool v[2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int r = lane + 32 * i;
-          if (KEYS) {
-            const int q = (f / chunks) * tq + r / gc, g = (f % chunks) * gc + r % gc;
-            v[i] = r < tq * gc && q < bag.nq && g < p.G;
-            float lse = INFINITY, delta = 0.f;
-            if (v[i]) {
-              const int64_t at = (bag.q0 + q) * p.Hq + h * p.G + g;
-              lse = __ldg(p.lse + at) * 1.4426950408889634f;
-              if (lse == -INFINITY) lse = INFINITY;  // a row without keys: p = 0
-              delta = __ldg(p.delta + at);
+          for (int i = 0; i < 2; ++i) {
+            if (KEYS) {
+              const int q = jq + rq[i], g = jg + rg[i];
+              v[i] = rq[i] < tq && q < bag.nq && g < p.G;
+              if (v[i]) {
+                const int64_t at = (bag.q0 + q) * p.Hq + h * p.G + g;
+                lse[i] = -__ldg(p.lse + at);
+                delta[i] = -__ldg(p.delta + at);
+              }
+            } else {
+              const int key = ks + j * kY + lane + 32 * i;
+              v[i] = key < ke && (!p.mask || p.mask[bag.k0 + key]);
             }
-            s_lse[st * kY + r] = lse;
-            s_delta[st * kY + r] = delta;
-          } else {
-            const int key = ks + f * kY + r;
-            v[i] = key < ke && (!p.mask || p.mask[bag.k0 + key]);
-            const unsigned bits = __ballot_sync(0xffffffffu, v[i]);
-            if (lane == 0) s_valid[st][i] = bits;
           }
         }
-        if (special(f)) {
-          ok = mbar_wait(y_raw + st, (f / kNS) & 1, spin_max);  // every tile of a stage's turn completes this phase
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            if (!v[i])
-              for (int k = 0; k < C::kBlocks; ++k) {
-                uint4* a = reinterpret_cast<uint4*>(y1 + st * C::kYBytes + (k * kY + lane + 32 * i) * 128);
-                uint4* c = reinterpret_cast<uint4*>(y2 + st * C::kYBytes + (k * kY + lane + 32 * i) * 128);
-#pragma unroll
-                for (int u = 0; u < 8; ++u) a[u] = c[u] = make_uint4(0, 0, 0, 0);
-              }
-          fence_async_smem();
-        } else if (lane == 0) {
-          mbar_arrive(y_raw + st);  // keeps the stage's phases in step
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(y_full + st);
       }
       // copies in flight end before the block does
       ok = mbar_wait(x_full, 0, spin_max) && ok;
@@ -250,7 +264,7 @@ __global__ void __launch_bounds__(BackCfg<DP>::kThreads, BackCfg<DP>::kBlocksPer
     bool live;
     int64_t t;       // its row in memory
     int hx;          // its head
-    float lse = INFINITY, delta = 0.f;
+    float lse = -INFINITY, delta = 0.f;  // queries: the row's -lse * log2(e) and -delta
     if (KEYS) {
       live = first + row < bag.nk;
       t = bag.k0 + first + row;
@@ -260,9 +274,9 @@ __global__ void __launch_bounds__(BackCfg<DP>::kThreads, BackCfg<DP>::kBlocksPer
       t = bag.q0 + first + row / p.G;
       hx = h * p.G + row % p.G;
       if (live) {
-        lse = p.lse[t * p.Hq + hx] * 1.4426950408889634f;
-        if (lse == -INFINITY) lse = INFINITY;
-        delta = p.delta[t * p.Hq + hx];
+        lse = -p.lse[t * p.Hq + hx] * 1.4426950408889634f;
+        if (lse == INFINITY) lse = -INFINITY;  // a row without keys: p = 0
+        delta = -p.delta[t * p.Hq + hx];
       }
     }
     const bool any = __any_sync(0xffffffffu, live);
@@ -293,25 +307,25 @@ __global__ void __launch_bounds__(BackCfg<DP>::kThreads, BackCfg<DP>::kBlocksPer
               ls = *reinterpret_cast<const float4*>(s_lse + st * kY + col + i);
               de = *reinterpret_cast<const float4*>(s_delta + st * kY + col + i);
             }
-            float e[4], f[4];
-            e[0] = ex2(fmaf(__uint_as_float(s[i]), c, -ls.x));
-            e[1] = ex2(fmaf(__uint_as_float(s[i + 1]), c, -ls.y));
-            e[2] = ex2(fmaf(__uint_as_float(s[i + 2]), c, -ls.z));
-            e[3] = ex2(fmaf(__uint_as_float(s[i + 3]), c, -ls.w));
-            f[0] = e[0] * (__uint_as_float(d[i]) - de.x);
-            f[1] = e[1] * (__uint_as_float(d[i + 1]) - de.y);
-            f[2] = e[2] * (__uint_as_float(d[i + 2]) - de.z);
-            f[3] = e[3] * (__uint_as_float(d[i + 3]) - de.w);
-            if (!KEYS && valid != 0xffffffffu)
-#pragma unroll
-              for (int u = 0; u < 4; ++u)
-                if (!(valid >> (i + u) & 1)) f[u] = 0.f;
-            if (KEYS) {
-              pk[i / 2] = pack2<T>(e[0], e[1]);
-              pk[i / 2 + 1] = pack2<T>(e[2], e[3]);
+            const float2 c2 = make_float2(c, c);
+            float2 e0 = fma2(as_f2(s[i], s[i + 1]), c2, make_float2(ls.x, ls.y));
+            float2 e1 = fma2(as_f2(s[i + 2], s[i + 3]), c2, make_float2(ls.z, ls.w));
+            e0 = make_float2(ex2(e0.x), ex2(e0.y));
+            e1 = make_float2(ex2(e1.x), ex2(e1.y));
+            float2 f0 = mul2(e0, add2(as_f2(d[i], d[i + 1]), make_float2(de.x, de.y)));
+            float2 f1 = mul2(e1, add2(as_f2(d[i + 2], d[i + 3]), make_float2(de.z, de.w)));
+            if (!KEYS && valid != 0xffffffffu) {
+              if (!(valid >> i & 1)) f0.x = 0.f;
+              if (!(valid >> (i + 1) & 1)) f0.y = 0.f;
+              if (!(valid >> (i + 2) & 1)) f1.x = 0.f;
+              if (!(valid >> (i + 3) & 1)) f1.y = 0.f;
             }
-            dk[i / 2] = pack2<T>(f[0], f[1]);
-            dk[i / 2 + 1] = pack2<T>(f[2], f[3]);
+            if (KEYS) {
+              pk[i / 2] = pack2<T>(e0.x, e0.y);
+              pk[i / 2 + 1] = pack2<T>(e1.x, e1.y);
+            }
+            dk[i / 2] = pack2<T>(f0.x, f0.y);
+            dk[i / 2 + 1] = pack2<T>(f1.x, f1.y);
           }
           if (KEYS) tmem_st16(mine + bf * 128 + col, pk);
           tmem_st16(mine + bf * 128 + 64 + col, dk);

@@ -52,8 +52,8 @@ __global__ void __launch_bounds__(kTcThreads, 2)
   uint8_t* sk = sq + L::kBytes;
   uint8_t* sv = sk + NS * L::kBytes;
   uint64_t* bar = reinterpret_cast<uint64_t*>(sv + NS * L::kBytes);
-  uint64_t *q_full = bar, *s_full = bar + 1, *p_full = bar + 2, *o_full = bar + 3;
-  uint64_t *k_full = bar + 4, *k_empty = k_full + NS, *v_full = k_empty + NS, *v_empty = v_full + NS;
+  uint64_t *q_full = bar, *s_full = bar + 1, *o_full = bar + 2, *p_full = bar + 3;  // p_full: two halves of a tile
+  uint64_t *k_full = bar + 5, *k_empty = k_full + NS, *v_full = k_empty + NS, *v_empty = v_full + NS;
   __shared__ uint32_t s_tmem;
   __shared__ uint32_t s_valid[2][4];
 
@@ -77,6 +77,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     mbar_init(q_full, 1);
     mbar_init(s_full, 1);
     mbar_init(p_full, kTile);
+    mbar_init(p_full + 1, kTile);
     mbar_init(o_full, 1);
     for (int i = 0; i < NS; ++i) {
       mbar_init(k_full + i, 1);
@@ -139,12 +140,16 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         }
         mma_commit(s_full);
         mma_commit(k_empty + st);
-        if (!(ok = mbar_wait(p_full, j & 1, spin_max))) break;
         if (!(ok = mbar_wait(v_full + st, ph, spin_max))) break;
-        tc_fence_after();
 #pragma unroll
-        for (int k = 0; k < kTile / 16; ++k)
-          mma_ts(tmem + 128, tmem + 8 * k, smem_desc(av + k * 2048, kTile * 128), id_o, j > 0 || k > 0);
+        for (int half = 0; half < 2; ++half) {
+          if (!(ok = mbar_wait(p_full + half, j & 1, spin_max))) break;
+          tc_fence_after();
+#pragma unroll
+          for (int k = half * kTile / 32; k < (half + 1) * kTile / 32; ++k)
+            mma_ts(tmem + 128, tmem + 8 * k, smem_desc(av + k * 2048, kTile * 128), id_o, j > 0 || k > 0);
+        }
+        if (!ok) break;
         mma_commit(v_empty + st);
       }
       mma_commit(o_full);
@@ -153,6 +158,9 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     __syncwarp();
   } else {  // softmax: thread tid is row tid
     const uint32_t mine = tmem + ((uint32_t)w << 21);  // lane 32 w
+    const float c = p.scale_log2;
+    // the score of a key that takes no part: -inf once scaled (c is never 0)
+    const uint32_t out_of = __float_as_uint(c >= 0.f ? -INFINITY : INFINITY);
     float m = -INFINITY, l = 0.f;
     for (int j = 0; j < n; ++j) {
       const int k0 = ks + j * kTile;
@@ -179,24 +187,30 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         break;
       }
       tc_fence_after();
-      float mx = -INFINITY;
-      const float c = p.scale_log2;
+      uint32_t r[kTile];  // the row's scores, in registers from here on
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        uint32_t r[32];
-        tmem_ld32(mine + 32 * q, r);
-        tmem_wait_ld();
-        if (tail) {
+      for (int q = 0; q < 4; ++q) tmem_ld32(mine + 32 * q, *reinterpret_cast<uint32_t(*)[32]>(r + 32 * q));
+      tmem_wait_ld();
+      if (tail) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
           const uint32_t bits = s_valid[j & 1][q];
 #pragma unroll
           for (int i = 0; i < 32; ++i)
-            if (!(bits >> i & 1)) r[i] = 0xffc00000u;  // NaN: passed over by fmaxf
+            if (!(bits >> i & 1)) r[32 * q + i] = out_of;
         }
-#pragma unroll
-        for (int i = 0; i < 32; ++i) mx = fmaxf(mx, __uint_as_float(r[i]) * c);
       }
+      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      if (c >= 0.f) {
+#pragma unroll
+        for (int i = 0; i < kTile; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(r[i]));
+      } else {
+#pragma unroll
+        for (int i = 0; i < kTile; ++i) mx[i & 3] = fmaxf(mx[i & 3], -__uint_as_float(r[i]));
+      }
+      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
       // the maximum that P is taken against: kept while it is near enough
-      const float grown = fmaxf(m, mx);
+      const float grown = fmaxf(m, top == -INFINITY ? top : top * fabsf(c));
       const bool move = j == 0 || grown > m + kLazy;
       if (__any_sync(0xffffffffu, move)) {
         const float next = grown == -INFINITY ? m : grown;
@@ -205,39 +219,41 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         l *= f;
         if (j > 0) {
 #pragma unroll
-          for (int q = 0; q < DP / 32; ++q) {
-            uint32_t r[32];
-            tmem_ld32(mine + 128 + 32 * q, r);
+          for (int q = 0; q < DP / 16; ++q) {
+            uint32_t o[16];
+            tmem_ld16(mine + 128 + 16 * q, o);
             tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * f);
-            tmem_st32(mine + 128 + 32 * q, r);
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+            tmem_st16(mine + 128 + 16 * q, o);
           }
         }
       }
-      const float mb = m == -INFINITY ? 0.f : m;
+      const float mb = m == -INFINITY ? 0.f : -m;
+      float2 s0 = make_float2(0.f, 0.f), s1 = s0;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        uint32_t r[32], pk[16];
-        tmem_ld32(mine + 32 * q, r);
-        tmem_wait_ld();
-        float s0 = 0.f, s1 = 0.f;
+        uint32_t pk[16];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          float e = ex2(fmaf(__uint_as_float(r[i]), c, -mb));
-          if (tail && !(s_valid[j & 1][q] >> i & 1)) e = 0.f;
-          if (i & 1) s1 += e;
-          else s0 += e;
-          r[i] = __float_as_uint(e);
+        for (int i = 0; i < 32; i += 4) {
+          float2 a = fma2(as_f2(r[32 * q + i], r[32 * q + i + 1]), make_float2(c, c), make_float2(mb, mb));
+          float2 b = fma2(as_f2(r[32 * q + i + 2], r[32 * q + i + 3]), make_float2(c, c), make_float2(mb, mb));
+          a = make_float2(ex2(a.x), ex2(a.y));
+          b = make_float2(ex2(b.x), ex2(b.y));
+          s0 = add2(s0, a);
+          s1 = add2(s1, b);
+          pk[i / 2] = pack2<T>(a.x, a.y);
+          pk[i / 2 + 1] = pack2<T>(b.x, b.y);
         }
-        l += s0 + s1;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) pk[i] = pack2<T>(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
         tmem_st16(mine + 16 * q, pk);
+        if (q & 1) {  // half of the row is there: its product may start
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(p_full + (q >> 1));
+        }
       }
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(p_full);
+      s0 = add2(s0, s1);
+      l += s0.x + s0.y;
     }
     if (n > 0) ok = ok && mbar_wait(o_full, 0, spin_max);
     tc_fence_after();

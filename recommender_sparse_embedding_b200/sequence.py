@@ -108,9 +108,15 @@ def _rows(t: torch.Tensor, name: str, D: Optional[int] = None):
     return n, width, step
 
 
-def _out(out, name, shape, dtype, device):
+def _out(out, name, like, shape, dtype):
+    """The output given, or a new contiguous one beside the tensor `like`, of
+    `shape` (None: like's)."""
+    if shape is None:
+        if out is None and like.is_contiguous():
+            return torch.empty_like(like, dtype=dtype)
+        shape = like.shape
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
     if out.shape != shape or out.dtype != dtype:
         raise ValueError(f"{name}: expected {tuple(shape)} of {dtype}, got {tuple(out.shape)} of {out.dtype}")
     return out
@@ -147,7 +153,7 @@ def embed_lookup(weight: torch.Tensor, tokens: torch.Tensor, scale: float = 1.0,
         with _on(stream, weight):
             return embed_lookup(weight, tokens, scale, padding, out_dtype, out)
     dev = weight.device
-    out = _out(out, "out", (*tokens.shape, D), out_dtype or (weight.dtype if out is None else out.dtype), dev)
+    out = _out(out, "out", weight, (*tokens.shape, D), out_dtype or (weight.dtype if out is None else out.dtype))
     ot = _type(out, "out")
     _, _, stride = _rows(out, "out", D)
     _r._check(_r.load().recis_embed_lookup(weight.data_ptr(), wt, V, D, _ptr(tokens), tokens.numel(), scale, padding,
@@ -171,7 +177,7 @@ def embed_grad(tokens: torch.Tensor, grad_out: torch.Tensor, num_rows: int, scal
         with _on(stream, grad_out):
             return embed_grad(tokens, grad_out, num_rows, scale, padding, dtype, out, accumulate)
     L, dev, n = _r.load(), grad_out.device, tokens.numel()
-    out = _out(out, "out", (num_rows, D), dtype or (torch.float32 if out is None else out.dtype), dev)
+    out = _out(out, "out", grad_out, (num_rows, D), dtype or (torch.float32 if out is None else out.dtype))
     ot = _type(out, "out")
     if not out.is_contiguous():
         raise ValueError("out: expected a contiguous tensor")
@@ -207,10 +213,11 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
         with _on(stream, x):
             return layer_norm(x, weight, bias, eps, out_dtype, out)
     dev = x.device
-    y = _out(out, "out", x.shape, out_dtype or (x.dtype if out is None else out.dtype), dev)
+    y = _out(out, "out", x, None, out_dtype or (x.dtype if out is None else out.dtype))
     yt = _type(y, "out")
     ys = _rows(y, "out", D)[2]
-    mean, rstd = torch.empty((2, *x.shape[:-1]), dtype=torch.float32, device=dev).unbind(0)
+    mean = x.new_empty(x.shape[:-1], dtype=torch.float32)
+    rstd = torch.empty_like(mean)
     _r._check(_r.load().recis_layer_norm(_ptr(x), xt, xs, M, D, _ptr(weight), _ptr(bias), wt, eps, _ptr(y), yt, ys,
                                          _ptr(mean), _ptr(rstd), _raw(dev)), "recis_layer_norm")
     return y, mean, rstd
@@ -234,7 +241,7 @@ def layer_norm_backward(grad_y: torch.Tensor, x: torch.Tensor, mean: torch.Tenso
         with _on(stream, x):
             return layer_norm_backward(grad_y, x, mean, rstd, weight, bias, grad_x)
     L, dev = _r.load(), x.device
-    gx = _out(grad_x, "grad_x", x.shape, x.dtype, dev)
+    gx = _out(grad_x, "grad_x", x, None, x.dtype)
     gxs = _rows(gx, "grad_x", D)[2]
     gw = None if weight is None else torch.empty_like(weight)
     gb = None if bias is None else torch.empty_like(bias)
@@ -310,11 +317,11 @@ def attend(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_offsets: torch.T
             return attend(q, k, v, q_offsets, k_offsets, max_q, max_k, scale, key_mask, out, lse)
     L, dev = _r.load(), q.device
     given = out is not None
-    out = _out(out, "out", q.shape, q.dtype, dev)
+    out = _out(out, "out", q, None, q.dtype)
     a.out_stride, a.out_head_stride = _heads(out, "out", q.dtype)
     if given:
         _written(out, "out", (a.out_stride, a.out_head_stride))
-    lse = _out(lse, "lse", q.shape[:2], torch.float32, dev)
+    lse = _out(lse, "lse", q, q.shape[:2], torch.float32)
     if not lse.is_contiguous():
         raise ValueError("lse: expected a contiguous tensor")
     a.out, a.lse = _ptr(out), _ptr(lse)
@@ -346,7 +353,7 @@ def attend_backward(grad_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v:
     L, dev = _r.load(), q.device
     grads, strides = [], []
     for t, name, like in ((grad_q, "grad_q", q), (grad_k, "grad_k", k), (grad_v, "grad_v", v)):
-        g = _out(t, name, like.shape, dtype, dev)
+        g = _out(t, name, like, None, dtype)
         st = _heads(g, name, dtype)
         if t is not None:
             _written(g, name, st)
