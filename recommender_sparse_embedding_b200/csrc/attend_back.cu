@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(BackCfg<DP>::kThreads, BackCfg<DP>::kBlocksPer
     mbar_init(acc_full, 1);
     for (int i = 0; i < NB; ++i) {
       mbar_init(s_full + i, 1);
-      mbar_init(e_full + i, WG * 128);
+      mbar_init(e_full + i, 128);
     }
     for (int i = 0; i < kNS; ++i) {
       mbar_init(y_full + i, 2);
@@ -281,7 +281,9 @@ __global__ void __launch_bounds__(BackCfg<DP>::kThreads, BackCfg<DP>::kBlocksPer
     }
     const bool any = __any_sync(0xffffffffu, live);
     const float c = p.scale_log2;
-    for (int j = 0; j < n; ++j) {
+    // two warpgroups take every other tile, each its own S and dP, so that one's
+    // exponentials run under the other's products
+    for (int j = wg; j < n; j += WG) {
       const int st = j % kNS, bf = j % NB;
       ok = mbar_wait(y_full + st, (j / kNS) & 1, spin_max) && mbar_wait(s_full + bf, (j / NB) & 1, spin_max);
       if (!__all_sync(0xffffffffu, ok)) {
@@ -291,8 +293,8 @@ __global__ void __launch_bounds__(BackCfg<DP>::kThreads, BackCfg<DP>::kBlocksPer
       tc_fence_after();
       if (any) {
 #pragma unroll
-        for (int q = 0; q < 2 / WG; ++q) {
-          const int col = (wg + q) * 32;  // WG == 2: the warpgroup's half; else both in turn
+        for (int q = 0; q < 2; ++q) {
+          const int col = q * 32;
           uint32_t s[32], d[32];
           tmem_ld32(mine + bf * 128 + col, s);
           tmem_ld32(mine + bf * 128 + 64 + col, d);
@@ -375,24 +377,27 @@ __global__ void __launch_bounds__(BackCfg<DP>::kThreads, BackCfg<DP>::kBlocksPer
   if (w == kIssuer) tmem_free(tmem, C::kCols);
 }
 
-// delta[t][h] = sum_d grad_out * out: one warp a (query, head)
+// delta[t][h] = sum_d grad_out * out: 16 lanes a (query, head), 8 columns each
 template <typename T>
 __global__ void __launch_bounds__(256) delta_kernel(const __grid_constant__ AttendParams p) {
-  const int lane = threadIdx.x & 31, d = lane * 4;
-  const int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (i >= p.Tq * p.Hq) return;
-  const int64_t t = i / p.Hq;
-  const int h = (int)(i % p.Hq);
+  const int lane = threadIdx.x & 15, d = lane * 8;
+  const int64_t i = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
   float s = 0.f;
-  if (d < p.D) {
-    const uint2 a = *reinterpret_cast<const uint2*>(static_cast<const T*>(p.out) + t * p.os + h * p.oh + d);
-    const uint2 b = *reinterpret_cast<const uint2*>(static_cast<const T*>(p.go) + t * p.gos + h * p.goh + d);
-    const float2 a0 = unpack2<T>(a.x), a1 = unpack2<T>(a.y), b0 = unpack2<T>(b.x), b1 = unpack2<T>(b.y);
-    s = a0.x * b0.x + a0.y * b0.y + a1.x * b1.x + a1.y * b1.y;
+  if (i < p.Tq * p.Hq && d < p.D) {
+    const int64_t t = i / p.Hq;
+    const int h = (int)(i - t * p.Hq);
+    RawVec<T, 8> a, b;
+    a.load(static_cast<const T*>(p.out) + t * p.os + h * p.oh + d);
+    b.load(static_cast<const T*>(p.go) + t * p.gos + h * p.goh + d);
+    float x[8], y[8];
+    a.unpack(x);
+    b.unpack(y);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s = fmaf(x[j], y[j], s);
   }
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-  if (lane == 0) p.delta[i] = s;
+  for (int off = 8; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+  if (lane == 0 && i < p.Tq * p.Hq) p.delta[i] = s;
 }
 
 // grad_q from the parts of the keys, added in order: one warp a (query, head)
@@ -453,7 +458,7 @@ recis_status back(const AttendParams& p, cudaStream_t s) {
   const int TQ = kX / p.G, gc = std::min(p.G, kY), tq = kY / gc;
   const int64_t kgrid = (int64_t)p.B * p.Hkv * (((int64_t)p.max_k + kX - 1) / kX);
   const int64_t qgrid = (int64_t)p.B * p.splits * p.Hkv * (((int64_t)p.max_q + TQ - 1) / TQ);
-  const int64_t dgrid = (p.Tq * p.Hq + 7) / 8;
+  const int64_t dgrid = (p.Tq * p.Hq + 15) / 16;
   for (int64_t g : {kgrid, qgrid, dgrid})
     if (g >= ((int64_t)1 << 31)) {
       set_error("attend_backward: too many blocks (bags times longest bag times heads)");
