@@ -216,15 +216,18 @@ __global__ void __launch_bounds__(kThreads, FewBackCfg<DP, NR>::kTwo ? 2 : 1)
     // where the thread's key lies in dS's rows: its 16-byte chunk is swizzled by the row
     uint8_t* ds_at = sds + (key >> 6) * 16384 + (key & 7) * 2;
     const int chunk = (key & 63) >> 3;
+    auto mask_at = [&](int j) {
+      const int i = ks + j * kKeys + key;
+      return i < ke && (!p.mask || p.mask[bag.k0 + i]);
+    };
+    bool takes_next = n > 0 && mask_at(0);
     for (int j = 0; j < n; ++j) {
       const int k0 = ks + j * kKeys;
-      const int64_t t = bag.k0 + k0 + key;
-      const bool in = k0 + key < ke, takes = in && (!p.mask || p.mask[t]);
-      ok = mbar_wait(s_full, j & 1, spin_max);
-      if (!__all_sync(0xffffffffu, ok)) {
-        ok = false;
-        break;
-      }
+      const bool takes = takes_next;
+      takes_next = j + 1 < n && mask_at(j + 1);
+      // a warp that gave up goes on without waiting: the block's barriers need it
+      ok = ok && mbar_wait(s_full, j & 1, spin_max);
+      __syncwarp();
       tc_fence_after();
       uint32_t s[H], d[H], pk[H / 2], dk[H / 2];
       tmem_ld(mine + wg * H, s);
@@ -268,29 +271,47 @@ __global__ void __launch_bounds__(kThreads, FewBackCfg<DP, NR>::kTwo ? 2 : 1)
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(e_full);
-      ok = mbar_wait(o_full, j & 1, spin_max);
-      if (!__all_sync(0xffffffffu, ok)) {
-        ok = false;
-        break;
-      }
+      ok = ok && mbar_wait(o_full, j & 1, spin_max);
+      __syncwarp();
       tc_fence_after();
-      // warpgroup 0 stores dV, warpgroup 1 dK
-      T* out = wg == 0 ? static_cast<T*>(p.gv) + t * p.gvs + h * p.gvh : static_cast<T*>(p.gk) + t * p.gks + h * p.gkh;
+      // warpgroup 0 stores dV, warpgroup 1 dK, 64 columns at a time: the thread's
+      // row goes to shared memory (its warpgroup's half of dS, whose product is
+      // done), and 8 lanes store a row's 128 bytes together
+      T* out = wg == 0 ? static_cast<T*>(p.gv) + h * p.gvh : static_cast<T*>(p.gk) + h * p.gkh;
+      const int64_t stride = wg == 0 ? p.gvs : p.gks;
       const float mul = wg == 0 ? 1.0f : p.scale;
+      uint8_t* stage = sds + wg * 16384;
 #pragma unroll
-      for (int q = 0; q < DP / 32; ++q) {
-        uint32_t r[32];
-        tmem_ld(mine + (wg == 0 ? C::kDv : C::kDk) + 32 * q, r);
-        tmem_wait_ld();
+      for (int half = 0; half < C::kBlocks; ++half) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float f[8];
+        for (int q = 0; q < 2; ++q) {
+          uint32_t r[32];
+          tmem_ld(mine + (wg == 0 ? C::kDv : C::kDk) + 64 * half + 32 * q, r);
+          tmem_wait_ld();
 #pragma unroll
-          for (int u = 0; u < 8; ++u) f[u] = takes ? __uint_as_float(r[8 * i + u]) * mul : 0.f;
-          if (in && 32 * q + 8 * i < p.D) store_vec(out + 32 * q + 8 * i, f);
+          for (int i = 0; i < 4; ++i) {
+            uint4 u;
+            uint32_t* v = &u.x;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              v[e] = takes ? pack2<T>(__uint_as_float(r[8 * i + 2 * e]) * mul, __uint_as_float(r[8 * i + 2 * e + 1]) * mul)
+                           : 0u;
+            *reinterpret_cast<uint4*>(stage + key * 128 + (((4 * q + i) ^ (key & 7)) << 4)) = u;
+          }
         }
+        if (half == C::kBlocks - 1) tc_fence_before();
+        asm volatile("bar.sync %0, 128;" ::"r"(6 + wg) : "memory");
+        const int ch = lane & 7, d = 64 * half + 8 * ch;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int row = (w & 3) * 32 + 4 * i + (lane >> 3);
+          const uint4 u = *reinterpret_cast<const uint4*>(stage + row * 128 + ((ch ^ (row & 7)) << 4));
+          if (k0 + row < ke && d < p.D) *reinterpret_cast<uint4*>(out + (bag.k0 + k0 + row) * stride + d) = u;
+        }
+        // the rows are out before the next half, or the next tile's dS, takes their place
+        if (half < C::kBlocks - 1) asm volatile("bar.sync %0, 128;" ::"r"(6 + wg) : "memory");
+        else asm volatile("bar.sync 5, 256;" ::: "memory");
       }
-      tc_fence_before();
     }
     // dQ: lane r of tensor memory is row r
     const int row = tid & 127;

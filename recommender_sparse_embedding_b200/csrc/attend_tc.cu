@@ -181,11 +181,9 @@ __global__ void __launch_bounds__(kTcThreads, 2)
           }
         fence_async_smem();
       }
+      // a warp that gave up goes on without waiting: the others' barrier needs it
       ok = ok && mbar_wait(s_full, j & 1, spin_max);
-      if (__any_sync(0xffffffffu, !ok)) {
-        ok = false;
-        break;
-      }
+      __syncwarp();
       tc_fence_after();
       uint32_t r[kTile];  // the row's scores, in registers from here on
 #pragma unroll
