@@ -33,21 +33,24 @@ namespace {
 
 constexpr int kX = 128;  // resident rows
 constexpr int kY = 64;   // streamed rows a step
-constexpr int kNS = 4;   // streamed tiles in flight
 
-template <int DP>
+template <int DP, bool KEYS>
 struct BackCfg {
   static constexpr int kBlocks = DP / 64;
   static constexpr int kXBytes = kBlocks * kX * 128, kYBytes = kBlocks * kY * 128;  // one tile
-  // D <= 64: two blocks an SM hide each other's waits (half of tensor memory
-  // each, S and dP once); D <= 128: one block, S and dP twice
-  static constexpr int kBuf = DP == 64 ? 1 : 2;
-  static constexpr int kWG = DP == 64 ? 1 : 2;      // compute warpgroups
+  // One block an SM.  S and dP are kept kBuf times: one's exponentials run under
+  // another's products.  kNS streamed tiles: those in use (kBuf) and enough in
+  // flight to cover a copy's latency, which a step (about 1000 cycles of
+  // products) is shorter than.
+  static constexpr int kBuf = DP == 64 ? 3 : 2;
+  static constexpr int kNS = DP == 64 ? 7 : 5;
+  static constexpr int kWG = 2;      // compute warpgroups
   static constexpr int kThreads = kWG * 128 + 64;
-  static constexpr int kBlocksPerSM = DP == 64 ? 2 : 1;
-  static constexpr uint32_t kCols = DP == 64 ? 256 : 512;
-  static constexpr uint32_t kAcc1 = kBuf * 128, kAcc2 = kAcc1 + DP;
-  static constexpr int kTotal = 2 * kXBytes + 2 * kNS * kYBytes + 1024 + 256 + 2 * kNS * kY * 4;
+  static constexpr uint32_t kCols = 512;
+  static constexpr uint32_t kAcc1 = kBuf * 128, kAcc2 = kAcc1 + (KEYS ? DP : 0);
+  // tiles, barriers, lse and delta (or masks) of the streamed rows
+  static constexpr int kBars = 2 * kXBytes + 2 * kNS * kYBytes, kRowData = kBars + 256;
+  static constexpr int kTotal = kRowData + kNS * (KEYS ? 2 * kY * 4 : 8);
 };
 
 struct BackMaps {
@@ -55,20 +58,20 @@ struct BackMaps {
 };
 
 template <typename T, int DP, bool KEYS>
-__global__ void __launch_bounds__(BackCfg<DP>::kThreads, BackCfg<DP>::kBlocksPerSM)
+__global__ void __launch_bounds__(BackCfg<DP, KEYS>::kThreads, 1)
     attend_back_kernel(const __grid_constant__ AttendParams p, const __grid_constant__ BackMaps maps, int spin_max) {
-  using C = BackCfg<DP>;
-  constexpr int NB = C::kBuf, WG = C::kWG;
-  extern __shared__ uint8_t s_raw[];
-  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(s_raw) + 1023) & ~(uintptr_t)1023);
+  using C = BackCfg<DP, KEYS>;
+  constexpr int NB = C::kBuf, WG = C::kWG, kNS = C::kNS;
+  extern __shared__ __align__(1024) uint8_t base[];  // nothing else is in shared memory: it starts at a tile's boundary
   uint8_t *x1 = base, *x2 = x1 + C::kXBytes, *y1 = x2 + C::kXBytes, *y2 = y1 + kNS * C::kYBytes;
-  uint64_t* bar = reinterpret_cast<uint64_t*>(y2 + kNS * C::kYBytes);
+  uint64_t* bar = reinterpret_cast<uint64_t*>(base + C::kBars);
   uint64_t *x_full = bar, *acc_full = bar + 1, *s_full = bar + 2, *e_full = s_full + NB;
   uint64_t *y_full = e_full + NB, *y_empty = y_full + kNS, *y_raw = y_empty + kNS;
-  float* s_lse = reinterpret_cast<float*>(y2 + kNS * C::kYBytes + 256);  // KEYS: [kNS][kY] -lse * log2(e)
-  float* s_delta = s_lse + kNS * kY;                                     // KEYS: [kNS][kY] -delta
-  __shared__ uint32_t s_tmem;
-  __shared__ uint32_t s_valid[kNS][2];  // queries: the streamed keys that take part
+  static_assert(2 + 2 * NB + 3 * kNS < 32, "barriers and the address of tensor memory in 256 bytes");
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bar + 31);
+  float* s_lse = reinterpret_cast<float*>(base + C::kRowData);  // KEYS: [kNS][kY] -lse * log2(e)
+  float* s_delta = s_lse + kNS * kY;                            // KEYS: [kNS][kY] -delta
+  uint32_t(*s_valid)[2] = reinterpret_cast<uint32_t(*)[2]>(base + C::kRowData);  // queries: the keys that take part
 
   // the block's tile: of keys, or of (query, head) rows against a part of the keys
   const int TQ = kX / p.G;                                  // queries: queries a tile
@@ -89,7 +92,7 @@ __global__ void __launch_bounds__(BackCfg<DP>::kThreads, BackCfg<DP>::kBlocksPer
 
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   constexpr int kLoader = WG * 4, kIssuer = kLoader + 1;
-  if (w == kIssuer) tmem_alloc(&s_tmem, C::kCols);
+  if (w == kIssuer) tmem_alloc(s_tmem, C::kCols);
   if (tid == kLoader * 32) {
     mbar_init(x_full, 1);
     mbar_init(acc_full, 1);
@@ -106,7 +109,7 @@ __global__ void __launch_bounds__(BackCfg<DP>::kThreads, BackCfg<DP>::kBlocksPer
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = s_tmem;
+  const uint32_t tmem = *s_tmem;
   bool ok = true;  // false: a wait gave up
 
   if (w == kLoader) {
@@ -238,10 +241,12 @@ __global__ void __launch_bounds__(BackCfg<DP>::kThreads, BackCfg<DP>::kBlocksPer
         mma_commit(s_full + bf);
         return true;
       };
-      ok = mbar_wait(x_full, 0, spin_max) && scores(0);
+      // the scores run NB - 1 tiles ahead of the products that use them
+      ok = mbar_wait(x_full, 0, spin_max);
+      for (int j = 0; j < max(NB - 1, 1) && j < n && ok; ++j) ok = scores(j);
       for (int j = 0; j < n && ok; ++j) {
         const int st = j % kNS, bf = j % NB;
-        if (NB == 2 && j + 1 < n && !(ok = scores(j + 1))) break;
+        if (NB > 1 && j + NB - 1 < n && !(ok = scores(j + NB - 1))) break;
         if (!(ok = mbar_wait(e_full + bf, (j / NB) & 1, spin_max))) break;
         tc_fence_after();
 #pragma unroll
@@ -292,13 +297,18 @@ __global__ void __launch_bounds__(BackCfg<DP>::kThreads, BackCfg<DP>::kBlocksPer
       }
       tc_fence_after();
       if (any) {
+        uint32_t sd[2][2][32];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          tmem_ld32(mine + bf * 128 + 32 * q, sd[0][q]);
+          tmem_ld32(mine + bf * 128 + 64 + 32 * q, sd[1][q]);
+        }
+        tmem_wait_ld();
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           const int col = q * 32;
-          uint32_t s[32], d[32];
-          tmem_ld32(mine + bf * 128 + col, s);
-          tmem_ld32(mine + bf * 128 + 64 + col, d);
-          tmem_wait_ld();
+          const uint32_t(&s)[32] = sd[0][q];
+          const uint32_t(&d)[32] = sd[1][q];
           uint32_t valid = 0xffffffffu;
           if (!KEYS) valid = s_valid[st][col >> 5];
           uint32_t pk[16], dk[16];
@@ -342,31 +352,48 @@ __global__ void __launch_bounds__(BackCfg<DP>::kThreads, BackCfg<DP>::kBlocksPer
     tc_fence_after();
     const bool have = n > 0 && ok;
     const bool takes = !KEYS || !p.mask || (live && p.mask[t]);  // a masked key's gradients are zero
-    // 2 accumulators (keys) or 1 (queries) of DP columns, in pieces of 32
-    constexpr int kPieces = (KEYS ? 2 : 1) * DP / 32;
+    // 2 accumulators (keys) or 1 (queries) of DP columns, in pieces of 64: the
+    // thread's row goes to shared memory (X's tiles are done with), 8 lanes store
+    // a row's 128 bytes together.  Parts of grad_q are stored directly, in fp32.
+    constexpr int kPieces = (KEYS ? 2 : 1) * C::kBlocks;
 #pragma unroll
-    for (int q = 0; q < kPieces / WG; ++q) {
-      const int piece = q + wg * (kPieces / WG);
-      const bool acc1 = KEYS && piece < DP / 32;
-      const int d0 = piece * 32 % DP;
-      uint32_t r[32];
-      if (have) {
-        tmem_ld32(mine + (acc1 ? C::kAcc1 : C::kAcc2) + d0, r);
-        tmem_wait_ld();
-      }
+    for (int piece = wg; piece < kPieces; piece += WG) {
+      const bool acc1 = KEYS && piece < C::kBlocks;
+      const int d0 = piece * 64 % DP;
       const float mul = acc1 ? 1.0f : p.scale;
+      uint8_t* stage = x1 + piece * kX * 128;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int d = d0 + 8 * i;
-        float f[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = have && takes ? __uint_as_float(r[8 * i + e]) * mul : 0.f;
-        if (live && d < p.D) {
-          if (KEYS) store_vec(static_cast<T*>(acc1 ? p.gv : p.gk) + t * (acc1 ? p.gvs : p.gks) +
-                                  hx * (acc1 ? p.gvh : p.gkh) + d, f);
-          else if (p.splits == 1) store_vec(static_cast<T*>(p.gq) + t * p.gqs + hx * p.gqh + d, f);
-          else store_vec(p.po + (((int64_t)sp * p.Tq + t) * p.Hq + hx) * p.D + d, f);
+      for (int q = 0; q < 2; ++q) {
+        uint32_t r[32];
+        if (have) {
+          tmem_ld32(mine + (acc1 ? C::kAcc1 : C::kAcc2) + d0 + 32 * q, r);
+          tmem_wait_ld();
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float f[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[e] = have && takes ? __uint_as_float(r[8 * i + e]) * mul : 0.f;
+          const int d = d0 + 32 * q + 8 * i;
+          if (KEYS || p.splits == 1)
+            *reinterpret_cast<uint4*>(stage + row * 128 + (((4 * q + i) ^ (row & 7)) << 4)) = make_uint4(
+                pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]), pack2<T>(f[4], f[5]), pack2<T>(f[6], f[7]));
+          else if (live && d < p.D)
+            store_vec(p.po + (((int64_t)sp * p.Tq + t) * p.Hq + hx) * p.D + d, f);
+        }
+      }
+      if (!KEYS && p.splits > 1) continue;
+      asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory");
+      T* out = static_cast<T*>(KEYS ? acc1 ? p.gv : p.gk : p.gq);
+      const int64_t rs = KEYS ? acc1 ? p.gvs : p.gks : p.gqs, hs = KEYS ? acc1 ? p.gvh : p.gkh : p.gqh;
+      const int ch = lane & 7, d = d0 + 8 * ch;
+      for (int i = 0; i < 8; ++i) {
+        const int rr = (w & 3) * 32 + 4 * i + (lane >> 3);
+        const int q = KEYS ? rr : rr / p.G, hh = KEYS ? h : h * p.G + rr - q * p.G;
+        const bool lives = KEYS ? first + rr < bag.nk : rr < TQ * p.G && first + q < bag.nq;
+        const uint4 u = *reinterpret_cast<const uint4*>(stage + rr * 128 + ((ch ^ (rr & 7)) << 4));
+        if (lives && d < p.D)
+          *reinterpret_cast<uint4*>(out + ((KEYS ? bag.k0 : bag.q0) + first + q) * rs + hh * hs + d) = u;
       }
     }
   }
@@ -424,7 +451,7 @@ __global__ void __launch_bounds__(128) join_q_kernel(const __grid_constant__ Att
 
 template <typename T, int DP, bool KEYS>
 cudaError_t back_launch(const AttendParams& p, const BackMaps& m, int64_t grid, cudaStream_t s) {
-  using C = BackCfg<DP>;
+  using C = BackCfg<DP, KEYS>;
   auto kernel = attend_back_kernel<T, DP, KEYS>;
   static std::atomic<uint64_t> done[2];
   const cudaError_t e = allow_smem(kernel, C::kTotal, done);

@@ -261,12 +261,14 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     const int hq = h * p.G + r % p.G;
     const float inv = l == 0.f ? 0.f : 1.0f / l;
     const float lse = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
-    ok = __all_sync(0xffffffffu, ok);
+    const bool have = n > 0 && ok;
+    // the thread's row goes to shared memory (Q is done with), 8 lanes store a
+    // row's 128 bytes together; parts are stored directly, in fp32
 #pragma unroll
     for (int q = 0; q < DP / 32; ++q) {
-      uint32_t r32[32];
-      if (n > 0 && ok) {
-        tmem_ld32(mine + 128 + 32 * q, r32);
+      uint32_t o[32];
+      if (have) {
+        tmem_ld32(mine + 128 + 32 * q, o);
         tmem_wait_ld();
       }
 #pragma unroll
@@ -274,12 +276,25 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         const int d = 32 * q + 8 * i;
         float f[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = l == 0.f ? 0.f : __uint_as_float(r32[8 * i + e]) * inv;
-        if (live && d < p.D) {
-          if (p.splits == 1) store_vec(static_cast<T*>(p.out) + t * p.os + hq * p.oh + d, f);
-          else store_vec(p.po + (((int64_t)sp * p.Tq + t) * p.Hq + hq) * p.D + d, f);
-        }
+        for (int e = 0; e < 8; ++e) f[e] = !have || l == 0.f ? 0.f : __uint_as_float(o[8 * i + e]) * inv;
+        if (p.splits == 1)
+          *reinterpret_cast<uint4*>(sq + (q >> 1) * kTile * 128 + r * 128 + (((4 * (q & 1) + i) ^ (r & 7)) << 4)) =
+              make_uint4(pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]), pack2<T>(f[4], f[5]), pack2<T>(f[6], f[7]));
+        else if (live && d < p.D)
+          store_vec(p.po + (((int64_t)sp * p.Tq + t) * p.Hq + hq) * p.D + d, f);
       }
+    }
+    if (p.splits == 1) {
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+#pragma unroll
+      for (int blk = 0; blk < L::kBlocks; ++blk)
+        for (int i = 0; i < 8; ++i) {
+          const int rr = w * 32 + 4 * i + (lane >> 3), ch = lane & 7, d = 64 * blk + 8 * ch;
+          const int qq = rr / p.G, g = rr - qq * p.G;
+          const uint4 u = *reinterpret_cast<const uint4*>(sq + blk * kTile * 128 + rr * 128 + ((ch ^ (rr & 7)) << 4));
+          if (rr < TQ * p.G && t0 + qq < bag.nq && d < p.D)
+            *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + (bag.q0 + t0 + qq) * p.os + (h * p.G + g) * p.oh + d) = u;
+        }
     }
     if (live) {
       if (p.splits == 1) p.lse[t * p.Hq + hq] = lse;
