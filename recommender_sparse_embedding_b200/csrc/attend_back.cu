@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(BackCfg<DP, KEYS>::kThreads, 1)
   const int gc = min(p.G, kY), chunks = (p.G + gc - 1) / gc, tq = kY / gc;
   const int n = KEYS ? (bag.nq + tq - 1) / tq * chunks : ke > ks ? (ke - ks + kY - 1) / kY : 0;
 
-  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, w = __shfl_sync(0xffffffffu, tid >> 5, 0);
   constexpr int kLoader = WG * 4, kIssuer = kLoader + 1;
   if (w == kIssuer) tmem_alloc(s_tmem, C::kCols);
   if (tid == kLoader * 32) {
@@ -220,47 +220,56 @@ __global__ void __launch_bounds__(BackCfg<DP, KEYS>::kThreads, 1)
           mbar_wait((special(j) ? y_raw : y_full) + j % kNS, (j / kNS) & 1, 64);
     }
   } else if (w == kIssuer) {
-    if (lane == 0 && n > 0) {
+    if (n > 0) {
       constexpr uint32_t id_s = mma_desc<T>(kX, kY, false, false), id_a = mma_desc<T>(kX, DP, false, true);
-      const uint32_t ax1 = smem_u32(x1), ax2 = smem_u32(x2), ay1 = smem_u32(y1), ay2 = smem_u32(y2);
+      // descriptors count 16 bytes
+      const uint64_t dx1 = smem_desc(smem_u32(x1), 16), dx2 = smem_desc(smem_u32(x2), 16);
+      const uint64_t dy1 = smem_desc(smem_u32(y1), 16), dy2 = smem_desc(smem_u32(y2), 16);
+      const uint64_t ty1 = smem_desc(smem_u32(y1), kY * 128), ty2 = smem_desc(smem_u32(y2), kY * 128);
+      const bool one = elect_one();
       auto scores = [&](int j) {
         const int st = j % kNS, bf = j % NB;
-        if (!mbar_wait(y_full + st, (j / kNS) & 1, spin_max)) return false;
+        if (!warp_wait(y_full + st, (j / kNS) & 1, spin_max)) return false;
         tc_fence_after();
         const uint32_t d = tmem + bf * 128;
+        const uint64_t b1 = dy1 + st * (C::kYBytes >> 4), b2 = dy2 + st * (C::kYBytes >> 4);
+        if (one) {
 #pragma unroll
-        for (int k = 0; k < DP / 16; ++k) {
-          const uint32_t xo = (k >> 2) * kX * 128 + (k & 3) * 32, yo = st * C::kYBytes + (k >> 2) * kY * 128 + (k & 3) * 32;
-          mma_ss(d, smem_desc(ax1 + xo, 16), smem_desc(ay1 + yo, 16), id_s, k > 0);
-        }
+          for (int k = 0; k < DP / 16; ++k)
+            mma_ss(d, dx1 + (((k >> 2) * kX * 128 + (k & 3) * 32) >> 4), b1 + (((k >> 2) * kY * 128 + (k & 3) * 32) >> 4),
+                   id_s, k > 0);
 #pragma unroll
-        for (int k = 0; k < DP / 16; ++k) {
-          const uint32_t xo = (k >> 2) * kX * 128 + (k & 3) * 32, yo = st * C::kYBytes + (k >> 2) * kY * 128 + (k & 3) * 32;
-          mma_ss(d + 64, smem_desc(ax2 + xo, 16), smem_desc(ay2 + yo, 16), id_s, k > 0);
+          for (int k = 0; k < DP / 16; ++k)
+            mma_ss(d + 64, dx2 + (((k >> 2) * kX * 128 + (k & 3) * 32) >> 4),
+                   b2 + (((k >> 2) * kY * 128 + (k & 3) * 32) >> 4), id_s, k > 0);
+          mma_commit(s_full + bf);
         }
-        mma_commit(s_full + bf);
+        __syncwarp();
         return true;
       };
       // the scores run NB - 1 tiles ahead of the products that use them
-      ok = mbar_wait(x_full, 0, spin_max);
-      for (int j = 0; j < max(NB - 1, 1) && j < n && ok; ++j) ok = scores(j);
+      ok = warp_wait(x_full, 0, spin_max);
+      for (int j = 0; j < NB - 1 && j < n && ok; ++j) ok = scores(j);
       for (int j = 0; j < n && ok; ++j) {
         const int st = j % kNS, bf = j % NB;
-        if (NB > 1 && j + NB - 1 < n && !(ok = scores(j + NB - 1))) break;
-        if (!(ok = mbar_wait(e_full + bf, (j / NB) & 1, spin_max))) break;
+        if (j + NB - 1 < n && !(ok = scores(j + NB - 1))) break;
+        if (!(ok = warp_wait(e_full + bf, (j / NB) & 1, spin_max))) break;
         tc_fence_after();
+        const uint32_t e = tmem + bf * 128;
+        const uint64_t b1 = ty1 + st * (C::kYBytes >> 4), b2 = ty2 + st * (C::kYBytes >> 4);
+        if (one) {
 #pragma unroll
-        for (int k = 0; k < kY / 16; ++k) {
-          const uint32_t e = tmem + bf * 128 + (k >> 1) * 32 + (k & 1) * 8;
-          if (KEYS)
-            mma_ts(tmem + C::kAcc1, e, smem_desc(ay2 + st * C::kYBytes + k * 2048, kY * 128), id_a, j > 0 || k > 0);
-          mma_ts(tmem + C::kAcc2, e + 64, smem_desc(ay1 + st * C::kYBytes + k * 2048, kY * 128), id_a, j > 0 || k > 0);
+          for (int k = 0; k < kY / 16; ++k) {
+            const uint32_t at = (k >> 1) * 32 + (k & 1) * 8;
+            if (KEYS) mma_ts(tmem + C::kAcc1, e + at, b2 + (k * 2048 >> 4), id_a, j > 0 || k > 0);
+            mma_ts(tmem + C::kAcc2, e + 64 + at, b1 + (k * 2048 >> 4), id_a, j > 0 || k > 0);
+          }
+          mma_commit(y_empty + st);
         }
-        mma_commit(y_empty + st);
-        if (NB == 1 && j + 1 < n && !(ok = scores(j + 1))) break;
+        __syncwarp();
       }
-      mma_commit(acc_full);
-      ok = mbar_wait(acc_full, 0, spin_max) && ok;
+      if (one) mma_commit(acc_full);
+      ok = warp_wait(acc_full, 0, spin_max) && ok;
     }
     __syncwarp();
   } else {

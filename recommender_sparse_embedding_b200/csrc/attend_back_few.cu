@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(kThreads, FewBackCfg<DP, NR>::kTwo ? 2 : 1)
   const int rows = bag.nq * p.G;  // <= NR
   const int ks = sp * p.split_keys, ke = min(ks + p.split_keys, bag.nk);
   if (sp > 0 && ks >= bag.nk) return;
-  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, w = __shfl_sync(0xffffffffu, tid >> 5, 0);
   if (rows == 0) {  // keys without queries: zero gradients
     const int per = p.D / 8;
     for (int i = tid; i < (ke - ks) * per; i += kThreads) {
@@ -144,44 +144,52 @@ __global__ void __launch_bounds__(kThreads, FewBackCfg<DP, NR>::kTwo ? 2 : 1)
       __syncwarp();
     }
   } else if (w == kIssuer) {
-    if (lane == 0 && n > 0) {
+    if (n > 0) {
       constexpr uint32_t id_s = mma_desc<T>(kKeys, NR, false, false), id_o = mma_desc<T>(kKeys, DP, false, true);
-      const uint32_t aq = smem_u32(sq), ao = smem_u32(so), ads = smem_u32(sds), akv = smem_u32(skv);
+      // descriptors count 16 bytes
+      const uint64_t dq = smem_desc(smem_u32(sq), 16), dg = smem_desc(smem_u32(so), 16);
+      const uint64_t tq = smem_desc(smem_u32(sq), NR * 128), tg = smem_desc(smem_u32(so), NR * 128);
+      const uint64_t dds = smem_desc(smem_u32(sds), 16);
+      const uint64_t dkv = smem_desc(smem_u32(skv), 16), tkv = smem_desc(smem_u32(skv), kKeys * 128);
+      const bool one = elect_one();
       auto scores = [&](int j) {
         const int st = j % NS;
-        if (!mbar_wait(kv_full + st, (j / NS) & 1, spin_max)) return false;
+        if (!warp_wait(kv_full + st, (j / NS) & 1, spin_max)) return false;
         tc_fence_after();
-        const uint32_t ak = akv + 2 * st * C::kTile, av = ak + C::kTile;
+        const uint64_t dk = dkv + st * (2 * C::kTile >> 4), dv = dk + (C::kTile >> 4);
+        if (one) {
 #pragma unroll
-        for (int k = 0; k < DP / 16; ++k) {
-          const uint32_t xo = (k >> 2) * kKeys * 128 + (k & 3) * 32, yo = (k >> 2) * NR * 128 + (k & 3) * 32;
-          mma_ss(tmem, smem_desc(ak + xo, 16), smem_desc(aq + yo, 16), id_s, k > 0);
-        }
+          for (int k = 0; k < DP / 16; ++k)
+            mma_ss(tmem, dk + (((k >> 2) * kKeys * 128 + (k & 3) * 32) >> 4),
+                   dq + (((k >> 2) * NR * 128 + (k & 3) * 32) >> 4), id_s, k > 0);
 #pragma unroll
-        for (int k = 0; k < DP / 16; ++k) {
-          const uint32_t xo = (k >> 2) * kKeys * 128 + (k & 3) * 32, yo = (k >> 2) * NR * 128 + (k & 3) * 32;
-          mma_ss(tmem + C::kDp, smem_desc(av + xo, 16), smem_desc(ao + yo, 16), id_s, k > 0);
+          for (int k = 0; k < DP / 16; ++k)
+            mma_ss(tmem + C::kDp, dv + (((k >> 2) * kKeys * 128 + (k & 3) * 32) >> 4),
+                   dg + (((k >> 2) * NR * 128 + (k & 3) * 32) >> 4), id_s, k > 0);
+          mma_commit(s_full);
         }
-        mma_commit(s_full);
+        __syncwarp();
         return true;
       };
-      ok = mbar_wait(q_full, 0, spin_max) && scores(0);
+      ok = warp_wait(q_full, 0, spin_max) && scores(0);
       for (int j = 0; j < n && ok; ++j) {
-        const uint32_t ak = akv + 2 * (j % NS) * C::kTile;
-        if (!(ok = mbar_wait(e_full, j & 1, spin_max))) break;
+        const uint64_t tk = tkv + (j % NS) * (2 * C::kTile >> 4);
+        if (!(ok = warp_wait(e_full, j & 1, spin_max))) break;
         tc_fence_after();
+        if (one) {
 #pragma unroll
-        for (int k = 0; k < NR / 16; ++k)
-          mma_ts(tmem + C::kDv, tmem + 8 * k, smem_desc(ao + k * 2048, NR * 128), id_o, k > 0);
+          for (int k = 0; k < NR / 16; ++k) mma_ts(tmem + C::kDv, tmem + 8 * k, tg + (k * 2048 >> 4), id_o, k > 0);
 #pragma unroll
-        for (int k = 0; k < NR / 16; ++k)
-          mma_ts(tmem + C::kDk, tmem + C::kDp + 8 * k, smem_desc(aq + k * 2048, NR * 128), id_o, k > 0);
+          for (int k = 0; k < NR / 16; ++k)
+            mma_ts(tmem + C::kDk, tmem + C::kDp + 8 * k, tq + (k * 2048 >> 4), id_o, k > 0);
 #pragma unroll
-        for (int k = 0; k < kKeys / 16; ++k)
-          mma_ss(tmem + C::kDq, smem_desc(ads + (k >> 2) * 16384 + (k & 3) * 32, 16),
-                 smem_desc(ak + k * 2048, kKeys * 128), id_o, j > 0 || k > 0);
-        mma_commit(o_full);
-        mma_commit(kv_empty + j % NS);
+          for (int k = 0; k < kKeys / 16; ++k)
+            mma_ss(tmem + C::kDq, dds + (((k >> 2) * 16384 + (k & 3) * 32) >> 4), tk + (k * 2048 >> 4), id_o,
+                   j > 0 || k > 0);
+          mma_commit(o_full);
+          mma_commit(kv_empty + j % NS);
+        }
+        __syncwarp();
         if (j + 1 < n) ok = scores(j + 1);
       }
     }

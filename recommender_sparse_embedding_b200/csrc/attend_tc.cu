@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
   if (t0 >= bag.nq || (ks >= bag.nk && sp > 0)) return;
   const int n = ke > ks ? (ke - ks + kTile - 1) / kTile : 0;  // steps
 
-  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, w = __shfl_sync(0xffffffffu, tid >> 5, 0);
   if (w == 5) tmem_alloc(&s_tmem, kTmemCols);
   if (tid == 128) {
     mbar_init(q_full, 1);
@@ -124,36 +124,45 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     }
     __syncwarp();
   } else if (w == 5) {  // products
-    if (lane == 0 && n > 0) {
+    if (n > 0) {
       constexpr uint32_t id_s = mma_desc<T>(kTile, kTile, false, false), id_o = mma_desc<T>(kTile, DP, false, true);
-      const uint32_t aq = smem_u32(sq);
-      ok = mbar_wait(q_full, 0, spin_max);
+      // descriptors count 16 bytes
+      const uint64_t dq = smem_desc(smem_u32(sq), 16), dk = smem_desc(smem_u32(sk), 16);
+      const uint64_t dv = smem_desc(smem_u32(sv), kTile * 128);
+      const bool one = elect_one();
+      ok = warp_wait(q_full, 0, spin_max);
       for (int j = 0; j < n && ok; ++j) {
         const int st = j % NS, ph = (j / NS) & 1;
-        const uint32_t ak = smem_u32(sk + st * L::kBytes), av = smem_u32(sv + st * L::kBytes);
-        if (!(ok = mbar_wait(k_full + st, ph, spin_max))) break;
+        if (!(ok = warp_wait(k_full + st, ph, spin_max))) break;
         tc_fence_after();
+        if (one) {
+          const uint64_t b = dk + st * (L::kBytes >> 4);
 #pragma unroll
-        for (int k = 0; k < DP / 16; ++k) {
-          const uint32_t off = (k >> 2) * kTile * 128 + (k & 3) * 32;
-          mma_ss(tmem, smem_desc(aq + off, 16), smem_desc(ak + off, 16), id_s, k > 0);
+          for (int k = 0; k < DP / 16; ++k) {
+            const uint32_t off = ((k >> 2) * kTile * 128 + (k & 3) * 32) >> 4;
+            mma_ss(tmem, dq + off, b + off, id_s, k > 0);
+          }
+          mma_commit(s_full);
+          mma_commit(k_empty + st);
         }
-        mma_commit(s_full);
-        mma_commit(k_empty + st);
-        if (!(ok = mbar_wait(v_full + st, ph, spin_max))) break;
+        __syncwarp();
+        if (!(ok = warp_wait(v_full + st, ph, spin_max))) break;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          if (!(ok = mbar_wait(p_full + half, j & 1, spin_max))) break;
+          if (!(ok = warp_wait(p_full + half, j & 1, spin_max))) break;
           tc_fence_after();
+          if (one) {
+            const uint64_t b = dv + st * (L::kBytes >> 4);
 #pragma unroll
-          for (int k = half * kTile / 32; k < (half + 1) * kTile / 32; ++k)
-            mma_ts(tmem + 128, tmem + 8 * k, smem_desc(av + k * 2048, kTile * 128), id_o, j > 0 || k > 0);
+            for (int k = half * kTile / 32; k < (half + 1) * kTile / 32; ++k)
+              mma_ts(tmem + 128, tmem + 8 * k, b + (k * 2048 >> 4), id_o, j > 0 || k > 0);
+            if (half == 1) mma_commit(v_empty + st);
+          }
+          __syncwarp();
         }
-        if (!ok) break;
-        mma_commit(v_empty + st);
       }
-      mma_commit(o_full);
-      ok = mbar_wait(o_full, 0, spin_max) && ok;
+      if (one) mma_commit(o_full);
+      ok = warp_wait(o_full, 0, spin_max) && ok;
     }
     __syncwarp();
   } else {  // softmax: thread tid is row tid

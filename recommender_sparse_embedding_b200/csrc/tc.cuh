@@ -114,6 +114,20 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* mbar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(mbar)) : "memory");
 }
 
+// One lane of a converged warp.  The warp that issues products runs its loop as
+// a whole and branches to the elected lane only around the instructions, so
+// that descriptors stay in uniform registers: 40 cycles a product, against 64
+// when the whole loop is one lane's.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred P;\n elect.sync _|P, 0xffffffff;\n selp.u32 %0, 1, 0, P;\n}" : "=r"(p));
+  return p != 0;
+}
+// the whole warp waits; false in every lane if a lane gave up
+__device__ __forceinline__ bool warp_wait(uint64_t* mbar, unsigned parity, int limit) {
+  return __all_sync(0xffffffffu, mbar_wait(mbar, parity, limit));
+}
+
 // ---- tensor-map copies
 __device__ __forceinline__ void tma_load3(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* mbar) {
   asm volatile(
