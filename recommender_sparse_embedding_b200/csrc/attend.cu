@@ -348,7 +348,7 @@ AttendPlan attend_plan(const recis_attend_args& a, bool backward) {
     // over query tiles of its own, two blocks an SM.  At least 512 keys a part.
     const int64_t G = a.Hq / a.Hkv, rows = a.max_q * G;
     const bool few = rows <= kFewBackRows;
-    if (!few) g.delta_bytes = align256(a.Tq * a.Hq * 4);
+    if (!few) g.delta_bytes = 2 * align256(a.Tq * a.Hq * 4);
     const int64_t blocks = std::max<int64_t>(1, a.B * a.Hkv * (few ? 1 : (a.max_q + 128 / G - 1) / (128 / G)));
     const int64_t target = kSMs * (few ? 3 * few_back_per_sm(a.D, rows) : 2);
     const int64_t want = std::min<int64_t>((target + blocks - 1) / blocks, (a.max_k + 511) / 512);
@@ -430,6 +430,7 @@ recis_status fill(const recis_attend_args* a, AttendParams* p, const AttendPlan&
   p->po = reinterpret_cast<float*>(at);
   p->pl = reinterpret_cast<float*>(at + g.po_bytes);
   p->delta = reinterpret_cast<float*>(at + g.po_bytes + g.pl_bytes);
+  p->nlse = reinterpret_cast<float*>(at + g.po_bytes + g.pl_bytes + g.delta_bytes / 2);
   p->status = st;
   return RECIS_OK;
 }

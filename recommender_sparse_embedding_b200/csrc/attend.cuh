@@ -20,7 +20,8 @@ struct AttendParams {
   int splits, split_keys;   // parts of a bag's keys, keys a part
   float* po;                // splits > 1: [splits][Tq][Hq][D] each part's output ...
   float* pl;                // ... and [splits][Tq][Hq] its lse
-  float* delta;             // backward: [Tq][Hq] sum(grad_out * out)
+  float* delta;             // backward, many rows: [Tq][Hq] -sum(grad_out * out) ...
+  float* nlse;              // ... and [Tq][Hq] -lse * log2(e)
   int* status;
 };
 

@@ -101,7 +101,8 @@ __global__ void __launch_bounds__(BackCfg<DP, KEYS>::kThreads, 1)
       mbar_init(e_full + i, 128);
     }
     for (int i = 0; i < kNS; ++i) {
-      mbar_init(y_full + i, 2);
+      // a tile: its copies' bytes, the warp's word that it is finished, the lanes' copies of lse and delta
+      mbar_init(y_full + i, KEYS ? 34 : 2);
       mbar_init(y_empty + i, 1);
       mbar_init(y_raw + i, 1);
     }
@@ -114,7 +115,7 @@ __global__ void __launch_bounds__(BackCfg<DP, KEYS>::kThreads, 1)
 
   if (w == kLoader) {
     if (n > 0) {
-      if (lane == 0) {
+      if (elect_one()) {
         const int rows = KEYS ? kX : TQ * p.G;
         mbar_arrive_expect(x_full, (unsigned)(2 * C::kBlocks * rows * 128));
         for (int i = 0; i < C::kBlocks; ++i) {
@@ -123,11 +124,6 @@ __global__ void __launch_bounds__(BackCfg<DP, KEYS>::kThreads, 1)
           tma_load3(x2 + i * kX * 128, &maps.x2, 64 * i, y, z, x_full);
         }
       }
-      // a streamed tile that holds rows which must be zeroed
-      auto special = [&](int j) {
-        if (!KEYS) return ks + (j + 1) * kY > ke || p.mask != nullptr;
-        return tq * gc < kY || (j / chunks + 1) * tq > bag.nq || (j % chunks + 1) * gc > p.G;
-      };
       // the lane's rows of a tile: lane and lane + 32
       int rq[2], rg[2];
 #pragma unroll
@@ -135,89 +131,113 @@ __global__ void __launch_bounds__(BackCfg<DP, KEYS>::kThreads, 1)
         rq[i] = (lane + 32 * i) / gc;
         rg[i] = (lane + 32 * i) % gc;
       }
-      int asked = 0;
-      bool v[2];                     // of the tile asked for last: the lane's rows take part,
-      float lse[2], delta[2];        // and their -lse and -delta
-      // a tile is asked for, and finished one step later: its rows' lse and
-      // delta are under way meanwhile, and no tile waits for a later one's slot
-      for (int j = 0; j <= n; ++j) {
-        if (j > 0) {
-          const int f = j - 1, st = f % kNS;
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            if (KEYS) {
-              // a row without keys (lse -inf) or of no query: p = 0
-              s_lse[st * kY + lane + 32 * i] = v[i] && lse[i] != INFINITY ? lse[i] * 1.4426950408889634f : -INFINITY;
-              s_delta[st * kY + lane + 32 * i] = v[i] ? delta[i] : 0.f;
-            } else {
-              const unsigned bits = __ballot_sync(0xffffffffu, v[i]);
-              if (lane == 0) s_valid[st][i] = bits;
-            }
-          }
-          if (special(f)) {
-            ok = mbar_wait(y_raw + st, (f / kNS) & 1, spin_max);  // every tile of a stage's turn completes this phase
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-              if (!v[i])
-                for (int k = 0; k < C::kBlocks; ++k) {
-                  uint4* a = reinterpret_cast<uint4*>(y1 + st * C::kYBytes + (k * kY + lane + 32 * i) * 128);
-                  uint4* c = reinterpret_cast<uint4*>(y2 + st * C::kYBytes + (k * kY + lane + 32 * i) * 128);
-#pragma unroll
-                  for (int u = 0; u < 8; ++u) a[u] = c[u] = make_uint4(0, 0, 0, 0);
-                }
-            fence_async_smem();
-          } else if (lane == 0) {
-            mbar_arrive(y_raw + st);  // keeps the stage's phases in step
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(y_full + st);
+      // a tile's first query and head (keys), or key: advanced without divisions,
+      // which would take longer than the step
+      struct At {
+        int a, g;
+      };
+      auto next = [&](At& t) {
+        if (!KEYS) {
+          t.a += kY;
+        } else if ((t.g += gc) >= p.G) {
+          t.g = 0;
+          t.a += tq;
         }
-        if (j < n) {
-          const int st = j % kNS;
-          if (j >= kNS) ok = mbar_wait(y_empty + st, ((j / kNS) & 1) ^ 1, spin_max) && ok;
-          if (!__all_sync(0xffffffffu, ok)) {
-            ok = false;
-            break;
-          }
-          const int jq = KEYS ? (j / chunks) * tq : 0, jg = KEYS ? (j % chunks) * gc : 0;
-          if (lane == 0) {
-            uint64_t* full = y_full + st;
-            if (special(j)) {
-              mbar_arrive(full);
-              full = y_raw + st;
+      };
+      auto takes = [&](const At& t, int i) {  // whether the lane's i-th row of the tile takes part
+        if (KEYS) return rq[i] < tq && t.a + rq[i] < bag.nq && t.g + rg[i] < p.G;
+        const int key = t.a + lane + 32 * i;
+        return key < ke && (!p.mask || p.mask[bag.k0 + key]);
+      };
+      auto special = [&](const At& t) {  // whether it holds rows that must be zeroed
+        if (!KEYS) return t.a + kY > ke || p.mask != nullptr;
+        return tq * gc < kY || t.a + tq > bag.nq || t.g + gc > p.G;
+      };
+      const unsigned bytes = 2 * C::kBlocks * 128 * (KEYS ? tq * gc : kY);
+      // a special tile is finished a step after it is asked for; what its
+      // finishing needs (masks) is read a step before that
+      At at = {KEYS ? 0 : ks, 0}, ahead = at;
+      bool v[2] = {false, false}, v_next[2] = {takes(at, 0), takes(at, 1)}, last_special = false;
+      next(ahead);
+      int st = 0, last_st = 0;
+      unsigned ph = 0, last_ph = 0;
+      for (int j = 0; j <= n; ++j) {
+        if (last_special) {
+          if (!KEYS)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const unsigned bits = __ballot_sync(0xffffffffu, v[i]);
+              if (lane == 0) s_valid[last_st][i] = bits;
             }
-            const int rows = KEYS ? tq * gc : kY;
-            mbar_arrive_expect(full, (unsigned)(2 * C::kBlocks * rows * 128));
-            const int y = KEYS ? h * p.G + jg : h;
-            const int z = KEYS ? (int)(bag.q0 + jq) : (int)(bag.k0 + ks + j * kY);
-            for (int i = 0; i < C::kBlocks; ++i) {
-              tma_load3(y1 + st * C::kYBytes + i * kY * 128, &maps.y1, 64 * i, y, z, full);
-              tma_load3(y2 + st * C::kYBytes + i * kY * 128, &maps.y2, 64 * i, y, z, full);
-            }
+          ok = mbar_wait(y_raw + last_st, last_ph, spin_max) && ok;
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            if (!v[i])
+              for (int k = 0; k < C::kBlocks; ++k) {
+                uint4* a = reinterpret_cast<uint4*>(y1 + last_st * C::kYBytes + (k * kY + lane + 32 * i) * 128);
+                uint4* c = reinterpret_cast<uint4*>(y2 + last_st * C::kYBytes + (k * kY + lane + 32 * i) * 128);
+#pragma unroll
+                for (int u = 0; u < 8; ++u) a[u] = c[u] = make_uint4(0, 0, 0, 0);
+              }
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(y_full + last_st);
+        }
+        if (j == n) break;
+        v[0] = v_next[0];
+        v[1] = v_next[1];
+        if (j + 1 < n) {
+          v_next[0] = takes(ahead, 0);
+          v_next[1] = takes(ahead, 1);
+          next(ahead);
+        }
+        if (j >= kNS) ok = mbar_wait(y_empty + st, ph ^ 1, spin_max) && ok;
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        last_special = special(at);
+        if (elect_one()) {
+          uint64_t* full = y_full + st;
+          if (last_special) {
+            mbar_arrive(full);
+            full = y_raw + st;
+          } else {
+            if (!KEYS) s_valid[st][0] = s_valid[st][1] = 0xffffffffu;
+            mbar_arrive(y_raw + st);  // keeps the stage's phases in step
+            mbar_arrive(full);
           }
-          asked = j + 1;
+          mbar_arrive_expect(full, bytes);
+          const int y = KEYS ? h * p.G + at.g : h, z = (int)(KEYS ? bag.q0 : bag.k0) + at.a;
+          for (int i = 0; i < C::kBlocks; ++i) {
+            tma_load3(y1 + st * C::kYBytes + i * kY * 128, &maps.y1, 64 * i, y, z, full);
+            tma_load3(y2 + st * C::kYBytes + i * kY * 128, &maps.y2, 64 * i, y, z, full);
+          }
+        }
+        __syncwarp();
+        if (KEYS) {
+          // the rows' -lse and -delta; zeros for rows that do not take part, whose
+          // Q and dO are zeros too (p = 1, but p^T dO and ds are 0)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            if (KEYS) {
-              const int q = jq + rq[i], g = jg + rg[i];
-              v[i] = rq[i] < tq && q < bag.nq && g < p.G;
-              if (v[i]) {
-                const int64_t at = (bag.q0 + q) * p.Hq + h * p.G + g;
-                lse[i] = -__ldg(p.lse + at);
-                delta[i] = -__ldg(p.delta + at);
-              }
-            } else {
-              const int key = ks + j * kY + lane + 32 * i;
-              v[i] = key < ke && (!p.mask || p.mask[bag.k0 + key]);
-            }
+            const int64_t r = v[i] ? (bag.q0 + at.a + rq[i]) * p.Hq + h * p.G + at.g + rg[i] : 0;
+            copy4(s_lse + st * kY + lane + 32 * i, p.nlse + r, v[i]);
+            copy4(s_delta + st * kY + lane + 32 * i, p.delta + r, v[i]);
           }
+          copy_arrive(y_full + st);
+        }
+        last_st = st;
+        last_ph = ph;
+        next(at);
+        if (++st == kNS) {
+          st = 0;
+          ph ^= 1;
         }
       }
+      if (KEYS) copy_wait_all();
       // copies in flight end before the block does
       ok = mbar_wait(x_full, 0, spin_max) && ok;
-      if (!ok)
-        for (int j = max(asked - kNS, 0); j < asked; ++j)
-          mbar_wait((special(j) ? y_raw : y_full) + j % kNS, (j / kNS) & 1, 64);
+      for (int i = 0; i < kNS && !ok; ++i) mbar_wait(y_full + i, ph, 64);  // bounded: some may never come
     }
   } else if (w == kIssuer) {
     if (n > 0) {
@@ -288,9 +308,8 @@ __global__ void __launch_bounds__(BackCfg<DP, KEYS>::kThreads, 1)
       t = bag.q0 + first + row / p.G;
       hx = h * p.G + row % p.G;
       if (live) {
-        lse = -p.lse[t * p.Hq + hx] * 1.4426950408889634f;
-        if (lse == INFINITY) lse = -INFINITY;  // a row without keys: p = 0
-        delta = -p.delta[t * p.Hq + hx];
+        lse = p.nlse[t * p.Hq + hx];
+        delta = p.delta[t * p.Hq + hx];
       }
     }
     const bool any = __any_sync(0xffffffffu, live);
@@ -413,7 +432,9 @@ __global__ void __launch_bounds__(BackCfg<DP, KEYS>::kThreads, 1)
   if (w == kIssuer) tmem_free(tmem, C::kCols);
 }
 
-// delta[t][h] = sum_d grad_out * out: 16 lanes a (query, head), 8 columns each
+// What the passes need of a row: -delta, delta[t][h] = sum_d grad_out * out, and
+// -lse * log2(e) (-inf for a row without keys: p = 0).  16 lanes a (query,
+// head), 8 columns each.
 template <typename T>
 __global__ void __launch_bounds__(256) delta_kernel(const __grid_constant__ AttendParams p) {
   const int lane = threadIdx.x & 15, d = lane * 8;
@@ -433,7 +454,11 @@ __global__ void __launch_bounds__(256) delta_kernel(const __grid_constant__ Atte
   }
 #pragma unroll
   for (int off = 8; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-  if (lane == 0 && i < p.Tq * p.Hq) p.delta[i] = s;
+  if (lane == 0 && i < p.Tq * p.Hq) {
+    const float lse = p.lse[i];
+    p.delta[i] = -s;
+    p.nlse[i] = lse == -INFINITY ? -INFINITY : -lse * 1.4426950408889634f;
+  }
 }
 
 // grad_q from the parts of the keys, added in order: one warp a (query, head)

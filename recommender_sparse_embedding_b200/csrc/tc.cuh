@@ -140,6 +140,17 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 
+// ---- four-byte copies by a thread: zeros where not `take`; the thread arrives
+// on `mbar` (an arrival of its count) when its earlier copies have landed
+__device__ __forceinline__ void copy4(float* dst, const float* src, bool take) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(take ? 4 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copy_arrive(uint64_t* mbar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(mbar)) : "memory");
+}
+__device__ __forceinline__ void copy_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // 2^x, relative error below 2^-21, results below 2^-126 are 0
 __device__ __forceinline__ float ex2(float x) {
   float y;
