@@ -12,8 +12,9 @@
 // through all its rows, adds dw and db in registers, and a second kernel joins
 // the blocks' sums in block order in fp64 (no float atomic).
 #include <algorithm>
+#include <atomic>
 
-#include "seqops.cuh"
+#include "tc.cuh"
 
 namespace recis {
 
@@ -97,57 +98,147 @@ __device__ __forceinline__ void row_sum(float (&v)[K], int tpr, float (*s)[32]) 
     const int nw = tpr >> 5, w0 = w / nw * nw;  // the row's warps
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      float t = lane < nw ? s[k][w0 + lane] : 0.f;
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
+      float t = s[k][w0] + s[k][w0 + 1];
+      for (int q = 2; q < nw; q += 2) {
+        const float2 f = *reinterpret_cast<const float2*>(&s[k][w0 + q]);
+        t += f.x + f.y;
+      }
       v[k] = t;
     }
   }
 }
 
-// UPT vectors of VEC columns a thread: columns (lane + k * tpr) * VEC.  The
-// blocks are persistent: a thread keeps its columns' weight and bias in
-// registers through all its rows, and a row's loads are issued before the row
-// before it is worked on.
-template <typename TX, typename TY, int VEC, int UPT>
-__global__ void __launch_bounds__(kMaxRowThreads) norm_kernel(const __grid_constant__ NormParams p) {
-  __shared__ float s_red[2][1][32];
-  const int rows = blockDim.x / p.tpr;  // rows a block takes at once
-  const int row = threadIdx.x / p.tpr, lane = threadIdx.x % p.tpr;
-  float w[UPT][VEC], b[UPT][VEC];
+// 1 / sqrt(x): the approximation and one Newton step (relative error below 2^-22)
+__device__ __forceinline__ float inv_sqrt(float x) {
+  const float r = rsqrtf(x);
+  return isinf(r) || r == 0.f ? r : r * fmaf(-0.5f * x * r, r, 1.5f);  // 0 and infinity as they are
+}
+
+// Arithmetic on a thread's VEC columns, two at an instruction where there are 8.
+template <int VEC>
+__device__ __forceinline__ float vec_sum(const float (&f)[VEC]) {
+  if constexpr (VEC == 8) {
+    const float2 a = add2(add2(make_float2(f[0], f[1]), make_float2(f[2], f[3])),
+                          add2(make_float2(f[4], f[5]), make_float2(f[6], f[7])));
+    return a.x + a.y;
+  } else {
+    return f[0];
+  }
+}
+// f -= mu; the sum of its squares
+template <int VEC>
+__device__ __forceinline__ float vec_center(float (&f)[VEC], float mu) {
+  if constexpr (VEC == 8) {
+    float2 s = make_float2(0.f, 0.f);
 #pragma unroll
-  for (int k = 0; k < UPT; ++k) {
-    const int c = lane + k * p.tpr;
-    if (c < p.units) {
-      load_params(p.w, p.w_type, c * VEC, 1.0f, w[k]);
-      load_params(p.b, p.w_type, c * VEC, 0.0f, b[k]);
+    for (int j = 0; j < 8; j += 2) {
+      const float2 d = add2(make_float2(f[j], f[j + 1]), make_float2(-mu, -mu));
+      s = fma2(d, d, s);
+      f[j] = d.x;
+      f[j + 1] = d.y;
+    }
+    return s.x + s.y;
+  } else {
+    f[0] -= mu;
+    return f[0] * f[0];
+  }
+}
+// f r w + b
+template <int VEC>
+__device__ __forceinline__ void vec_affine(float (&f)[VEC], float r, const float (&w)[VEC], const float (&b)[VEC]) {
+  if constexpr (VEC == 8) {
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+      const float2 d = fma2(mul2(make_float2(f[j], f[j + 1]), make_float2(r, r)), make_float2(w[j], w[j + 1]),
+                            make_float2(b[j], b[j + 1]));
+      f[j] = d.x;
+      f[j + 1] = d.y;
+    }
+  } else {
+    f[0] = fmaf(f[0] * r, w[0], b[0]);
+  }
+}
+// Weight and bias of a thread's columns: in registers through all rows where a
+// thread has few columns, else in shared memory as fp32 (the block's copy), so
+// that the registers go to more rows an SM.
+template <int VEC, int UPT, int N>
+struct Params {
+  static constexpr bool kKeep = UPT * VEC <= 8;
+  float f[kKeep ? N : 1][kKeep ? UPT : 1][VEC];
+  const float* s;
+  // the block's threads all call; `s`: [N][D] floats
+  __device__ __forceinline__ void init(const NormParams& p, float* s, int lane) {
+    this->s = s;
+    if constexpr (kKeep) {
+#pragma unroll
+      for (int k = 0; k < UPT; ++k) {
+        const int c = lane + k * p.tpr;
+        if (c < p.units) {
+          load_params(p.w, p.w_type, c * VEC, 1.0f, f[0][k]);
+          if constexpr (N == 2) load_params(p.b, p.w_type, c * VEC, 0.0f, f[1][k]);
+        }
+      }
+    } else {
+      // a vector's halves lie in two planes: 16 bytes from lane to lane, no bank conflicts
+      for (int c = threadIdx.x; c < p.D; c += blockDim.x) {
+        const int at = VEC == 8 ? (c >> 2 & 1) * (p.D >> 1) + (c >> 3) * 4 + (c & 3) : c;
+        s[at] = p.w ? param_at(p.w, p.w_type, c) : 1.0f;
+        if (N == 2) s[p.D + at] = p.b ? param_at(p.b, p.w_type, c) : 0.0f;
+      }
+      __syncthreads();
     }
   }
+  __device__ __forceinline__ void get(int n, int k, int c, int D, float (&out)[VEC]) const {
+    if constexpr (kKeep) {
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) out[j] = f[n][k][j];
+    } else {
+      if constexpr (VEC == 8) {
+        RawVec<float, 8> r;
+        r.a = *reinterpret_cast<const float4*>(s + n * D + c * 4);
+        r.b = *reinterpret_cast<const float4*>(s + n * D + (D >> 1) + c * 4);
+        r.unpack(out);
+      } else {
+        out[0] = s[n * D + c];
+      }
+    }
+  }
+};
+
+// UPT vectors of VEC columns a thread: columns (lane + k * tpr) * VEC.  The
+// blocks are persistent, and a row's loads are issued before the row before it
+// is worked on.  EXACT: the threads' columns are the row's.
+template <typename TX, typename TY, int VEC, int UPT, bool EXACT>
+__global__ void __launch_bounds__(kMaxRowThreads, UPT * VEC <= 16 ? 2 : 1) norm_kernel(const __grid_constant__ NormParams p) {
+  __shared__ __align__(16) float s_red[2][1][32];
+  extern __shared__ __align__(16) float s_dyn[];
+  const int rows = blockDim.x / p.tpr;  // rows a block takes at once
+  const int row = threadIdx.x / p.tpr, lane = threadIdx.x % p.tpr;
+  Params<VEC, UPT, 2> par;
+  par.init(p, s_dyn, lane);
   const float inv = 1.0f / (float)p.D;
   const int64_t step = (int64_t)gridDim.x * rows;
+  auto mine = [&](int k) { return EXACT || lane + k * p.tpr < p.units; };
   RawVec<TX, VEC> raw[UPT];
   auto fetch = [&](int64_t i) {
+    const TX* x = static_cast<const TX*>(p.x) + (i < p.M ? i : p.M - 1) * p.x_stride + lane * VEC;
 #pragma unroll
-    for (int k = 0; k < UPT; ++k) {
-      const int c = lane + k * p.tpr;
-      if (i < p.M && c < p.units) raw[k].load(static_cast<const TX*>(p.x) + i * p.x_stride + (int64_t)c * VEC);
-    }
+    for (int k = 0; k < UPT; ++k)
+      if (mine(k)) raw[k].load(x + k * p.tpr * VEC);
   };
-  fetch((int64_t)blockIdx.x * rows + row);
+  int64_t i = (int64_t)blockIdx.x * rows + row;
+  fetch(i);
   // every thread of the block goes through the same number of steps (a warp may
-  // hold several rows, and all its lanes take part in the sums)
-  for (int64_t i0 = (int64_t)blockIdx.x * rows; i0 < p.M; i0 += step) {
-    const int64_t i = i0 + row;
-    const bool live = i < p.M;
+  // hold several rows, and all its lanes take part in the sums); a row past the
+  // last is the last one again, and is not stored
+  for (int64_t i0 = (int64_t)blockIdx.x * rows; i0 < p.M; i0 += step, i += step) {
     float v[UPT][VEC];
     float s[1] = {0.f};
 #pragma unroll
     for (int k = 0; k < UPT; ++k) {
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) v[k][j] = 0.f;
-      if (live && lane + k * p.tpr < p.units) raw[k].unpack(v[k]);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) s[0] += v[k][j];
+      if (!mine(k)) break;
+      raw[k].unpack(v[k]);
+      s[0] += vec_sum(v[k]);
     }
     fetch(i + step);
     row_sum<1>(s, p.tpr, s_red[0]);
@@ -155,29 +246,25 @@ __global__ void __launch_bounds__(kMaxRowThreads) norm_kernel(const __grid_const
     s[0] = 0.f;
 #pragma unroll
     for (int k = 0; k < UPT; ++k) {
-      if (lane + k * p.tpr >= p.units) break;
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        v[k][j] -= mu;
-        s[0] = fmaf(v[k][j], v[k][j], s[0]);
-      }
+      if (!mine(k)) break;
+      s[0] += vec_center(v[k], mu);
     }
     row_sum<1>(s, p.tpr, s_red[1]);
-    const float r = 1.0f / sqrtf(fmaf(s[0], inv, p.eps));
-    if (!live) continue;
+    const float r = inv_sqrt(fmaf(s[0], inv, p.eps));
+    if (i >= p.M) continue;
     if (lane == 0) {
       if (p.mean) p.mean[i] = mu;
       if (p.rstd) p.rstd[i] = r;
     }
-    TY* y = static_cast<TY*>(p.y) + i * p.y_stride;
+    TY* y = static_cast<TY*>(p.y) + i * p.y_stride + lane * VEC;
 #pragma unroll
     for (int k = 0; k < UPT; ++k) {
-      const int c = lane + k * p.tpr;
-      if (c >= p.units) break;
-      float f[VEC];
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) f[j] = fmaf(v[k][j] * r, w[k][j], b[k][j]);
-      store_vec(y + (int64_t)c * VEC, f);
+      if (!mine(k)) break;
+      float w[VEC], b[VEC];
+      par.get(0, k, lane + k * p.tpr, p.D, w);
+      par.get(1, k, lane + k * p.tpr, p.D, b);
+      vec_affine(v[k], r, w, b);
+      store_vec(y + k * p.tpr * VEC, v[k]);
     }
   }
 }
@@ -185,7 +272,7 @@ __global__ void __launch_bounds__(kMaxRowThreads) norm_kernel(const __grid_const
 // Rows wider than the registers of a block hold: three reads of the row.
 template <typename TX, typename TY>
 __global__ void __launch_bounds__(kWideThreads) norm_wide_kernel(const __grid_constant__ NormParams p) {
-  __shared__ float s_red[2][1][32];
+  __shared__ __align__(16) float s_red[2][1][32];
   const TX* x = static_cast<const TX*>(p.x) + (int64_t)blockIdx.x * p.x_stride;
   TY* y = static_cast<TY*>(p.y) + (int64_t)blockIdx.x * p.y_stride;
   float s[1] = {0.f};
@@ -209,19 +296,20 @@ __global__ void __launch_bounds__(kWideThreads) norm_wide_kernel(const __grid_co
   }
 }
 
-template <typename TX, typename TY, int VEC, int UPT>
+template <typename TX, typename TY, int VEC, int UPT, bool EXACT>
 __global__ void __launch_bounds__(kMaxRowThreads) norm_back_kernel(const __grid_constant__ NormParams p) {
-  __shared__ float s_red[2][2][32];
-  extern __shared__ float s_part[];  // [2][tpr * UPT * VEC] sums of the block's rows at once
+  __shared__ __align__(16) float s_red[2][2][32];
+  // the weight (Params), and later [2][tpr * UPT * VEC] sums of the block's rows
+  extern __shared__ __align__(16) float s_part[];
   const int rows = blockDim.x / p.tpr, row = threadIdx.x / p.tpr, lane = threadIdx.x % p.tpr;
-  float w[UPT][VEC], dw[UPT][VEC], db[UPT][VEC];
+  Params<VEC, UPT, 1> par;
+  par.init(p, s_part, lane);
+  float dw[UPT][VEC], db[UPT][VEC];
 #pragma unroll
-  for (int k = 0; k < UPT; ++k) {
-    const int c = lane + k * p.tpr;
+  for (int k = 0; k < UPT; ++k)
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) w[k][j] = dw[k][j] = db[k][j] = 0.f;
-    if (c < p.units) load_params(p.w, p.w_type, c * VEC, 1.0f, w[k]);
-  }
+    for (int j = 0; j < VEC; ++j) dw[k][j] = db[k][j] = 0.f;
+  auto mine = [&](int k) { return EXACT || lane + k * p.tpr < p.units; };
   const float inv = 1.0f / (float)p.D;
   const int64_t step = (int64_t)gridDim.x * rows;
   int flip = 0;
@@ -233,7 +321,7 @@ __global__ void __launch_bounds__(kMaxRowThreads) norm_back_kernel(const __grid_
 #pragma unroll
     for (int k = 0; k < UPT; ++k) {
       const int c = lane + k * p.tpr;
-      if (c < p.units) {
+      if (mine(k)) {
         rx[k].load(static_cast<const TX*>(p.x) + i * p.x_stride + (int64_t)c * VEC);
         rg[k].load(static_cast<const TY*>(p.gy) + i * p.gy_stride + (int64_t)c * VEC);
       }
@@ -254,15 +342,17 @@ __global__ void __launch_bounds__(kMaxRowThreads) norm_back_kernel(const __grid_
       const int c = lane + k * p.tpr;
 #pragma unroll
       for (int j = 0; j < VEC; ++j) xh[k][j] = g[k][j] = 0.f;
-      if (live && c < p.units) {
+      if (live && mine(k)) {
         rx[k].unpack(xh[k]);
         rg[k].unpack(g[k]);
+        float w[VEC];
+        par.get(0, k, c, p.D, w);
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
           xh[k][j] = (xh[k][j] - mu) * r;
           db[k][j] += g[k][j];
           dw[k][j] = fmaf(g[k][j], xh[k][j], dw[k][j]);
-          g[k][j] *= w[k][j];
+          g[k][j] *= w[j];
           s[0] += g[k][j];
           s[1] = fmaf(g[k][j], xh[k][j], s[1]);
         }
@@ -277,7 +367,7 @@ __global__ void __launch_bounds__(kMaxRowThreads) norm_back_kernel(const __grid_
 #pragma unroll
       for (int k = 0; k < UPT; ++k) {
         const int c = lane + k * p.tpr;
-        if (c >= p.units) break;
+        if (!mine(k)) break;
         float f[VEC];
 #pragma unroll
         for (int j = 0; j < VEC; ++j) f[j] = r * (g[k][j] - m0 - xh[k][j] * m1);
@@ -286,6 +376,7 @@ __global__ void __launch_bounds__(kMaxRowThreads) norm_back_kernel(const __grid_
     }
   }
   if (!p.partial) return;
+  __syncthreads();  // the weight is done with
   // the block's rows, added in row order
   const int cols = p.tpr * UPT * VEC;
   for (int q = 0; q < rows; ++q) {
@@ -312,7 +403,7 @@ __global__ void __launch_bounds__(kMaxRowThreads) norm_back_kernel(const __grid_
 // live in its partial row in global memory (no other block touches it).
 template <typename TX, typename TY>
 __global__ void __launch_bounds__(kWideThreads) norm_back_wide_kernel(const __grid_constant__ NormParams p) {
-  __shared__ float s_red[2][2][32];
+  __shared__ __align__(16) float s_red[2][2][32];
   float* out = p.partial ? p.partial + (int64_t)blockIdx.x * 2 * p.D : nullptr;
   if (out)
     for (int c = threadIdx.x; c < 2 * p.D; c += kWideThreads) out[c] = 0.f;
@@ -347,17 +438,18 @@ __global__ void __launch_bounds__(kWideThreads) norm_back_wide_kernel(const __gr
 
 // dw and db from the blocks' sums: 32 columns a block, warp k the k-th part of
 // the blocks in order, fp64.
-__global__ void __launch_bounds__(1024) norm_join_kernel(const float* partial, int blocks, int D, int w_type, void* dw,
+__global__ void __launch_bounds__(1024) norm_join_kernel(float* partial, int blocks, int D, int w_type, void* dw,
                                                          void* db) {
   __shared__ double s[32][33];
   const int lane = threadIdx.x & 31, k = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;  // columns of [dw | db]
   double t = 0.0;
   const int per = (blocks + 31) / 32;
+  pdl_wait();
   if (c < 2 * D) {
     const int q1 = min((k + 1) * per, blocks);
 #pragma unroll 8
-    for (int q = k * per; q < q1; ++q) t += (double)__ldg(partial + (int64_t)q * 2 * D + c);
+    for (int q = k * per; q < q1; ++q) t += (double)partial[(int64_t)q * 2 * D + c];
   }
   s[k][lane] = t;
   __syncthreads();
@@ -380,64 +472,98 @@ int row_threads(int units, int upt) {
   return t <= kMaxRowThreads ? t : 0;
 }
 
-// persistent blocks: as many as the SMs hold at `threads` threads an SM
-int persistent_blocks(int64_t M, int rows, int block, int threads) {
-  return (int)std::min<int64_t>((M + rows - 1) / rows, (int64_t)kSMs * std::max(1, threads / block));
+// Blocks of `kernel` that all SMs hold at once; asked for once, `cache` is the
+// kernel's own (its block size and shared memory may differ: one entry a log2
+// of the block's threads).
+template <typename K>
+int resident_blocks(K kernel, int block, size_t smem, std::atomic<int> (&cache)[16]) {
+  int at = 0;
+  while ((1 << at) < block) ++at;
+  int n = cache[at].load(std::memory_order_relaxed);
+  if (n == 0) {
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, block, smem) != cudaSuccess || n < 1) n = 1;
+    cache[at].store(n, std::memory_order_relaxed);
+  }
+  return n * kSMs;
+}
+
+// dynamic shared memory beyond the default, once asked for
+template <typename K>
+cudaError_t more_smem(K kernel, size_t smem) {
+  return smem > 48 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)
+                          : cudaSuccess;
+}
+
+template <typename TX, typename TY, int VEC, int UPT, bool EXACT>
+cudaError_t norm_go(const NormParams& p, cudaStream_t s) {
+  static std::atomic<int> cache[16];
+  auto kernel = norm_kernel<TX, TY, VEC, UPT, EXACT>;
+  const int block = std::max(p.tpr, 128), rows = block / p.tpr;
+  const size_t smem = Params<VEC, UPT, 2>::kKeep ? 0 : (size_t)p.D * 8;  // at most 128 KB
+  const cudaError_t e = more_smem(kernel, smem);
+  if (e != cudaSuccess) return e;
+  const int grid = (int)std::min<int64_t>((p.M + rows - 1) / rows, resident_blocks(kernel, block, smem, cache));
+  kernel<<<grid, block, smem, s>>>(p);
+  return cudaGetLastError();
 }
 
 template <typename TX, typename TY, int VEC>
 cudaError_t norm_launch(NormParams p, cudaStream_t s) {
   p.units = p.D / VEC;
   LaunchScope ls("layer_norm", s);
-  // a warp's width of threads first, then up to 16 columns a thread, then more
-  // threads, then up to 32 (single columns: 8) a thread
-  const int most = VEC == 8 ? 4 : 8;
+  // A warp a row, up to two vectors a thread (single columns: 8), then more
+  // threads.  More columns a thread share the sums' shuffles and barriers, fewer
+  // leave registers for more rows an SM: 16384 x 4096 bf16 takes 89 us at 8
+  // columns (issue), 97 at 32 (latency at 16 warps an SM).
   int upt = p.units <= 32 ? 1 : 2;
   if (VEC == 1 && p.units > 64) upt = 8;
   p.tpr = row_threads(p.units, upt);
-  if (!p.tpr) p.tpr = row_threads(p.units, upt = most);
+  if (VEC == 8 && !p.tpr) p.tpr = row_threads(p.units, upt = 4);
   if (!p.tpr) {
     norm_wide_kernel<TX, TY><<<(unsigned)p.M, kWideThreads, 0, s>>>(p);
     return cudaGetLastError();
   }
-  const int block = std::max(p.tpr, 128), rows = block / p.tpr;
-  const int grid = persistent_blocks(p.M, rows, block, upt == 1 ? 1536 : 1024);
-  if (upt == 1) norm_kernel<TX, TY, VEC, 1><<<grid, block, 0, s>>>(p);
-  else if (upt == 2) norm_kernel<TX, TY, VEC, 2><<<grid, block, 0, s>>>(p);
-  else norm_kernel<TX, TY, VEC, VEC == 8 ? 4 : 8><<<grid, block, 0, s>>>(p);
-  return cudaGetLastError();
+  const bool exact = p.tpr * upt == p.units;
+  if (upt == 1) return norm_go<TX, TY, VEC, 1, false>(p, s);
+  if (upt == 2) return exact ? norm_go<TX, TY, VEC, 2, true>(p, s) : norm_go<TX, TY, VEC, 2, false>(p, s);
+  return norm_go<TX, TY, VEC, VEC == 8 ? 4 : 8, false>(p, s);
 }
 
 // blocks of the backward (its partial sums' rows): the same for every type
-int back_blocks(int64_t M) { return (int)std::min<int64_t>(M, kSMs * 4); }
+int back_blocks(int64_t M) { return (int)std::min<int64_t>(M, kSMs * 6); }
+
+template <typename TX, typename TY, int VEC, int UPT, bool EXACT>
+cudaError_t back_go(const NormParams& p, cudaStream_t s, int* blocks_out) {
+  static std::atomic<int> cache[16];
+  auto kernel = norm_back_kernel<TX, TY, VEC, UPT, EXACT>;
+  const int block = std::max(p.tpr, 256), rows = block / p.tpr;
+  const size_t smem = (size_t)2 * p.tpr * UPT * VEC * 4;  // at most 64 KB
+  const cudaError_t e = more_smem(kernel, smem);
+  if (e != cudaSuccess) return e;
+  const int64_t most = std::min<int64_t>(back_blocks(p.M), (p.M + rows - 1) / rows);
+  const int grid = (int)std::min<int64_t>(most, resident_blocks(kernel, block, smem, cache));
+  *blocks_out = grid;
+  kernel<<<grid, block, smem, s>>>(p);
+  return cudaGetLastError();
+}
 
 template <typename TX, typename TY, int VEC>
 cudaError_t back_launch(NormParams p, cudaStream_t s, int* blocks_out) {
   p.units = p.D / VEC;
   LaunchScope ls("layer_norm_backward", s);
+  // as the forward, but at most two vectors a thread: it keeps two sums a column
   const int upt = p.units <= 32 ? 1 : VEC == 1 && p.units > 64 ? 8 : 2;
   p.tpr = row_threads(p.units, upt);
-  int blocks = back_blocks(p.M);
   if (!p.tpr) {
-    *blocks_out = blocks;
-    norm_back_wide_kernel<TX, TY><<<blocks, kWideThreads, 0, s>>>(p);
+    *blocks_out = back_blocks(p.M);
+    norm_back_wide_kernel<TX, TY><<<*blocks_out, kWideThreads, 0, s>>>(p);
     return cudaGetLastError();
   }
-  const int block = std::max(p.tpr, 256), rows = block / p.tpr;
-  blocks = std::min(blocks, persistent_blocks(p.M, rows, block, 1024));
-  *blocks_out = blocks;
-  const size_t smem = p.partial ? (size_t)2 * p.tpr * upt * VEC * 4 : 0;
-  auto go = [&](auto kernel) {
-    if (smem > 48 * 1024) {
-      const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-      if (e != cudaSuccess) return e;
-    }
-    kernel<<<blocks, block, smem, s>>>(p);
-    return cudaGetLastError();
-  };
-  if (upt == 1) return go(norm_back_kernel<TX, TY, VEC, 1>);
-  if (upt == 2) return go(norm_back_kernel<TX, TY, VEC, 2>);
-  return go(norm_back_kernel<TX, TY, VEC, VEC == 1 ? 8 : 2>);
+  const bool exact = p.tpr * upt == p.units;
+  if (upt == 1) return back_go<TX, TY, VEC, 1, false>(p, s, blocks_out);
+  if (VEC == 1) return upt == 2 ? back_go<TX, TY, VEC, 2, false>(p, s, blocks_out)
+                                : back_go<TX, TY, VEC, VEC == 1 ? 8 : 2, false>(p, s, blocks_out);
+  return exact ? back_go<TX, TY, VEC, 2, true>(p, s, blocks_out) : back_go<TX, TY, VEC, 2, false>(p, s, blocks_out);
 }
 
 bool norm_sizes_ok(int64_t M, int32_t D) { return M >= 0 && M <= INT32_MAX && D >= 1 && D <= 65536; }
@@ -554,9 +680,9 @@ extern "C" recis_status recis_layer_norm_backward(const void* grad_y, int32_t y_
   if (e != cudaSuccess) return cuda_fail(e, "layer_norm_backward launch");
   if (sums) {
     LaunchScope ls("layer_norm_join", s);
-    norm_join_kernel<<<(unsigned)((2 * D + 31) / 32), 1024, 0, s>>>(p.partial, blocks, D, w_type, grad_weight,
-                                                                  grad_bias);
-    if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "layer_norm_join launch");
+    e = launch_pdl(norm_join_kernel, (unsigned)((2 * D + 31) / 32), 1024, 0, s, p.partial, blocks, D, w_type,
+                   grad_weight, grad_bias);
+    if (e != cudaSuccess) return cuda_fail(e, "layer_norm_join launch");
   }
   return RECIS_OK;
 }
