@@ -86,6 +86,8 @@ __global__ void __launch_bounds__(kFewWarps * 32 + 32)
   const int h = id % p.Hkv;
   id /= p.Hkv;
   const int sp = id % p.splits, b = id / p.splits;
+  pdl_wait();
+  pdl_trigger();  // the join may be brought in; it waits for this grid's end
   const Bag bag = load_bag(p, b);
   const int rows = bag.nq * p.G, r0 = rt * kRowTile;
   const int ks = sp * p.split_keys, ke = min(ks + p.split_keys, bag.nk);
@@ -138,8 +140,15 @@ __global__ void __launch_bounds__(kFewWarps * 32 + 32)
     // the lane's rows of K and V for the matrix loads, and its swizzle
     const int krow = w * 16 + (lane >> 4) * 8 + (lane & 7), vrow = w * 16 + ((lane >> 3) & 1) * 8 + (lane & 7);
     const int kch = (lane >> 3) & 1, vch = lane >> 4, sw = lane & 7;
+    auto takes = [&](int j) {  // whether the lane's key (of 16) of tile j takes part
+      const int key = ks + j * kFewKeys + w * 16 + (lane & 15);
+      return key < ke && (!p.mask || p.mask[bag.k0 + key]);
+    };
+    bool v_next = n > 0 && takes(0);
     for (int j = 0; j < n; ++j) {
       const int st = j % NS, k0 = ks + j * kFewKeys + w * 16;  // the warp's first key
+      const bool v = v_next;
+      v_next = j + 1 < n && takes(j + 1);
       ok = mbar_wait(full + st, (j / NS) & 1, spin_max);
       if (!__all_sync(0xffffffffu, ok)) {
         ok = false;
@@ -161,8 +170,6 @@ __global__ void __launch_bounds__(kFewWarps * 32 + 32)
       }
       if (k0 + 16 > ke || p.mask) {
         // keys that take no part: their scores -inf, their rows of V zeros (0 * NaN is NaN)
-        const int key = k0 + (lane & 15);
-        const bool v = key < ke && (!p.mask || p.mask[bag.k0 + key]);
         const unsigned bits = __ballot_sync(0xffffffffu, v);
 #pragma unroll
         for (int t = 0; t < 2; ++t)
@@ -298,6 +305,7 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Atten
   const int lane = threadIdx.x & 31;
   const int tiles = (p.max_q * p.Hq + 3) / 4;
   const int b = blockIdx.x / tiles, i = (blockIdx.x % tiles) * 4 + (threadIdx.x >> 5);
+  pdl_wait();
   const Bag bag = load_bag(p, b);
   if (i >= bag.nq * p.Hq) return;
   const int64_t t = bag.q0 + i / p.Hq;
@@ -305,7 +313,7 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Atten
   const int n = max(1, (bag.nk + p.split_keys - 1) / p.split_keys);
   const int64_t step = p.Tq * p.Hq, at = t * p.Hq + hq;
   float m = -INFINITY;
-  for (int s = lane; s < n; s += 32) m = fmaxf(m, __ldg(p.pl + s * step + at));
+  for (int s = lane; s < n; s += 32) m = fmaxf(m, p.pl[s * step + at]);
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
   const float base = m == -INFINITY ? 0.f : m;
@@ -313,7 +321,7 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Atten
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   const int d = lane * 4;
   for (int s = 0; s < n; ++s) {
-    const float f = expf(__ldg(p.pl + s * step + at) - base);
+    const float f = expf(p.pl[s * step + at] - base);
     sum += f;
     if (d < p.D) {
       const float4 v = *reinterpret_cast<const float4*>(p.po + (s * step + at) * p.D + d);
@@ -442,8 +450,7 @@ cudaError_t few_launch(const AttendParams& p, const CUtensorMap& mk, const CUten
   static std::atomic<uint64_t> done[2];
   const cudaError_t e = allow_smem(kernel, FewCfg<DP>::kTotal, done);
   if (e != cudaSuccess) return e;
-  kernel<<<(unsigned)grid, kFewWarps * 32 + 32, FewCfg<DP>::kTotal, s>>>(p, mk, mv, spin_limit());
-  return cudaGetLastError();
+  return launch_pdl(kernel, (unsigned)grid, kFewWarps * 32 + 32, FewCfg<DP>::kTotal, s, p, mk, mv, spin_limit());
 }
 
 template <typename T>
@@ -473,8 +480,8 @@ recis_status forward(const AttendParams& p, cudaStream_t s) {
   cudaError_t e;
   if (p.splits > 1) {
     LaunchScope ls("attend_join", s);
-    join_kernel<T><<<(unsigned)jgrid, 128, 0, s>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "attend_join launch");
+    e = launch_pdl(join_kernel<T>, (unsigned)jgrid, 128, 0, s, p);
+    if (e != cudaSuccess) return cuda_fail(e, "attend_join launch");
   }
   return RECIS_OK;
 }

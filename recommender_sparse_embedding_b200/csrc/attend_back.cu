@@ -81,6 +81,8 @@ __global__ void __launch_bounds__(BackCfg<DP, KEYS>::kThreads, 1)
   id /= per_bag;
   const int h = id % p.Hkv;
   id /= p.Hkv;
+  pdl_wait();
+  pdl_trigger();  // the next kernel may be brought in; it waits for this grid's end
   const int sp = KEYS ? 0 : id % p.splits, b = KEYS ? id : id / p.splits;
   const Bag bag = load_bag(p, b);
   const int first = tile * (KEYS ? kX : TQ);                // first key, or query, of the tile
@@ -437,6 +439,8 @@ __global__ void __launch_bounds__(BackCfg<DP, KEYS>::kThreads, 1)
 // head), 8 columns each.
 template <typename T>
 __global__ void __launch_bounds__(256) delta_kernel(const __grid_constant__ AttendParams p) {
+  pdl_wait();
+  pdl_trigger();
   const int lane = threadIdx.x & 15, d = lane * 8;
   const int64_t i = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
   float s = 0.f;
@@ -467,6 +471,7 @@ __global__ void __launch_bounds__(128) join_q_kernel(const __grid_constant__ Att
   const int lane = threadIdx.x & 31, d = lane * 4;
   const int tiles = (p.max_q * p.Hq + 3) / 4;
   const int b = blockIdx.x / tiles, i = (blockIdx.x % tiles) * 4 + (threadIdx.x >> 5);
+  pdl_wait();
   const Bag bag = load_bag(p, b);
   if (i >= bag.nq * p.Hq || d >= p.D) return;
   const int64_t t = bag.q0 + i / p.Hq, step = p.Tq * p.Hq;
@@ -490,8 +495,7 @@ cudaError_t back_launch(const AttendParams& p, const BackMaps& m, int64_t grid, 
   static std::atomic<uint64_t> done[2];
   const cudaError_t e = allow_smem(kernel, C::kTotal, done);
   if (e != cudaSuccess) return e;
-  kernel<<<(unsigned)grid, C::kThreads, C::kTotal, s>>>(p, m, spin_limit());
-  return cudaGetLastError();
+  return launch_pdl(kernel, (unsigned)grid, C::kThreads, C::kTotal, s, p, m, spin_limit());
 }
 
 // joins the parts of grad_q
@@ -504,8 +508,7 @@ recis_status join_q(const AttendParams& p, cudaStream_t s) {
     return RECIS_ERR_INVALID_ARG;
   }
   LaunchScope ls("attend_join_q", s);
-  join_q_kernel<T><<<(unsigned)grid, 128, 0, s>>>(p);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_pdl(join_q_kernel<T>, (unsigned)grid, 128, 0, s, p);
   return e == cudaSuccess ? RECIS_OK : cuda_fail(e, "attend_join_q launch");
 }
 
@@ -545,8 +548,8 @@ recis_status back(const AttendParams& p, cudaStream_t s) {
   cudaError_t e;
   if (dgrid > 0) {
     LaunchScope ls("attend_delta", s);
-    delta_kernel<T><<<(unsigned)dgrid, 256, 0, s>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "attend_delta launch");
+    e = launch_pdl(delta_kernel<T>, (unsigned)dgrid, 256, 0, s, p);
+    if (e != cudaSuccess) return cuda_fail(e, "attend_delta launch");
   }
   if (kgrid > 0) {
     LaunchScope ls("attend_back_keys", s);

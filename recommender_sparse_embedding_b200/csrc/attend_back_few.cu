@@ -65,6 +65,8 @@ __global__ void __launch_bounds__(kThreads, FewBackCfg<DP, NR>::kTwo ? 2 : 1)
   const int h = id % p.Hkv;
   id /= p.Hkv;
   const int sp = id % p.splits, b = id / p.splits;
+  pdl_wait();
+  pdl_trigger();  // the join may be brought in; it waits for this grid's end
   const Bag bag = load_bag(p, b);
   const int rows = bag.nq * p.G;  // <= NR
   const int ks = sp * p.split_keys, ke = min(ks + p.split_keys, bag.nk);
@@ -363,8 +365,7 @@ cudaError_t few_back_launch(const AttendParams& p, const CUtensorMap (&m)[4], in
   static std::atomic<uint64_t> done[2];
   const cudaError_t e = allow_smem(kernel, C::kTotal, done);
   if (e != cudaSuccess) return e;
-  kernel<<<(unsigned)grid, kThreads, C::kTotal, s>>>(p, m[0], m[1], m[2], m[3], spin_limit());
-  return cudaGetLastError();
+  return launch_pdl(kernel, (unsigned)grid, kThreads, C::kTotal, s, p, m[0], m[1], m[2], m[3], spin_limit());
 }
 
 }  // namespace

@@ -64,6 +64,8 @@ __global__ void __launch_bounds__(kTcThreads, 2)
   id /= qtiles;
   const int h = id % p.Hkv;
   id /= p.Hkv;
+  pdl_wait();
+  pdl_trigger();  // the join may be brought in; it waits for this grid's end
   const int sp = id % p.splits, b = id / p.splits;
   const Bag bag = load_bag(p, b);
   const int t0 = qt * TQ;
@@ -348,8 +350,7 @@ static cudaError_t tc_launch(const AttendParams& p, const CUtensorMap& mq, const
   const cudaError_t e =
       allow_smem(kernel, FwdSmem<DP>::kTotal, done);
   if (e != cudaSuccess) return e;
-  kernel<<<(unsigned)grid, kTcThreads, FwdSmem<DP>::kTotal, s>>>(p, mq, mk, mv, spin_limit());
-  return cudaGetLastError();
+  return launch_pdl(kernel, (unsigned)grid, kTcThreads, FwdSmem<DP>::kTotal, s, p, mq, mk, mv, spin_limit());
 }
 
 recis_status launch_attend_tc(const AttendParams& p, bool bf16, cudaStream_t s) {
