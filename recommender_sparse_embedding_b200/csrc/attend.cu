@@ -140,15 +140,18 @@ __global__ void __launch_bounds__(kFewWarps * 32 + 32)
     // the lane's rows of K and V for the matrix loads, and its swizzle
     const int krow = w * 16 + (lane >> 4) * 8 + (lane & 7), vrow = w * 16 + ((lane >> 3) & 1) * 8 + (lane & 7);
     const int kch = (lane >> 3) & 1, vch = lane >> 4, sw = lane & 7;
-    auto takes = [&](int j) {  // whether the lane's key (of 16) of tile j takes part
+    // whether the lane's key (of 16) of tile j takes part: not 0 (the byte is not looked at before its turn)
+    auto takes = [&](int j) -> unsigned {
       const int key = ks + j * kFewKeys + w * 16 + (lane & 15);
-      return key < ke && (!p.mask || p.mask[bag.k0 + key]);
+      unsigned m = key < ke;
+      if (m && p.mask) m = __ldg(p.mask + bag.k0 + key);
+      return m;
     };
-    bool v_next = n > 0 && takes(0);
+    unsigned v_next = takes(0);
     for (int j = 0; j < n; ++j) {
       const int st = j % NS, k0 = ks + j * kFewKeys + w * 16;  // the warp's first key
-      const bool v = v_next;
-      v_next = j + 1 < n && takes(j + 1);
+      const unsigned v = v_next;
+      v_next = takes(j + 1);
       ok = mbar_wait(full + st, (j / NS) & 1, spin_max);
       if (!__all_sync(0xffffffffu, ok)) {
         ok = false;
@@ -168,23 +171,18 @@ __global__ void __launch_bounds__(kFewWarps * 32 + 32)
         mma16816<T>(s[0], qa[i], kf[0], kf[1]);
         mma16816<T>(s[1], qa[i], kf[2], kf[3]);
       }
-      if (k0 + 16 > ke || p.mask) {
-        // keys that take no part: their scores -inf, their rows of V zeros (0 * NaN is NaN)
-        const unsigned bits = __ballot_sync(0xffffffffu, v);
+      uint32_t keep[2] = {0xffffffffu, 0xffffffffu};  // the lane's pairs of keys in V's registers
+      const bool some = k0 + 16 > ke || p.mask;
+      if (some) {
+        // keys that take no part: their scores -inf, their values zeros (0 * NaN is NaN)
+        const unsigned bits = __ballot_sync(0xffffffffu, v != 0);
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int t = 0; t < 2; ++t) {
+          const unsigned pair = bits >> (t * 8 + 2 * c);
+          keep[t] = (pair & 1 ? 0x0000ffffu : 0u) | (pair & 2 ? 0xffff0000u : 0u);
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (!(bits >> (t * 8 + 2 * c + (i & 1)) & 1)) s[t][i] = -INFINITY;
-            else s[t][i] *= p.scale_log2;
-        if (!v && lane < 16)
-          for (int i = 0; i < C::kBlocks; ++i) {
-            uint4* row = reinterpret_cast<uint4*>(base + (2 * st + 1) * C::kBytes + (i * kFewKeys + w * 16 + lane) * 128);
-#pragma unroll
-            for (int u = 0; u < 8; ++u) row[u] = make_uint4(0, 0, 0, 0);
-          }
-        fence_async_smem();
-        __syncwarp();
+          for (int i = 0; i < 4; ++i) s[t][i] = pair >> (i & 1) & 1 ? s[t][i] * p.scale_log2 : -INFINITY;
+        }
       } else {
 #pragma unroll
         for (int t = 0; t < 2; ++t)
@@ -228,6 +226,12 @@ __global__ void __launch_bounds__(kFewWarps * 32 + 32)
       for (int i = 0; i < DP / 16; ++i) {
         uint32_t vf[4];
         ldsm4t(vf, av + (i >> 2) * kFewKeys * 128 + ((((i & 3) * 2 + vch) ^ sw) << 4));
+        if (some) {
+          vf[0] &= keep[0];
+          vf[1] &= keep[1];
+          vf[2] &= keep[0];
+          vf[3] &= keep[1];
+        }
         mma16816<T>(o[2 * i], pa, vf[0], vf[1]);
         mma16816<T>(o[2 * i + 1], pa, vf[2], vf[3]);
       }

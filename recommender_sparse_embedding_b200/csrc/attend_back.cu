@@ -146,10 +146,13 @@ __global__ void __launch_bounds__(BackCfg<DP, KEYS>::kThreads, 1)
           t.a += tq;
         }
       };
-      auto takes = [&](const At& t, int i) {  // whether the lane's i-th row of the tile takes part
+      // whether the lane's i-th row of the tile takes part: not 0 (a mask's byte is not looked at before its turn)
+      auto takes = [&](const At& t, int i) -> unsigned {
         if (KEYS) return rq[i] < tq && t.a + rq[i] < bag.nq && t.g + rg[i] < p.G;
         const int key = t.a + lane + 32 * i;
-        return key < ke && (!p.mask || p.mask[bag.k0 + key]);
+        unsigned m = key < ke;
+        if (m && p.mask) m = __ldg(p.mask + bag.k0 + key);
+        return m;
       };
       auto special = [&](const At& t) {  // whether it holds rows that must be zeroed
         if (!KEYS) return t.a + kY > ke || p.mask != nullptr;
@@ -159,7 +162,8 @@ __global__ void __launch_bounds__(BackCfg<DP, KEYS>::kThreads, 1)
       // a special tile is finished a step after it is asked for; what its
       // finishing needs (masks) is read a step before that
       At at = {KEYS ? 0 : ks, 0}, ahead = at;
-      bool v[2] = {false, false}, v_next[2] = {takes(at, 0), takes(at, 1)}, last_special = false;
+      unsigned v[2] = {0, 0}, v_next[2] = {takes(at, 0), takes(at, 1)};
+      bool last_special = false;
       next(ahead);
       int st = 0, last_st = 0;
       unsigned ph = 0, last_ph = 0;
@@ -168,7 +172,7 @@ __global__ void __launch_bounds__(BackCfg<DP, KEYS>::kThreads, 1)
           if (!KEYS)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              const unsigned bits = __ballot_sync(0xffffffffu, v[i]);
+              const unsigned bits = __ballot_sync(0xffffffffu, v[i] != 0);
               if (lane == 0) s_valid[last_st][i] = bits;
             }
           ok = mbar_wait(y_raw + last_st, last_ph, spin_max) && ok;
@@ -223,8 +227,8 @@ __global__ void __launch_bounds__(BackCfg<DP, KEYS>::kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const int64_t r = v[i] ? (bag.q0 + at.a + rq[i]) * p.Hq + h * p.G + at.g + rg[i] : 0;
-            copy4(s_lse + st * kY + lane + 32 * i, p.nlse + r, v[i]);
-            copy4(s_delta + st * kY + lane + 32 * i, p.delta + r, v[i]);
+            copy4(s_lse + st * kY + lane + 32 * i, p.nlse + r, v[i] != 0);
+            copy4(s_delta + st * kY + lane + 32 * i, p.delta + r, v[i] != 0);
           }
           copy_arrive(y_full + st);
         }

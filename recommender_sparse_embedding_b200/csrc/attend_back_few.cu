@@ -226,15 +226,18 @@ __global__ void __launch_bounds__(kThreads, FewBackCfg<DP, NR>::kTwo ? 2 : 1)
     // where the thread's key lies in dS's rows: its 16-byte chunk is swizzled by the row
     uint8_t* ds_at = sds + (key >> 6) * 16384 + (key & 7) * 2;
     const int chunk = (key & 63) >> 3;
-    auto mask_at = [&](int j) {
+    // whether the thread's key of tile j takes part: not 0 (the byte is not looked at before its turn)
+    auto mask_at = [&](int j) -> unsigned {
       const int i = ks + j * kKeys + key;
-      return i < ke && (!p.mask || p.mask[bag.k0 + i]);
+      unsigned m = i < ke;
+      if (m && p.mask) m = __ldg(p.mask + bag.k0 + i);
+      return m;
     };
-    bool takes_next = n > 0 && mask_at(0);
+    unsigned takes_next = mask_at(0);
     for (int j = 0; j < n; ++j) {
       const int k0 = ks + j * kKeys;
-      const bool takes = takes_next;
-      takes_next = j + 1 < n && mask_at(j + 1);
+      const bool takes = takes_next != 0;
+      takes_next = mask_at(j + 1);
       // a warp that gave up goes on without waiting: the block's barriers need it
       ok = ok && mbar_wait(s_full, j & 1, spin_max);
       __syncwarp();
