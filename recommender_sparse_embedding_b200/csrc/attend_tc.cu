@@ -172,14 +172,22 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     const float c = p.scale_log2;
     // the score of a key that takes no part: -inf once scaled (c is never 0)
     const uint32_t out_of = __float_as_uint(c >= 0.f ? -INFINITY : INFINITY);
+    // whether key tid of step j takes part: not 0 (the byte is not looked at before its turn)
+    auto takes = [&](int j) -> unsigned {
+      const int key = ks + j * kTile + tid;
+      unsigned m = key < ke;
+      if (m && p.mask) m = __ldg(p.mask + bag.k0 + key);
+      return m;
+    };
+    unsigned v_next = takes(0);
     float m = -INFINITY, l = 0.f;
     for (int j = 0; j < n; ++j) {
       const int k0 = ks + j * kTile;
       const bool tail = k0 + kTile > ke || p.mask;
+      const unsigned v = v_next;
+      v_next = takes(j + 1);
       if (tail) {  // which of the tile's keys take part
-        const int key = k0 + tid;
-        const bool v = key < ke && (!p.mask || p.mask[bag.k0 + key]);
-        const unsigned bits = __ballot_sync(0xffffffffu, v);
+        const unsigned bits = __ballot_sync(0xffffffffu, v != 0);
         if (lane == 0) s_valid[j & 1][w] = bits;
         asm volatile("bar.sync 1, 128;" ::: "memory");
         const int st = j % NS;
