@@ -1,5 +1,5 @@
 // attend.cu -- attention of each bag's queries over the bag's keys: argument
-// checks, the plan of a call, and the forward pass for few queries.
+// checks, the plan of a call, and the forward pass for few rows.
 //
 //   s = scale q k^T over the bag's unmasked keys, out = softmax(s) v,
 //   lse = log sum exp s;  a bag without keys: out 0, lse -inf.
@@ -392,12 +392,13 @@ AttendPlan attend_plan(const recis_attend_args& a, bool backward) {
 }
 
 recis_status check_sizes(const recis_attend_args* a, const char* what) {
-  const int64_t top = INT32_MAX;
+  // room below 2^31 for coordinates and counts rounded up to tiles
+  const int64_t top = INT32_MAX - 65536, bound = (int64_t)1 << 30;
   if (!a || (a->type != RECIS_BF16 && a->type != RECIS_F16) || a->D < 8 || a->D > 128 || a->D % 8 != 0 || a->Hkv < 1 ||
       a->Hq < a->Hkv || a->Hq % a->Hkv != 0 || a->Hq / a->Hkv > 128 || a->B < 0 || a->Tq < 0 || a->Tk < 0 ||
       a->max_q < 0 || a->max_k < 0 || a->B >= top || a->Tq >= top || a->Tk >= top || a->max_q >= top ||
-      a->max_k >= top || a->max_q * a->Hq >= top || a->max_k * a->Hkv >= top || !(a->scale > -1e30 && a->scale < 1e30)) {
-    set_error(std::string(what) + ": bad arguments (bf16 or fp16, D a multiple of 8 up to 128, Hq a multiple of Hkv, max_q * Hq and max_k * Hkv below 2^31)");
+      a->max_k >= top || a->max_q * a->Hq > bound || a->max_k * a->Hkv > bound || !(a->scale > -1e30 && a->scale < 1e30)) {
+    set_error(std::string(what) + ": bad arguments (bf16 or fp16, D a multiple of 8 up to 128, Hq a multiple of Hkv, max_q * Hq and max_k * Hkv up to 2^30)");
     return RECIS_ERR_INVALID_ARG;
   }
   return RECIS_OK;
@@ -454,7 +455,7 @@ cudaError_t few_launch(const AttendParams& p, const CUtensorMap& mk, const CUten
   static std::atomic<uint64_t> done[2];
   const cudaError_t e = allow_smem(kernel, FewCfg<DP>::kTotal, done);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kernel, (unsigned)grid, kFewWarps * 32 + 32, FewCfg<DP>::kTotal, s, p, mk, mv, spin_limit());
+  return launch_pdl(kernel, (unsigned)grid, kFewWarps * 32 + 32, FewCfg<DP>::kTotal, s, p, mk, mv, kSpinLimit);
 }
 
 template <typename T>

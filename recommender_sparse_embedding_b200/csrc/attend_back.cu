@@ -165,8 +165,8 @@ __global__ void __launch_bounds__(BackCfg<DP, KEYS>::kThreads, 1)
       unsigned v[2] = {0, 0}, v_next[2] = {takes(at, 0), takes(at, 1)};
       bool last_special = false;
       next(ahead);
-      int st = 0, last_st = 0;
-      unsigned ph = 0, last_ph = 0;
+      int st = 0, last_st = 0, asked = 0;
+      unsigned ph = 0, last_ph = 0, raw = 0;  // raw: stages whose tile is a special one
       for (int j = 0; j <= n; ++j) {
         if (last_special) {
           if (!KEYS)
@@ -203,6 +203,8 @@ __global__ void __launch_bounds__(BackCfg<DP, KEYS>::kThreads, 1)
           break;
         }
         last_special = special(at);
+        raw = (raw & ~(1u << st)) | (last_special ? 1u << st : 0u);
+        asked = j + 1;
         if (elect_one()) {
           uint64_t* full = y_full + st;
           if (last_special) {
@@ -243,7 +245,9 @@ __global__ void __launch_bounds__(BackCfg<DP, KEYS>::kThreads, 1)
       if (KEYS) copy_wait_all();
       // copies in flight end before the block does
       ok = mbar_wait(x_full, 0, spin_max) && ok;
-      for (int i = 0; i < kNS && !ok; ++i) mbar_wait(y_full + i, ph, 64);  // bounded: some may never come
+      if (!ok)
+        for (int j = max(asked - kNS, 0); j < asked; ++j)
+          mbar_wait((raw >> (j % kNS) & 1 ? y_raw : y_full) + j % kNS, (j / kNS) & 1, spin_max);
     }
   } else if (w == kIssuer) {
     if (n > 0) {
@@ -499,7 +503,7 @@ cudaError_t back_launch(const AttendParams& p, const BackMaps& m, int64_t grid, 
   static std::atomic<uint64_t> done[2];
   const cudaError_t e = allow_smem(kernel, C::kTotal, done);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kernel, (unsigned)grid, C::kThreads, C::kTotal, s, p, m, spin_limit());
+  return launch_pdl(kernel, (unsigned)grid, C::kThreads, C::kTotal, s, p, m, kSpinLimit);
 }
 
 // joins the parts of grad_q

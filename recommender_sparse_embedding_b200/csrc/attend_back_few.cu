@@ -55,8 +55,8 @@ __global__ void __launch_bounds__(kThreads, FewBackCfg<DP, NR>::kTwo ? 2 : 1)
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(s_raw) + 1023) & ~(uintptr_t)1023);
   uint8_t *skv = base, *sds = skv + 2 * NS * C::kTile, *sq = sds + 2 * 16384, *so = sq + C::kRows;
   uint64_t* bar = reinterpret_cast<uint64_t*>(so + C::kRows);
-  uint64_t *q_raw = bar, *q_full = bar + 1, *s_full = bar + 2, *e_full = bar + 3, *o_full = bar + 4;
-  uint64_t *kv_full = bar + 5, *kv_empty = kv_full + NS;
+  uint64_t *q_raw = bar, *q_full = bar + 1, *s_full = bar + 2, *e_full = bar + 3, *o_full = bar + 4, *all_done = bar + 5;
+  uint64_t *kv_full = bar + 6, *kv_empty = kv_full + NS;
   float* s_lse = reinterpret_cast<float*>(so + C::kRows + 128);  // [NR] lse * log2(e)
   float* s_delta = s_lse + NR;
   __shared__ uint32_t s_tmem;
@@ -92,6 +92,7 @@ __global__ void __launch_bounds__(kThreads, FewBackCfg<DP, NR>::kTwo ? 2 : 1)
     mbar_init(s_full, 1);
     mbar_init(e_full, kCompute);
     mbar_init(o_full, 1);
+    mbar_init(all_done, 1);
     for (int i = 0; i < NS; ++i) {
       mbar_init(kv_full + i, 1);
       mbar_init(kv_empty + i, 1);
@@ -194,6 +195,8 @@ __global__ void __launch_bounds__(kThreads, FewBackCfg<DP, NR>::kTwo ? 2 : 1)
         __syncwarp();
         if (j + 1 < n) ok = scores(j + 1);
       }
+      if (one) mma_commit(all_done);
+      ok = warp_wait(all_done, 0, spin_max) && ok;
     }
     __syncwarp();
   } else {
@@ -368,7 +371,7 @@ cudaError_t few_back_launch(const AttendParams& p, const CUtensorMap (&m)[4], in
   static std::atomic<uint64_t> done[2];
   const cudaError_t e = allow_smem(kernel, C::kTotal, done);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kernel, (unsigned)grid, kThreads, C::kTotal, s, p, m[0], m[1], m[2], m[3], spin_limit());
+  return launch_pdl(kernel, (unsigned)grid, kThreads, C::kTotal, s, p, m[0], m[1], m[2], m[3], kSpinLimit);
 }
 
 }  // namespace

@@ -358,7 +358,7 @@ static cudaError_t tc_launch(const AttendParams& p, const CUtensorMap& mq, const
   const cudaError_t e =
       allow_smem(kernel, FwdSmem<DP>::kTotal, done);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kernel, (unsigned)grid, kTcThreads, FwdSmem<DP>::kTotal, s, p, mq, mk, mv, spin_limit());
+  return launch_pdl(kernel, (unsigned)grid, kTcThreads, FwdSmem<DP>::kTotal, s, p, mq, mk, mv, kSpinLimit);
 }
 
 recis_status launch_attend_tc(const AttendParams& p, bool bf16, cudaStream_t s) {

@@ -143,7 +143,7 @@ struct PassParams {
 
 template <int ITEMS>
 __device__ __forceinline__ uint2 pass_item(const PassParams& p, int64_t i, bool report) {
-  if (p.in) return __ldg(p.in + i);
+  if (p.in) return p.in[i];  // written by the kernel before: no read-only path
   return make_uint2(sort_key(__ldg(p.tok + i), p.V, p.padding, p.status, report), (uint32_t)i);
 }
 
@@ -235,8 +235,8 @@ __global__ void __launch_bounds__(kSortThreads) grad_scatter_kernel(const __grid
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
     const int b = tid * kPer + j;
-    tot[j] = b < bins ? __ldg(p.total + b) : 0;
-    pre[j] = b < bins ? __ldg(p.hist + (size_t)blockIdx.x * bins + b) : 0;
+    tot[j] = b < bins ? p.total[b] : 0;
+    pre[j] = b < bins ? p.hist[(size_t)blockIdx.x * bins + b] : 0;
     mine += tot[j];
   }
   uint32_t x = mine;
@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(256, 3) grad_span_kernel(const __grid_constant
   pdl_wait();
   for (int i = threadIdx.x; i < (p.spb + 2) * S + 2; i += blockDim.x) {
     const int64_t at = lo + i;
-    s_pair[i] = at >= 0 && at < p.N ? __ldg(p.pairs + at) : make_uint2(none, 0);
+    s_pair[i] = at >= 0 && at < p.N ? p.pairs[at] : make_uint2(none, 0);
   }
   __syncthreads();
   const int64_t span = (int64_t)blockIdx.x * p.spb + threadIdx.x / p.lanes;
