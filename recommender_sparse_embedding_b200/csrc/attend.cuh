@@ -45,6 +45,8 @@ __device__ __forceinline__ Bag load_bag(const AttendParams& p, int b) {
 
 // more rows (queries times heads of a group) than this in a bag: tensor-core tiles
 constexpr int kFewRows = 16;
+// at most this many keys in a bag: the backward takes ds as two 16-bit values
+constexpr int kSplitKeys = 128;
 // at most this many rows in a bag: the backward takes them all at once, in one pass over the keys
 constexpr int kFewBackRows = 64;
 // blocks of that pass an SM holds

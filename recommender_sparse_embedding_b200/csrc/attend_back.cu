@@ -18,6 +18,12 @@
 // (row r: query r / G, head r % G), so dK and dV sum over them in the
 // accumulator.
 //
+// Bags of few keys (SPLIT) have dS go into its products as two 16-bit values,
+// its rounding and what that leaves out (over the two halves of dP's columns):
+// there the rounding of dS and that of `out` in delta would add up to more than
+// 1.5 times the gradients' own rounding.  The more keys, the more the second
+// averages out, and one value is enough.
+//
 // Rows of a tile that belong to another bag, or to masked keys, are overwritten
 // with zeros before the products (0 * NaN is NaN) by the warp that issues the
 // copies, which waits for such a tile's data itself.
@@ -57,7 +63,7 @@ struct BackMaps {
   CUtensorMap x1, x2, y1, y2;
 };
 
-template <typename T, int DP, bool KEYS>
+template <typename T, int DP, bool KEYS, bool SPLIT>
 __global__ void __launch_bounds__(BackCfg<DP, KEYS>::kThreads, 1)
     attend_back_kernel(const __grid_constant__ AttendParams p, const __grid_constant__ BackMaps maps, int spin_max) {
   using C = BackCfg<DP, KEYS>;
@@ -293,6 +299,7 @@ __global__ void __launch_bounds__(BackCfg<DP, KEYS>::kThreads, 1)
             const uint32_t at = (k >> 1) * 32 + (k & 1) * 8;
             if (KEYS) mma_ts(tmem + C::kAcc1, e + at, b2 + (k * 2048 >> 4), id_a, j > 0 || k > 0);
             mma_ts(tmem + C::kAcc2, e + 64 + at, b1 + (k * 2048 >> 4), id_a, j > 0 || k > 0);
+            if (SPLIT) mma_ts(tmem + C::kAcc2, e + 80 + at, b1 + (k * 2048 >> 4), id_a, true);
           }
           mma_commit(y_empty + st);
         }
@@ -349,7 +356,7 @@ __global__ void __launch_bounds__(BackCfg<DP, KEYS>::kThreads, 1)
           const uint32_t(&d)[32] = sd[1][q];
           uint32_t valid = 0xffffffffu;
           if (!KEYS) valid = s_valid[st][col >> 5];
-          uint32_t pk[16], dk[16];
+          uint32_t pk[16], dk[16], dl[16];
 #pragma unroll
           for (int i = 0; i < 32; i += 4) {
             float4 ls = make_float4(lse, lse, lse, lse), de = make_float4(delta, delta, delta, delta);
@@ -376,9 +383,15 @@ __global__ void __launch_bounds__(BackCfg<DP, KEYS>::kThreads, 1)
             }
             dk[i / 2] = pack2<T>(f0.x, f0.y);
             dk[i / 2 + 1] = pack2<T>(f1.x, f1.y);
+            if (SPLIT) {
+              const float2 r0 = unpack2<T>(dk[i / 2]), r1 = unpack2<T>(dk[i / 2 + 1]);
+              dl[i / 2] = pack2<T>(f0.x - r0.x, f0.y - r0.y);
+              dl[i / 2 + 1] = pack2<T>(f1.x - r1.x, f1.y - r1.y);
+            }
           }
           if (KEYS) tmem_st16(mine + bf * 128 + col, pk);
           tmem_st16(mine + bf * 128 + 64 + col, dk);
+          if (SPLIT) tmem_st16(mine + bf * 128 + 80 + col, dl);
         }
         tmem_wait_st();
       }
@@ -496,14 +509,21 @@ __global__ void __launch_bounds__(128) join_q_kernel(const __grid_constant__ Att
       make_uint2(pack2<T>(a.x, a.y), pack2<T>(a.z, a.w));
 }
 
-template <typename T, int DP, bool KEYS>
-cudaError_t back_launch(const AttendParams& p, const BackMaps& m, int64_t grid, cudaStream_t s) {
+template <typename T, int DP, bool KEYS, bool SPLIT>
+cudaError_t back_go(const AttendParams& p, const BackMaps& m, int64_t grid, cudaStream_t s) {
   using C = BackCfg<DP, KEYS>;
-  auto kernel = attend_back_kernel<T, DP, KEYS>;
+  auto kernel = attend_back_kernel<T, DP, KEYS, SPLIT>;
   static std::atomic<uint64_t> done[2];
   const cudaError_t e = allow_smem(kernel, C::kTotal, done);
   if (e != cudaSuccess) return e;
   return launch_pdl(kernel, (unsigned)grid, C::kThreads, C::kTotal, s, p, m, kSpinLimit);
+}
+
+template <typename T, bool KEYS>
+cudaError_t back_launch(const AttendParams& p, const BackMaps& m, int64_t grid, cudaStream_t s) {
+  const bool split = p.max_k <= kSplitKeys;
+  if (p.D <= 64) return split ? back_go<T, 64, KEYS, true>(p, m, grid, s) : back_go<T, 64, KEYS, false>(p, m, grid, s);
+  return split ? back_go<T, 128, KEYS, true>(p, m, grid, s) : back_go<T, 128, KEYS, false>(p, m, grid, s);
 }
 
 // joins the parts of grad_q
@@ -561,12 +581,12 @@ recis_status back(const AttendParams& p, cudaStream_t s) {
   }
   if (kgrid > 0) {
     LaunchScope ls("attend_back_keys", s);
-    e = p.D <= 64 ? back_launch<T, 64, true>(p, mk, kgrid, s) : back_launch<T, 128, true>(p, mk, kgrid, s);
+    e = back_launch<T, true>(p, mk, kgrid, s);
     if (e != cudaSuccess) return cuda_fail(e, "attend_back_keys launch");
   }
   if (qgrid > 0) {
     LaunchScope ls("attend_back_queries", s);
-    e = p.D <= 64 ? back_launch<T, 64, false>(p, mq, qgrid, s) : back_launch<T, 128, false>(p, mq, qgrid, s);
+    e = back_launch<T, false>(p, mq, qgrid, s);
     if (e != cudaSuccess) return cuda_fail(e, "attend_back_queries launch");
   }
   return join_q<T>(p, s);

@@ -14,6 +14,12 @@
 //   dV = P^T dO, dK = dS^T Q        (128 keys x D), stored
 //   dQ += dS K                      (NR rows x D, kept in tensor memory)
 //
+// Bags of few keys (SPLIT, as in the other backward) have dS go into its products
+// as two 16-bit values, its rounding and what that leaves out: for dQ the second
+// values are rows NR .. 2 NR - 1 of the 128 that a product takes anyway, for dK a
+// product of NR more values.  (On long bags, where it is not needed, it takes 170
+// us instead of 152 for 0-16 queries over 256 bags of 1000-5000 keys.)
+//
 // While the compute warps store dV and dK of one tile, the scores of the next
 // are made; the copies run further ahead.  Parts of dQ (several blocks a bag)
 // are joined in order by join_q_kernel.
@@ -44,7 +50,7 @@ struct FewBackCfg {
   static constexpr int kTotal = 2 * kStages * kTile + 2 * 16384 + 2 * kRows + 1024 + 128 + 2 * NR * 4;
 };
 
-template <typename T, int DP, int NR>
+template <typename T, int DP, int NR, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, FewBackCfg<DP, NR>::kTwo ? 2 : 1)
     attend_back_few_kernel(const __grid_constant__ AttendParams p, const __grid_constant__ CUtensorMap mq,
                            const __grid_constant__ CUtensorMap mo, const __grid_constant__ CUtensorMap mk,
@@ -186,6 +192,9 @@ __global__ void __launch_bounds__(kThreads, FewBackCfg<DP, NR>::kTwo ? 2 : 1)
           for (int k = 0; k < NR / 16; ++k)
             mma_ts(tmem + C::kDk, tmem + C::kDp + 8 * k, tq + (k * 2048 >> 4), id_o, k > 0);
 #pragma unroll
+          for (int k = 0; SPLIT && k < NR / 16; ++k)
+            mma_ts(tmem + C::kDk, tmem + C::kDp + NR / 2 + 8 * k, tq + (k * 2048 >> 4), id_o, true);
+#pragma unroll
           for (int k = 0; k < kKeys / 16; ++k)
             mma_ss(tmem + C::kDq, dds + (((k >> 2) * 16384 + (k & 3) * 32) >> 4), tk + (k * 2048 >> 4), id_o,
                    j > 0 || k > 0);
@@ -245,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, FewBackCfg<DP, NR>::kTwo ? 2 : 1)
       ok = ok && mbar_wait(s_full, j & 1, spin_max);
       __syncwarp();
       tc_fence_after();
-      uint32_t s[H], d[H], pk[H / 2], dk[H / 2];
+      uint32_t s[H], d[H], pk[H / 2], dk[H / 2], dl[H / 2];
       tmem_ld(mine + wg * H, s);
       tmem_ld(mine + C::kDp + wg * H, d);
       tmem_wait_ld();
@@ -266,16 +275,23 @@ __global__ void __launch_bounds__(kThreads, FewBackCfg<DP, NR>::kTwo ? 2 : 1)
         f[3] = takes ? e[3] * (__uint_as_float(d[i + 3]) - de.w) : 0.f;
         pk[i / 2] = pack2<T>(e[0], e[1]);
         pk[i / 2 + 1] = pack2<T>(e[2], e[3]);
-        dk[i / 2] = pack2<T>(f[0], f[1]);
-        dk[i / 2 + 1] = pack2<T>(f[2], f[3]);
+#pragma unroll
+        for (int u = 0; u < 4; u += 2) {
+          const uint32_t hi = pack2<T>(f[u], f[u + 1]);
+          const float2 r = unpack2<T>(hi);
+          dk[(i + u) / 2] = hi;
+          if (SPLIT) dl[(i + u) / 2] = pack2<T>(f[u] - r.x, f[u + 1] - r.y);
+        }
       }
       tmem_st(mine + wg * (H / 2), pk);
       tmem_st(mine + C::kDp + wg * (H / 2), dk);
+      if (SPLIT) tmem_st(mine + C::kDp + NR / 2 + wg * (H / 2), dl);
 #pragma unroll
       for (int i = 0; i < H; ++i) {
         const int r = wg * H + i;
-        *reinterpret_cast<uint16_t*>(ds_at + r * 128 + ((chunk ^ (r & 7)) << 4)) =
-            (uint16_t)(i & 1 ? dk[i / 2] >> 16 : dk[i / 2]);
+        uint8_t* at = ds_at + r * 128 + ((chunk ^ (r & 7)) << 4);
+        *reinterpret_cast<uint16_t*>(at) = (uint16_t)(i & 1 ? dk[i / 2] >> 16 : dk[i / 2]);
+        if (SPLIT) *reinterpret_cast<uint16_t*>(at + NR * 128) = (uint16_t)(i & 1 ? dl[i / 2] >> 16 : dl[i / 2]);
       }
       if (wg == 0 && !takes)  // a row of K that another bag or a masked key holds: 0 * NaN is NaN
         for (int i = 0; i < C::kBlocks; ++i) {
@@ -329,31 +345,49 @@ __global__ void __launch_bounds__(kThreads, FewBackCfg<DP, NR>::kTwo ? 2 : 1)
         else asm volatile("bar.sync 5, 256;" ::: "memory");
       }
     }
-    // dQ: lane r of tensor memory is row r
-    const int row = tid & 127;
-    if (wg == 0 && (w & 3) * 32 < NR) {
+    // dQ: lane r of tensor memory is row r with dS rounded, lane NR + r (SPLIT)
+    // with the rest; the two are added in shared memory (K and V are done with)
+    if (wg == 0) {
+      constexpr int LD = DP + 4, kRowsOut = SPLIT ? 2 * NR : NR;
+      float* sum = reinterpret_cast<float*>(skv);
+      const int row = tid & 127;
       tc_fence_after();
-      const int64_t t = bag.q0 + row / p.G;
-      const int hq = h * p.G + row % p.G;
       const bool have = n > 0 && ok;
+      if ((w & 3) * 32 < kRowsOut) {
 #pragma unroll
-      for (int q = 0; q < DP / 32; ++q) {
-        uint32_t r[32];
-        if (have) {
-          tmem_ld(mine + C::kDq + 32 * q, r);
-          tmem_wait_ld();
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int d = 32 * q + 8 * i;
-          float f[8];
-#pragma unroll
-          for (int u = 0; u < 8; ++u) f[u] = have ? __uint_as_float(r[8 * i + u]) * p.scale : 0.f;
-          if (row < rows && d < p.D) {
-            if (p.splits == 1) store_vec(static_cast<T*>(p.gq) + t * p.gqs + hq * p.gqh + d, f);
-            else store_vec(p.po + (((int64_t)sp * p.Tq + t) * p.Hq + hq) * p.D + d, f);
+        for (int q = 0; q < DP / 32; ++q) {
+          uint32_t r[32];
+          if (have) {
+            tmem_ld(mine + C::kDq + 32 * q, r);
+            tmem_wait_ld();
           }
+#pragma unroll
+          for (int i = 0; i < 32; i += 4)
+            if (row < kRowsOut)
+              *reinterpret_cast<float4*>(sum + row * LD + 32 * q + i) =
+                  have ? make_float4(__uint_as_float(r[i]), __uint_as_float(r[i + 1]), __uint_as_float(r[i + 2]),
+                                     __uint_as_float(r[i + 3]))
+                       : make_float4(0.f, 0.f, 0.f, 0.f);
         }
+      }
+      asm volatile("bar.sync 6, 128;" ::: "memory");
+      const int per = p.D / 8;
+      for (int i = row; i < rows * per; i += 128) {
+        const int r = i / per, d = (i - r * per) * 8;
+        RawVec<float, 8> x;
+        x.load(sum + r * LD + d);
+        float f[8], e[8] = {};
+        x.unpack(f);
+        if (SPLIT) {
+          x.load(sum + (r + NR) * LD + d);
+          x.unpack(e);
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) f[u] = (f[u] + e[u]) * p.scale;
+        const int64_t t = bag.q0 + r / p.G;
+        const int hq = h * p.G + r % p.G;
+        if (p.splits == 1) store_vec(static_cast<T*>(p.gq) + t * p.gqs + hq * p.gqh + d, f);
+        else store_vec(p.po + (((int64_t)sp * p.Tq + t) * p.Hq + hq) * p.D + d, f);
       }
     }
   }
@@ -364,14 +398,20 @@ __global__ void __launch_bounds__(kThreads, FewBackCfg<DP, NR>::kTwo ? 2 : 1)
   if (w == kIssuer) tmem_free(tmem, C::kCols);
 }
 
-template <typename T, int DP, int NR>
-cudaError_t few_back_launch(const AttendParams& p, const CUtensorMap (&m)[4], int64_t grid, cudaStream_t s) {
+template <typename T, int DP, int NR, bool SPLIT>
+cudaError_t few_back_go(const AttendParams& p, const CUtensorMap (&m)[4], int64_t grid, cudaStream_t s) {
   using C = FewBackCfg<DP, NR>;
-  auto kernel = attend_back_few_kernel<T, DP, NR>;
+  auto kernel = attend_back_few_kernel<T, DP, NR, SPLIT>;
   static std::atomic<uint64_t> done[2];
   const cudaError_t e = allow_smem(kernel, C::kTotal, done);
   if (e != cudaSuccess) return e;
   return launch_pdl(kernel, (unsigned)grid, kThreads, C::kTotal, s, p, m[0], m[1], m[2], m[3], kSpinLimit);
+}
+
+template <typename T, int DP, int NR>
+cudaError_t few_back_launch(const AttendParams& p, const CUtensorMap (&m)[4], int64_t grid, cudaStream_t s) {
+  return p.max_k <= kSplitKeys ? few_back_go<T, DP, NR, true>(p, m, grid, s)
+                               : few_back_go<T, DP, NR, false>(p, m, grid, s);
 }
 
 }  // namespace
