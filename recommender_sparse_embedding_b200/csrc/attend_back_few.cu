@@ -345,15 +345,35 @@ __global__ void __launch_bounds__(kThreads, FewBackCfg<DP, NR>::kTwo ? 2 : 1)
         else asm volatile("bar.sync 5, 256;" ::: "memory");
       }
     }
-    // dQ: lane r of tensor memory is row r with dS rounded, lane NR + r (SPLIT)
-    // with the rest; the two are added in shared memory (K and V are done with)
+    // dQ: lane r of tensor memory is row r with dS rounded; lane NR + r (SPLIT) is
+    // the same row with the rest, and is added through shared memory (K and V are
+    // done with)
     if (wg == 0) {
-      constexpr int LD = DP + 4, kRowsOut = SPLIT ? 2 * NR : NR;
-      float* sum = reinterpret_cast<float*>(skv);
+      constexpr int LD = DP + 4;
+      float* rest = reinterpret_cast<float*>(skv);
       const int row = tid & 127;
-      tc_fence_after();
       const bool have = n > 0 && ok;
-      if ((w & 3) * 32 < kRowsOut) {
+      tc_fence_after();
+      if (SPLIT) {
+        if (have && (w & 3) * 32 < 2 * NR) {
+#pragma unroll
+          for (int q = 0; q < DP / 32; ++q) {
+            uint32_t r[32];
+            tmem_ld(mine + C::kDq + 32 * q, r);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+              if (row >= NR && row < 2 * NR)
+                *reinterpret_cast<float4*>(rest + (row - NR) * LD + 32 * q + i) =
+                    make_float4(__uint_as_float(r[i]), __uint_as_float(r[i + 1]), __uint_as_float(r[i + 2]),
+                                __uint_as_float(r[i + 3]));
+          }
+        }
+        asm volatile("bar.sync 6, 128;" ::: "memory");
+      }
+      if ((w & 3) * 32 < NR) {
+        const int64_t t = bag.q0 + row / p.G;
+        const int hq = h * p.G + row % p.G;
 #pragma unroll
         for (int q = 0; q < DP / 32; ++q) {
           uint32_t r[32];
@@ -362,32 +382,22 @@ __global__ void __launch_bounds__(kThreads, FewBackCfg<DP, NR>::kTwo ? 2 : 1)
             tmem_wait_ld();
           }
 #pragma unroll
-          for (int i = 0; i < 32; i += 4)
-            if (row < kRowsOut)
-              *reinterpret_cast<float4*>(sum + row * LD + 32 * q + i) =
-                  have ? make_float4(__uint_as_float(r[i]), __uint_as_float(r[i + 1]), __uint_as_float(r[i + 2]),
-                                     __uint_as_float(r[i + 3]))
-                       : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-      }
-      asm volatile("bar.sync 6, 128;" ::: "memory");
-      const int per = p.D / 8;
-      for (int i = row; i < rows * per; i += 128) {
-        const int r = i / per, d = (i - r * per) * 8;
-        RawVec<float, 8> x;
-        x.load(sum + r * LD + d);
-        float f[8], e[8] = {};
-        x.unpack(f);
-        if (SPLIT) {
-          x.load(sum + (r + NR) * LD + d);
-          x.unpack(e);
-        }
+          for (int i = 0; i < 4; ++i) {
+            const int d = 32 * q + 8 * i;
+            float f[8], e[8] = {};
+            if (SPLIT && have && row < NR) {
+              RawVec<float, 8> x;
+              x.load(rest + row * LD + d);
+              x.unpack(e);
+            }
 #pragma unroll
-        for (int u = 0; u < 8; ++u) f[u] = (f[u] + e[u]) * p.scale;
-        const int64_t t = bag.q0 + r / p.G;
-        const int hq = h * p.G + r % p.G;
-        if (p.splits == 1) store_vec(static_cast<T*>(p.gq) + t * p.gqs + hq * p.gqh + d, f);
-        else store_vec(p.po + (((int64_t)sp * p.Tq + t) * p.Hq + hq) * p.D + d, f);
+            for (int u = 0; u < 8; ++u) f[u] = have ? (__uint_as_float(r[8 * i + u]) + e[u]) * p.scale : 0.f;
+            if (row < rows && d < p.D) {
+              if (p.splits == 1) store_vec(static_cast<T*>(p.gq) + t * p.gqs + hq * p.gqh + d, f);
+              else store_vec(p.po + (((int64_t)sp * p.Tq + t) * p.Hq + hq) * p.D + d, f);
+            }
+          }
+        }
       }
     }
   }
