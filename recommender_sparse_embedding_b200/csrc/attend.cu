@@ -7,6 +7,10 @@
 // The query heads that share a key head are rows of one matrix: row r of key
 // head h is query r / G, head h G + r % G, so K and V are read once for all of
 // them.
+//
+// Measured on B200: one query over 256 bags of 1000-5000 keys, 8 heads of 128 over
+// 2, 140 us with the join (5.4 TB/s, 0.87 of its floor); up to 16 queries, 2 heads of
+// 64, 83 us (4.6 TB/s).
 #include <algorithm>
 #include <type_traits>
 

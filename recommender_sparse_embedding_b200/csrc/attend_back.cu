@@ -18,6 +18,12 @@
 // (row r: query r / G, head r % G), so dK and dV sum over them in the
 // accumulator.
 //
+// Measured on B200, bf16: 4 bags of 4096 queries over 4096 keys, 8 heads of 128, 771
+// us, 891 TFLOP/s counted as 5 products (keys 409 us, queries 346); heads of 64, 544
+// us, 632.  A step of 64 rows takes 1750 cycles over keys, 1400 over queries; its
+// products take 1294 and 1038 (64 columns a product from shared memory take 49
+// cycles instead of 32), issuing them and their waits and commits about 1400.
+//
 // Bags of few keys (SPLIT) have dS go into its products as two 16-bit values,
 // its rounding and what that leaves out (over the two halves of dP's columns):
 // there the rounding of dS and that of `out` in delta would add up to more than

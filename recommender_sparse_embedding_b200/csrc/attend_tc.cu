@@ -15,6 +15,12 @@
 // time (P then stays below 2^8 and sums stay fp32), which after the first
 // steps is rare.
 //
+// Measured on B200, bf16: 4 bags of 4096 queries over 4096 keys, 8 heads of 128,
+// 249 us, 1105 TFLOP/s (0.66 of the measured matrix peak); heads of 64, 202 us, 680
+// TFLOP/s.  Products and exponentials each fill about half of the time (1024
+// cycles a tile each); what is left is the chain scores - softmax - values, which
+// two blocks an SM overlap only in part.
+//
 // A copy brings whole tiles of 128 rows, so the last one of a bag holds rows of
 // the next bag.  Their scores are replaced by -inf, and their V rows (like
 // those of masked keys) are overwritten with zeros before the product, because

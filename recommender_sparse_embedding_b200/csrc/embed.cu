@@ -14,6 +14,11 @@
 // fp32, and goes on into the next span to finish a run that ends there.  A
 // longer run (a hot token) leaves one fp32 partial per span, and a second
 // kernel adds those in span order in fp64: no float atomic is used.
+//
+// Measured on B200 (L2 flushed): 1.5M tokens over 1M rows of 128, fp32 weight to
+// bf16 rows, 129 us, 5.1 TB/s of DRAM traffic; their gradient (bf16 to fp32, dW
+// of 512 MB) 283 us, of which the spans 135 us at 4.3 TB/s, the sort about 95 us
+// beside 77 us worth of zeros that hide a quarter of it, the join 22 us.
 #include <algorithm>
 
 #include "seqops.cuh"
@@ -24,7 +29,9 @@ namespace {
 
 __device__ int g_seq_status;
 
-constexpr int kSmallN = 1024;     // up to here one kernel finds and sums each token's rows
+// up to here one kernel finds and sums each token's rows (1000 tokens over 1000
+// rows of 64: 9.5 us, 19.7 by sorting)
+constexpr int kSmallN = 1024;
 constexpr int kSortThreads = 256;
 constexpr int kMaxDigit = 10;     // bits a pass sorts by
 constexpr int kMaxSpan = 64;      // sorted positions a group of lanes walks: 16, 32 or 64
@@ -92,7 +99,8 @@ cudaError_t lookup_launch(LookupParams p, cudaStream_t s) {
   p.units = p.D / VEC;
   p.lanes = 1;
   while (p.lanes < p.units && p.lanes < 256) p.lanes *= 2;
-  // four rows a group once that still fills the machine; one row each below
+  // four rows a group once that still fills the machine, one row each below
+  // (1.5M rows of 128: 122 and 134 us; 64 rows of 1024: 2.9 and 2.5)
   const bool many = p.N / 4 * p.lanes >= (int64_t)kSMs * 1024;
   const int64_t groups = many ? (p.N + 3) / 4 : p.N;
   const int64_t blocks = std::min<int64_t>((groups * p.lanes + 255) / 256, kSMs * (many ? 4 : 6));
@@ -420,7 +428,8 @@ __global__ void __launch_bounds__(256, 3) grad_span_kernel(const __grid_constant
 // Adds the parts of the listed runs: a block takes a run, `256 / lanes` strided
 // groups of lanes add its spans' parts in fp64, eight loads in flight, then the
 // groups' sums are added in a fixed order.  The list's order, the only thing that
-// scheduling decides, does not enter the sums.
+// scheduling decides, does not enter the sums.  (Few parts a run, many runs: with
+// 512 threads a block it takes 29 us instead of 23 on 1.5M tokens.)
 constexpr int kJoinThreads = 256;
 template <typename TO, int VEC>
 __global__ void __launch_bounds__(kJoinThreads) grad_join_kernel(const __grid_constant__ SumParams p) {
@@ -560,13 +569,14 @@ GradPlan grad_plan(int64_t N, int64_t V, int D) {
   int bits = 1;
   while (((int64_t)1 << bits) <= V) ++bits;  // keys 0 .. V
   // a pass costs a block its bins as well as its keys: digits of at most 8 bits
-  // where there are keys for many blocks (1.5M tokens of 20 bits: see sort
-  // times in the header), of 10 where launches are what counts
+  // where there are keys for many blocks, of 10 where launches are what counts
+  // (1.5M tokens of 20 bits: 283 us with digits of 8, 293 of 10; 65536 of 18
+  // bits: 98 and 93)
   const int most = N >= 400000 ? 8 : kMaxDigit;
   g.passes = (bits + most - 1) / most;
   g.bits = (bits + g.passes - 1) / g.passes;
   if (g.bits < 5) g.bits = 5;  // the scan takes 32 bins at a time
-  // 8 keys a thread once there are tiles for every SM, 4 below
+  // 8 keys a thread once there are tiles for every SM, 4 below (1.5M tokens: 283 and 305 us)
   g.items = N >= (int64_t)kSMs * kSortThreads * 8 ? 8 : 4;
   const int64_t tile = (int64_t)kSortThreads * g.items;
   g.tiles = (int)((N + tile - 1) / tile);
@@ -574,7 +584,8 @@ GradPlan grad_plan(int64_t N, int64_t V, int D) {
   g.hist_bytes = align256(((int64_t)g.tiles << g.bits) * 4);
   g.total_bytes = align256(((int64_t)1 << g.bits) * 4 + 4);  // and the number of listed runs
   // long spans leave fewer parts, short ones make enough groups to fill the
-  // machine (a group takes 8 columns a lane)
+  // machine, 8 columns a lane (30000 tokens over rows of 128: 33 us with spans of
+  // 16, 51 of 64)
   g.span = kMaxSpan;
   while (g.span > 16 && N / g.span * ((D + 7) / 8) < (int64_t)kSMs * 2048) g.span /= 2;
   const int64_t spans = (N + g.span - 1) / g.span;
