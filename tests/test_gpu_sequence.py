@@ -126,9 +126,20 @@ def test_embed_grad_accumulates(R, N, dt):
     S.close(out, want, 132 * S.F32 * (mag + old.double().abs()) + S.half_step(dt) * 1.01 * want.abs(), "accumulated")
 
 
+@pytest.mark.parametrize("N", [700, 5000])
+def test_embed_grad_does_not_read_padding_rows(R, N):
+    g = _gen(N + 1)
+    t = _tokens("hot", N, 60, g)
+    grad = _randn((N, 32), BF16, g)
+    want = R.embed_grad(t, grad, 60)
+    grad[t == -1] = math.nan
+    assert (t == -1).any() and torch.equal(R.embed_grad(t, grad, 60), want)
+
+
 # ------------------------------------------------------------------ layer norm
 NORM_SIZES = [(1, 1), (5, 7), (64, 256), (1000, 8), (257, 40), (33, 128), (300, 1001), (70, 4096), (9, 8192),
-              (5, 16384), (3, 5003), (4, 40000), (20000, 16), (2, 512), (40, 520)]
+              (5, 16384), (3, 5003), (4, 40000), (20000, 16), (2, 512), (40, 520), (2500, 2048), (1700, 8192),
+              (3001, 300)]
 
 
 @pytest.mark.parametrize("xt,yt,wt", [(F32, F32, F32), (F32, BF16, F32), (BF16, BF16, BF16), (F16, F16, F32),
@@ -213,6 +224,10 @@ ATTEND = [
     (1, (2, 2), (9000, 9000), 2, 1, 128, 0.0),
     (2, (3, 9), (60, 70), 130, 2, 16, 0.0),
     (6, (1, 200), (0, 500), 1, 1, 40, 1.0),
+    (4, (70, 150), (0, 100), 2, 2, 64, 0.0),    # few keys, many rows
+    (3, (100, 300), (1, 128), 6, 3, 128, 0.2),
+    (5, (3, 40), (0, 90), 1, 1, 128, 0.1),      # few keys, few rows
+    (9, (30, 64), (200, 260), 1, 1, 48, 0.0),
 ]
 
 
@@ -311,6 +326,20 @@ def test_attend_offsets_past_32_bits(R):
     S.close(gk[0, -n:], *small["grad_k"], "grad_k")
     S.close(gk[1, -n:], *small["grad_v"], "grad_v")
     assert not gk[:, : Tk - n].any()  # keys of a bag without queries
+
+
+def test_attend_reads_rows_in_any_order_of_strides(R):
+    """Keys that share memory between heads' rows (a window over one buffer)."""
+    g = _gen(11)
+    buf = _randn((300 + 16, 32), F16, g)
+    k = buf.as_strided((300, 2, 32), (32, 256, 1))  # head 1 is head 0, 8 rows on
+    q = _randn((20, 2, 32), F16, g)
+    qo, ko = _offsets([20]), _offsets([300])
+    out, lse = R.attend(q, k, k, qo, ko, 20, 300)
+    same, lse2 = R.attend(q, k.contiguous(), k.contiguous(), qo, ko, 20, 300)
+    assert torch.equal(out, same) and torch.equal(lse, lse2)
+    with pytest.raises(ValueError):  # but gradients need memory of their own
+        R.attend_backward(out, q, k, k, out, lse, qo, ko, 20, 300, grad_k=buf.as_strided((300, 2, 32), (32, 256, 1)))
 
 
 def test_attend_bad_offsets_are_reported(R):

@@ -180,3 +180,18 @@ def test_sequence_attention_refuses_rows_that_do_not_fit(R):
     assert R.SequenceAttention(T(), torch.zeros(5, 64), 4, 2, w, w).head_dim == 16
     with pytest.raises(RuntimeError):
         R.SequenceAttention(T(), torch.zeros(5, 64), 4, 2, w, w).backward(w)
+
+
+def test_rows_of_views():
+    from recommender_sparse_embedding_b200.sequence import _rows
+    x = torch.zeros(4, 6, 10)
+    assert _rows(x, "x") == (24, 10, 10)
+    assert _rows(x[:, :, 2:7], "x") == (24, 5, 10)
+    assert _rows(x[:, 1], "x") == (4, 10, 60)
+    assert _rows(x[1:2, 3:4, :4], "x") == (1, 4, 4)
+    assert _rows(x[:0], "x")[0] == 0
+    for bad in (x[:, :3], x.transpose(0, 1), x[:, :, ::2], x[:, :, :1].expand(4, 6, 3), x[:1].expand(3, 6, 10)):
+        with pytest.raises(ValueError):
+            _rows(bad, "x")
+    with pytest.raises(ValueError):
+        _rows(x, "x", 9)
