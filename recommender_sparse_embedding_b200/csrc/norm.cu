@@ -13,10 +13,10 @@
 // the blocks' sums in block order in fp64 (no float atomic).
 //
 // Measured on B200 (L2 flushed): 1.5M rows of 128, fp32 to bf16, forward 187 us
-// (6.2 TB/s), backward 308 us (6.2 TB/s); 16384 rows of 4096 bf16, forward 80 us
-// (3.4 TB/s, bound by the latency of a row's two sums at 32 warps an SM),
-// backward 94 us (4.3 TB/s, by instructions: two sums a column kept in registers
-// leave 16 warps an SM).
+// (6.2 TB/s), backward 308 us (6.2 TB/s); 16384 rows of 4096 bf16, forward 65 us
+// (4.1 TB/s, bound by instructions: a value is unpacked three times), backward 94
+// us (4.3 TB/s, by instructions: two sums a column kept in registers leave 16 warps
+// an SM).
 #include <algorithm>
 #include <atomic>
 
@@ -275,6 +275,63 @@ __global__ void __launch_bounds__(kMaxRowThreads, UPT * VEC <= 16 ? 2 : 1) norm_
   }
 }
 
+// Rows of several vectors a lane, a warp a row: the row stays in registers as it
+// lies in memory (UPT x 8 values a lane) and is unpacked anew for the mean, the
+// squares and the output, so a row needs no barrier, and ten shuffles in all.
+template <typename TX, typename TY, int UPT>
+__global__ void __launch_bounds__(256, 2) norm_row_kernel(const __grid_constant__ NormParams p) {
+  extern __shared__ __align__(16) float s_dyn[];
+  const int lane = threadIdx.x & 31;
+  Params<8, UPT, 2> par;
+  par.init(p, s_dyn, lane);
+  const float inv = 1.0f / (float)p.D;
+  auto mine = [&](int k) { return lane + k * 32 < p.units; };
+  auto warp_sum = [](float v) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    return v;
+  };
+  for (int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); i < p.M; i += (int64_t)gridDim.x * 8) {
+    const TX* x = static_cast<const TX*>(p.x) + i * p.x_stride + lane * 8;
+    TY* y = static_cast<TY*>(p.y) + i * p.y_stride + lane * 8;
+    RawVec<TX, 8> raw[UPT];
+#pragma unroll
+    for (int k = 0; k < UPT; ++k)
+      if (mine(k)) raw[k].load(x + k * 256);
+    float s = 0.f, v[8];
+#pragma unroll
+    for (int k = 0; k < UPT; ++k)
+      if (mine(k)) {
+        raw[k].unpack(v);
+        s += vec_sum(v);
+      }
+    const float mu = warp_sum(s) * inv;
+    s = 0.f;
+#pragma unroll
+    for (int k = 0; k < UPT; ++k)
+      if (mine(k)) {
+        raw[k].unpack(v);
+        s += vec_center(v, mu);
+      }
+    const float r = inv_sqrt(fmaf(warp_sum(s), inv, p.eps));
+    if (lane == 0) {
+      if (p.mean) p.mean[i] = mu;
+      if (p.rstd) p.rstd[i] = r;
+    }
+#pragma unroll
+    for (int k = 0; k < UPT; ++k)
+      if (mine(k)) {
+        float w[8], b[8];
+        par.get(0, k, lane + k * 32, p.D, w);
+        par.get(1, k, lane + k * 32, p.D, b);
+        raw[k].unpack(v);
+        vec_center(v, mu);
+        vec_affine(v, r, w, b);
+        store_vec(y + k * 256, v);
+      }
+  }
+}
+
 // Rows wider than the registers of a block hold: three reads of the row.
 template <typename TX, typename TY>
 __global__ void __launch_bounds__(kWideThreads) norm_wide_kernel(const __grid_constant__ NormParams p) {
@@ -513,14 +570,35 @@ cudaError_t norm_go(const NormParams& p, cudaStream_t s) {
   return cudaGetLastError();
 }
 
+template <typename TX, typename TY, int UPT>
+cudaError_t norm_row_go(const NormParams& p, cudaStream_t s) {
+  static std::atomic<int> cache[16];
+  auto kernel = norm_row_kernel<TX, TY, UPT>;
+  const size_t smem = (size_t)p.D * 8;  // at most 32 KB
+  const int grid = (int)std::min<int64_t>((p.M + 7) / 8, resident_blocks(kernel, 256, smem, cache));
+  kernel<<<grid, 256, smem, s>>>(p);
+  return cudaGetLastError();
+}
+
 template <typename TX, typename TY, int VEC>
 cudaError_t norm_launch(NormParams p, cudaStream_t s) {
   p.units = p.D / VEC;
   LaunchScope ls("layer_norm", s);
-  // A warp a row, up to two vectors a thread (single columns: 8), then more
-  // threads.  More columns a thread share the sums' shuffles and barriers, fewer
-  // leave registers for more rows an SM: 16384 x 4096 bf16 takes 89 us at 8
-  // columns (issue), 97 at 32 (latency at 16 warps an SM).
+  // A warp a row while it holds in 64 registers a lane and there are rows for every
+  // SM (bf16, with a block's threads a row instead: 16384 x 4096 65 and 82 us, 65536
+  // x 1024 55 and 65, 1200 x 2048 16 and 23).
+  if constexpr (VEC == 8) {
+    constexpr int most = sizeof(TX) == 2 ? 16 : 8;
+    if (p.units > 64 && p.units <= 32 * most && p.M >= kSMs * 8) {
+      if (p.units <= 128) return norm_row_go<TX, TY, 4>(p, s);
+      if (p.units <= 256) return norm_row_go<TX, TY, 8>(p, s);
+      return norm_row_go<TX, TY, most>(p, s);
+    }
+  }
+  // Else up to two vectors a thread (single columns: 8), then more threads.  More
+  // columns a thread share the sums' shuffles and barriers, fewer leave registers
+  // for more rows an SM: 16384 x 4096 bf16 takes 89 us at 8 columns (issue), 82 at
+  // 16, 97 at 32 (latency at 16 warps an SM).
   int upt = p.units <= 32 ? 1 : 2;
   if (VEC == 1 && p.units > 64) upt = 8;
   p.tpr = row_threads(p.units, upt);

@@ -139,7 +139,7 @@ def test_embed_grad_does_not_read_padding_rows(R, N):
 # ------------------------------------------------------------------ layer norm
 NORM_SIZES = [(1, 1), (5, 7), (64, 256), (1000, 8), (257, 40), (33, 128), (300, 1001), (70, 4096), (9, 8192),
               (5, 16384), (3, 5003), (4, 40000), (20000, 16), (2, 512), (40, 520), (2500, 2048), (1700, 8192),
-              (3001, 300)]
+              (3001, 300), (1300, 1000), (1250, 4096), (1210, 2600)]
 
 
 @pytest.mark.parametrize("xt,yt,wt", [(F32, F32, F32), (F32, BF16, F32), (BF16, BF16, BF16), (F16, F16, F32),
