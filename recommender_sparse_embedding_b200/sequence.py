@@ -6,9 +6,10 @@ As in recis.py, this is argument marshalling: the arithmetic runs in the CUDA
 library, forward and backward are separate calls, and there is no CPU fallback.
 Calls are asynchronous on `stream` (the current stream of the tensors' device
 by default); outputs and scratch are allocated by torch for that stream, so the
-calls may be captured into CUDA graphs (after a first call on the device).  Inputs used on another stream than the
-one they were made on are the caller's to order.  Errors found on the device (a
-token out of range, malformed offsets) are raised by sequence_status_sync.
+calls may be captured into CUDA graphs (after a first call on the device).
+Inputs used on another stream than the one they were made on are the caller's to
+order.  Errors found on the device (a token out of range, malformed offsets) are
+raised by sequence_status_sync.
 """
 from __future__ import annotations
 
