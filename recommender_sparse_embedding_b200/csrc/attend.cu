@@ -354,16 +354,27 @@ struct AttendPlan {
   int64_t bytes;
 };
 
+// The call with bounds of 0 raised to 1: the blocks that look at every bag's
+// offsets run all the same.  The checks, the plan and the launches all take
+// their sizes from this, so that a launch never needs more than its plan gave.
+recis_attend_args launch_sizes(const recis_attend_args& a) {
+  recis_attend_args c = a;
+  if (c.max_q == 0) c.max_q = 1;
+  if (c.max_k == 0) c.max_k = 1;
+  return c;
+}
+
+// a: of launch_sizes
 AttendPlan attend_plan(const recis_attend_args& a, bool backward) {
   AttendPlan g = {};
   g.splits = 1;
-  g.split_keys = (int)std::max<int64_t>(a.max_k, 1);
+  g.split_keys = (int)a.max_k;
   if (backward) {
     // parts of the keys for grad_q.  Few rows: the keys' pass makes it, three
     // rounds of blocks on every SM even out the bags' lengths; many: a pass
     // over query tiles of its own, two blocks an SM.  At least 512 keys a part.
     const int64_t G = a.Hq / a.Hkv, rows = a.max_q * G;
-    const bool few = rows <= kFewBackRows;
+    const bool few = few_back_rows(a.max_q, G);
     if (!few) g.delta_bytes = 2 * align256(a.Tq * a.Hq * 4);
     const int64_t blocks = std::max<int64_t>(1, a.B * a.Hkv * (few ? 1 : (a.max_q + 128 / G - 1) / (128 / G)));
     const int64_t target = kSMs * (few ? 3 * few_back_per_sm(a.D, rows) : 2);
@@ -377,7 +388,7 @@ AttendPlan attend_plan(const recis_attend_args& a, bool backward) {
     // parts of the keys: enough blocks for every SM to hold a few, each part
     // at least 256 keys (few rows: 16 iterations a warp) or 512 (tiles: 4 steps)
     const int64_t G = a.Hq / a.Hkv;
-    const bool few = a.max_q * G <= kFewRows;
+    const bool few = few_rows(a.max_q, G);
     const int64_t tile = few ? std::max<int64_t>(kRowTile / G, 1) : 128 / G;  // queries a block
     const int64_t blocks = std::max<int64_t>(1, a.B * a.Hkv * ((a.max_q + tile - 1) / tile));
     const int64_t least = few ? 256 : 512;
@@ -398,7 +409,7 @@ AttendPlan attend_plan(const recis_attend_args& a, bool backward) {
 recis_status check_sizes(const recis_attend_args* a, const char* what) {
   // room below 2^31 for coordinates and counts rounded up to tiles
   const int64_t top = INT32_MAX - 65536, bound = (int64_t)1 << 30;
-  if (!a || (a->type != RECIS_BF16 && a->type != RECIS_F16) || a->D < 8 || a->D > 128 || a->D % 8 != 0 || a->Hkv < 1 ||
+  if ((a->type != RECIS_BF16 && a->type != RECIS_F16) || a->D < 8 || a->D > 128 || a->D % 8 != 0 || a->Hkv < 1 ||
       a->Hq < a->Hkv || a->Hq % a->Hkv != 0 || a->Hq / a->Hkv > 128 || a->B < 0 || a->Tq < 0 || a->Tk < 0 ||
       a->max_q < 0 || a->max_k < 0 || a->B >= top || a->Tq >= top || a->Tk >= top || a->max_q >= top ||
       a->max_k >= top || a->max_q * a->Hq > bound || a->max_k * a->Hkv > bound || !(a->scale > -1e30 && a->scale < 1e30)) {
@@ -435,8 +446,7 @@ recis_status fill(const recis_attend_args* a, AttendParams* p, const AttendPlan&
   p->gvs = a->grad_v_stride; p->gvh = a->grad_v_head_stride;
   p->Tq = a->Tq; p->Tk = a->Tk;
   p->B = (int)a->B; p->Hq = a->Hq; p->Hkv = a->Hkv; p->G = a->Hq / a->Hkv; p->D = a->D;
-  // a bound of 0 still launches the blocks that look at every bag's offsets
-  p->max_q = (int)std::max<int64_t>(a->max_q, 1); p->max_k = (int)std::max<int64_t>(a->max_k, 1);
+  p->max_q = (int)a->max_q; p->max_k = (int)a->max_k;
   p->scale = (float)a->scale;
   p->scale_log2 = (float)(a->scale * 1.4426950408889634);
   // a scale of 0 makes every score 0; 1e-30 does too, and keeps the -inf of keys that take no part
@@ -464,7 +474,7 @@ cudaError_t few_launch(const AttendParams& p, const CUtensorMap& mk, const CUten
 
 template <typename T>
 recis_status forward(const AttendParams& p, cudaStream_t s) {
-  const bool few = p.max_q * p.G <= kFewRows;
+  const bool few = few_rows(p.max_q, p.G);
   const int64_t rtiles = ((int64_t)p.max_q * p.G + kRowTile - 1) / kRowTile;
   const int64_t grid = (int64_t)p.B * p.splits * p.Hkv * rtiles, jgrid = (int64_t)p.B * (((int64_t)p.max_q * p.Hq + 3) / 4);
   if ((few && !grid_fits(grid)) || !grid_fits(jgrid)) {
@@ -500,7 +510,11 @@ recis_status forward(const AttendParams& p, cudaStream_t s) {
 
 using namespace recis;
 
-extern "C" recis_status recis_attend_workspace(const recis_attend_args* a, int32_t backward, int64_t* bytes_out) {
+// null pointers are refused with the sizes
+static recis_attend_args sizes_of(const recis_attend_args* a) { return a ? launch_sizes(*a) : recis_attend_args{}; }
+
+extern "C" recis_status recis_attend_workspace(const recis_attend_args* args, int32_t backward, int64_t* bytes_out) {
+  const recis_attend_args c = sizes_of(args), *a = &c;
   recis_status st = check_sizes(a, "attend_workspace");
   if (st != RECIS_OK) return st;
   if (!bytes_out) {
@@ -536,8 +550,9 @@ static recis_status check_call(const recis_attend_args* a, bool backward, void* 
   return RECIS_OK;
 }
 
-extern "C" recis_status recis_attend(const recis_attend_args* a, void* workspace, int64_t workspace_bytes,
+extern "C" recis_status recis_attend(const recis_attend_args* args, void* workspace, int64_t workspace_bytes,
                                      recis_stream_t stream) {
+  const recis_attend_args c = sizes_of(args), *a = &c;
   recis_status st = check_call(a, false, workspace, workspace_bytes, "attend");
   if (st != RECIS_OK) return st;
   if (a->B == 0 || a->Tq == 0) return RECIS_OK;
@@ -547,8 +562,9 @@ extern "C" recis_status recis_attend(const recis_attend_args* a, void* workspace
                                : forward<__half>(p, (cudaStream_t)stream);
 }
 
-extern "C" recis_status recis_attend_backward(const recis_attend_args* a, void* workspace, int64_t workspace_bytes,
+extern "C" recis_status recis_attend_backward(const recis_attend_args* args, void* workspace, int64_t workspace_bytes,
                                               recis_stream_t stream) {
+  const recis_attend_args c = sizes_of(args), *a = &c;
   recis_status st = check_call(a, true, workspace, workspace_bytes, "attend_backward");
   if (st != RECIS_OK) return st;
   if (a->B == 0) return RECIS_OK;

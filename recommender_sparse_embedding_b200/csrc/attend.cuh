@@ -48,6 +48,7 @@ __device__ __forceinline__ Bag load_bag(const AttendParams& p, int b) {
 // without them, 65 with; at 32 rows 73 and 64; 256 bags of up to 16 rows of 64: 83
 // and 112).
 constexpr int kFewRows = 16;
+inline bool few_rows(int64_t max_q, int64_t G) { return max_q * G <= kFewRows; }
 // At most this many keys in a bag: the backward takes ds as two 16-bit values.
 // (The gradients of q and k are then within 1.4 times their own rounding of 64
 // bits, at 8 keys as at 128; with one value they are at 1.7 times at 8 keys and
@@ -57,6 +58,7 @@ constexpr int kSplitKeys = 128;
 // pass over the keys (64 bags of 1000-5000 keys, 64 rows, 2 heads of 128: 140 us,
 // 213 in two passes; 256 bags of up to 16 rows, 2 heads of 64: 161 and 609).
 constexpr int kFewBackRows = 64;
+inline bool few_back_rows(int64_t max_q, int64_t G) { return max_q * G <= kFewBackRows; }
 // blocks of that pass an SM holds
 inline int few_back_per_sm(int D, int64_t rows) { return D <= 64 && rows <= 32 ? 2 : 1; }
 recis_status launch_attend_back_few(const AttendParams& p, bool bf16, cudaStream_t s);

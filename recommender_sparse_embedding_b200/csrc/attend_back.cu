@@ -549,7 +549,7 @@ recis_status join_q(const AttendParams& p, cudaStream_t s) {
 template <typename T>
 recis_status back(const AttendParams& p, cudaStream_t s) {
   constexpr bool bf16 = std::is_same<T, __nv_bfloat16>::value;
-  if (p.max_q * p.G <= kFewBackRows) {
+  if (few_back_rows(p.max_q, p.G)) {
     const recis_status st = launch_attend_back_few(p, bf16, s);
     return st == RECIS_OK ? join_q<T>(p, s) : st;
   }

@@ -372,6 +372,23 @@ def test_attend_empty_calls(R):
     assert not gk.any() and not gv.any()
 
 
+@pytest.mark.parametrize("Hq,Hkv", [(2, 2), (17, 1), (128, 1), (260, 2)])
+def test_attend_rows_of_no_bag_with_a_bound_of_zero(R, Hq, Hkv):
+    """max_q 0: no bag has queries, q's rows belong to none; keys get zeros."""
+    g = _gen(Hq)
+    D = 16
+    q, k = _randn((3, Hq, D), BF16, g), _randn((700, Hkv, D), BF16, g)
+    qo, ko = torch.zeros(3, dtype=torch.int64, device="cuda"), _offsets([650, 30])
+    out, lse = torch.full_like(q, 7.0), torch.full((3, Hq), 7.0, device="cuda")
+    R.attend(q, k, k, qo, ko, 0, 650, out=out, lse=lse)
+    gq, gk, gv = torch.full_like(q, 7.0), torch.full_like(k, 7.0), torch.full_like(k, 7.0)
+    R.attend_backward(q, q, k, k, out, lse, qo, ko, 0, 650, grad_q=gq, grad_k=gk, grad_v=gv)
+    R.sequence_status_sync()
+    assert (out == 7.0).all() and (lse == 7.0).all() and (gq == 7.0).all()
+    for t in (gk, gv):
+        assert not t[:680].any() and (t[680:] == 7.0).all()
+
+
 # ------------------------------------------------------------------ differences
 def test_gradients_against_differences(R):
     """Each gradient's product with a direction against the central difference

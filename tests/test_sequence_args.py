@@ -116,6 +116,22 @@ def test_attend_workspace_is_asked_for(R):
     assert L.recis_attend_workspace(ctypes.byref(a), 0, None) == R.ERR_INVALID_ARG
 
 
+@pytest.mark.parametrize("backward", [0, 1])
+@pytest.mark.parametrize("Hq", [1, 16, 17, 64, 65, 128])
+def test_attend_workspace_of_a_bound_of_zero(R, Hq, backward):
+    """The launches take a bound of 0 as 1, so the workspace does too: rows of no
+    bag (max_q 0) have their place in the backward's sums."""
+    L, sizes = R.load(), []
+    for bound in (0, 1):
+        nb = ctypes.c_int64()
+        a = _attend_args(Hq=Hq, Hkv=1, B=3, Tq=3, Tk=9000, max_q=bound, max_k=9000)
+        assert L.recis_attend_workspace(ctypes.byref(a), backward, ctypes.byref(nb)) == R.OK
+        sizes.append(nb.value)
+    assert sizes[0] == sizes[1]
+    if backward and Hq > 64:  # -delta and -lse of every row
+        assert sizes[0] >= 2 * 3 * Hq * 4
+
+
 def test_binding_refuses(R):
     w, t = torch.zeros(4, 8), torch.zeros(3, dtype=torch.int64)
     with pytest.raises(ValueError):  # no CPU fallback
