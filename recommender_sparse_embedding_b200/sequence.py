@@ -406,7 +406,8 @@ class SequenceAttention:
                 token_offsets: torch.Tensor, max_tokens: int, max_keys: int,
                 key_mask: Optional[torch.Tensor] = None) -> torch.Tensor:
         """keys int64[N] in bags bag_offsets int64[B+1]; tokens int64[T] in bags
-        token_offsets int64[B+1]; returns [T, heads, head_dim].  keys and
+        token_offsets int64[B+1]; returns [T, heads, head_dim], zeros for tokens
+        of no bag or of a bag that passes max_tokens or max_keys.  keys and
         bag_offsets stay unchanged until backward."""
         B = bag_offsets.numel() - 1
         rows = torch.empty((keys.numel(), self.table.dim), dtype=torch.float32, device=keys.device)
@@ -416,20 +417,23 @@ class SequenceAttention:
         q = q.view(-1, self.heads, self.head_dim)
         k, v = self._halves(kv)
         bags = (token_offsets, bag_offsets, max_tokens, max_keys)
-        out, lse = attend(q, k, v, *bags, key_mask=key_mask)
+        out, lse = attend(q, k, v, *bags, key_mask=key_mask, out=torch.zeros_like(q))
         self._ctx = (batch, rows, mean, rstd, tokens, q, kv, out, lse, bags, key_mask)
         return out
 
     def backward(self, grad_out: torch.Tensor):
         """(grad of query_weight, of norm_weight, of norm_bias); the table's rows
-        are updated."""
+        are updated.  Keys and tokens of no bag, or of a bag that passes max_keys or
+        max_tokens, have gradients of zero."""
         if self._ctx is None:
             raise RuntimeError("backward before forward")
         batch, rows, mean, rstd, tokens, q, kv, out, lse, bags, key_mask = self._ctx
         k, v = self._halves(kv)
-        dkv = torch.empty_like(kv)
+        # attend_backward leaves the rows of no bag, and of a bag it reports, as they
+        # were; all rows go on into the sums and the table
+        dkv, dq = torch.zeros_like(kv), torch.zeros_like(q)
         dk, dv = self._halves(dkv)
-        dq, _, _ = attend_backward(grad_out, q, k, v, out, lse, *bags, key_mask=key_mask, grad_k=dk, grad_v=dv)
+        attend_backward(grad_out, q, k, v, out, lse, *bags, key_mask=key_mask, grad_q=dq, grad_k=dk, grad_v=dv)
         drows, dw, db = layer_norm_backward(dkv, rows, mean, rstd, self.norm_weight, self.norm_bias)
         self.table.backward_update(batch, grad_unpooled=drows)
         dquery = embed_grad(tokens, dq.flatten(1), self.query_weight.shape[0], self.query_scale)

@@ -372,7 +372,7 @@ def test_attend_empty_calls(R):
     assert not gk.any() and not gv.any()
 
 
-@pytest.mark.parametrize("Hq,Hkv", [(2, 2), (17, 1), (128, 1), (260, 2)])
+@pytest.mark.parametrize("Hq,Hkv", [(2, 2), (17, 1), (128, 1), (256, 2)])
 def test_attend_rows_of_no_bag_with_a_bound_of_zero(R, Hq, Hkv):
     """max_q 0: no bag has queries, q's rows belong to none; keys get zeros."""
     g = _gen(Hq)
@@ -564,4 +564,51 @@ def test_sequence_attention_trains_the_table(R):
         most = float(per_key.max()) * 0.071 * (step + 1) + 1e-5
         assert float(abs(ge - pe).max()) <= most
     for t in (table, plain, b0, b1):
+        t.close()
+
+
+def test_sequence_attention_gives_rows_of_no_bag_no_gradient(R):
+    """A bag longer than max_keys, and tokens behind the last bag: as if the bag's
+    keys were masked and the tokens were not there.  New memory is filled with NaN."""
+    g = _gen(51)
+    Hkv, Dh, Hq, V = 2, 16, 4, 30
+    D = 2 * Hkv * Dh
+    tables = [R.Table(D, R.ADAGRAD, lr=0.05, adagrad_init_acc=0.5, init_scale=1.0, init_seed=3) for _ in range(2)]
+    batches = [R.Batch(), R.Batch()]
+    qw, nw, nb = _randn((V, Hq * Dh), F32, g), _randn((D,), F32, g) + 1, _randn((D,), F32, g)
+    kl, ql, tail = [40, 7, 140, 130], [2, 3, 4, 21], 5
+    keys = torch.randint(0, 90, (sum(kl),), device="cuda", generator=g) * 1009
+    tok = torch.randint(0, V, (sum(ql) + tail,), device="cuda", generator=g)
+    qo, ko = _offsets(ql), _offsets(kl)
+    go = _randn((sum(ql) + tail, Hq, Dh), F16, g)
+    got = []
+    torch.use_deterministic_algorithms(True, warn_only=True)  # fills new tensors with NaN
+    try:
+        for t, b, i in zip(tables, batches, range(2)):
+            att = R.SequenceAttention(t, qw, Hq, Hkv, nw, nb, query_scale=1.5, dtype=F16)
+            if i == 0:
+                out = att.forward(b, keys, ko, tok, qo, max(ql), 135)
+                with pytest.raises(R.RecisError):
+                    R.sequence_status_sync()
+                res = att.backward(go)
+                with pytest.raises(R.RecisError):
+                    R.sequence_status_sync()
+            else:
+                mask = torch.ones(sum(kl), dtype=torch.bool, device="cuda")
+                mask[47:187] = False
+                n = sum(ql)
+                out = att.forward(b, keys, ko, tok[:n], qo, max(ql), 140, key_mask=mask)
+                res = att.backward(go[:n])
+                R.sequence_status_sync()
+            t.status_sync()
+            got.append((out, *res, *t.export()[:3]))
+    finally:
+        torch.use_deterministic_algorithms(False)
+    n = sum(ql)
+    assert not got[0][0][n:].any() and torch.equal(got[0][0][:n], got[1][0])
+    for p, q in zip(got[0][1:4], got[1][1:4]):
+        assert torch.isfinite(p).all() and torch.equal(p, q)
+    for p, q in zip(got[0][4:], got[1][4:]):
+        assert (p == q).all()
+    for t in (*tables, *batches):
         t.close()
