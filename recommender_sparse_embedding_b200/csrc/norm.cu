@@ -550,10 +550,10 @@ int resident_blocks(K kernel, int block, size_t smem, std::atomic<int> (&cache)[
   return n * kSMs;
 }
 
-// dynamic shared memory beyond the default, once asked for
+// dynamic shared memory beyond the default (48 KB with the kernels' own half KB), once asked for
 template <typename K>
 cudaError_t more_smem(K kernel, size_t smem) {
-  return smem > 48 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)
+  return smem > 47 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)
                           : cudaSuccess;
 }
 

@@ -168,6 +168,18 @@ def test_layer_norm(R, M, D, xt, yt, wt):
     assert all(torch.equal(p, q) for p, q in zip((dx, dw, db), again))
 
 
+@pytest.mark.parametrize("D", [6112, 6120, 6144])
+@pytest.mark.parametrize("xt,yt", [(F16, BF16), (BF16, F16)])  # types no wider row is normalised in before
+def test_layer_norm_parameters_that_just_fit_the_default_shared_memory(R, xt, yt, D):
+    """Weight and bias take 48 KB of shared memory at 6144 columns, the block's
+    sums some more."""
+    g = _gen(D)
+    x, w, b = _randn((3, D), xt, g), _randn((D,), F32, g), _randn((D,), F32, g)
+    y = R.layer_norm(x, w, b, out_dtype=yt)[0]
+    ref = S.Norm(x, w, b, 1e-5)
+    S.close(y, ref.y, ref.y_err * 1.01 + S.half_step(yt) * 1.01 * ref.y.abs() + (2.0 ** -24 if yt == F16 else 0), "y")
+
+
 def test_layer_norm_strided_rows_and_no_parameters(R):
     g = _gen(8)
     buf = _randn((40, 3, 48), F32, g)
