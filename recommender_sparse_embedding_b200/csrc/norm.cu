@@ -550,11 +550,14 @@ int resident_blocks(K kernel, int block, size_t smem, std::atomic<int> (&cache)[
   return n * kSMs;
 }
 
-// dynamic shared memory beyond the default (48 KB with the kernels' own half KB), once asked for
-template <typename K>
-cudaError_t more_smem(K kernel, size_t smem) {
-  return smem > 47 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)
-                          : cudaSuccess;
+// Dynamic shared memory beyond the default (48 KB with the kernels' own half KB).
+// The limit is the function's, not the launch's, so it is raised once to the most
+// that any row takes: a smaller one set for a narrower row would refuse a wide
+// row's launch in another host thread.
+template <int MOST, typename K>
+cudaError_t more_smem(K kernel, std::atomic<uint64_t> (&done)[2]) {
+  if constexpr (MOST > 47 * 1024) return allow_smem(kernel, MOST, done);
+  else return cudaSuccess;
 }
 
 template <typename TX, typename TY, int VEC, int UPT, bool EXACT>
@@ -562,8 +565,10 @@ cudaError_t norm_go(const NormParams& p, cudaStream_t s) {
   static std::atomic<int> cache[16];
   auto kernel = norm_kernel<TX, TY, VEC, UPT, EXACT>;
   const int block = std::max(p.tpr, 128), rows = block / p.tpr;
-  const size_t smem = Params<VEC, UPT, 2>::kKeep ? 0 : (size_t)p.D * 8;  // at most 128 KB
-  const cudaError_t e = more_smem(kernel, smem);
+  constexpr bool keep = Params<VEC, UPT, 2>::kKeep;
+  const size_t smem = keep ? 0 : (size_t)p.D * 8;  // D is at most kMaxRowThreads * UPT * VEC
+  static std::atomic<uint64_t> done[2];
+  const cudaError_t e = more_smem<keep ? 0 : kMaxRowThreads * UPT * VEC * 8>(kernel, done);
   if (e != cudaSuccess) return e;
   const int grid = (int)std::min<int64_t>((p.M + rows - 1) / rows, resident_blocks(kernel, block, smem, cache));
   kernel<<<grid, block, smem, s>>>(p);
@@ -621,8 +626,9 @@ cudaError_t back_go(const NormParams& p, cudaStream_t s, int* blocks_out) {
   static std::atomic<int> cache[16];
   auto kernel = norm_back_kernel<TX, TY, VEC, UPT, EXACT>;
   const int block = std::max(p.tpr, 256), rows = block / p.tpr;
-  const size_t smem = (size_t)2 * p.tpr * UPT * VEC * 4;  // at most 64 KB
-  const cudaError_t e = more_smem(kernel, smem);
+  const size_t smem = (size_t)2 * p.tpr * UPT * VEC * 4;
+  static std::atomic<uint64_t> done[2];
+  const cudaError_t e = more_smem<2 * kMaxRowThreads * UPT * VEC * 4>(kernel, done);
   if (e != cudaSuccess) return e;
   const int64_t most = std::min<int64_t>(back_blocks(p.M), (p.M + rows - 1) / rows);
   const int grid = (int)std::min<int64_t>(most, resident_blocks(kernel, block, smem, cache));

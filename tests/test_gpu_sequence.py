@@ -3,6 +3,7 @@
 gradient, layer norm, attention over the keys of each bag, and the attention
 pooling of a table's bags built from them."""
 import math
+import threading
 
 import pytest
 import torch
@@ -178,6 +179,34 @@ def test_layer_norm_parameters_that_just_fit_the_default_shared_memory(R, xt, yt
     y = R.layer_norm(x, w, b, out_dtype=yt)[0]
     ref = S.Norm(x, w, b, 1e-5)
     S.close(y, ref.y, ref.y_err * 1.01 + S.half_step(yt) * 1.01 * ref.y.abs() + (2.0 ** -24 if yt == F16 else 0), "y")
+
+
+def test_layer_norm_from_two_threads(R):
+    """Widths whose parameters need more than 48 KB of shared memory each, from two
+    host threads at once."""
+    g = _gen(12)
+    xs = [_randn((2, D), F32, g) for D in (6400, 8000)]
+    want = [R.layer_norm(x)[0] for x in xs]
+    torch.cuda.synchronize()
+    L, failed = R.load(), []
+
+    def calls(x, y):  # the entry point itself, which runs outside the interpreter's lock
+        got = torch.empty_like(x)
+        M, D = x.shape
+        for _ in range(20000):
+            if L.recis_layer_norm(x.data_ptr(), 0, D, M, D, None, None, 0, 1e-5, got.data_ptr(), 0, D, None, None,
+                                  torch.cuda.current_stream().cuda_stream) != R.OK:
+                failed.append(L.recis_last_error_string())
+        torch.cuda.synchronize()
+        if not torch.equal(got, y):
+            failed.append("other values")
+
+    threads = [threading.Thread(target=calls, args=a) for a in zip(xs, want)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, (len(failed), failed[0])
 
 
 def test_layer_norm_strided_rows_and_no_parameters(R):
