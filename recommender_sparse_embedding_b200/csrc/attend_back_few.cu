@@ -83,10 +83,10 @@ __global__ void __launch_bounds__(kThreads, FewBackCfg<DP, NR>::kTwo ? 2 : 1)
   if (sp > 0 && ks >= bag.nk) return;
   const int tid = threadIdx.x, lane = tid & 31, w = __shfl_sync(0xffffffffu, tid >> 5, 0);
   if (rows == 0) {  // keys without queries: zero gradients
-    const int per = p.D / 8;
-    for (int i = tid; i < (ke - ks) * per; i += kThreads) {
-      const int64_t t = bag.k0 + ks + i / per;
-      const int d = i % per * 8;
+    // a thread keeps its piece of the rows: the pieces of all rows may pass 2^31
+    const int per = p.D / 8, step = kThreads / per, d = tid % per * 8;
+    for (int i = tid < step * per ? tid / per : ke - ks; i < ke - ks; i += step) {
+      const int64_t t = bag.k0 + ks + i;
       *reinterpret_cast<uint4*>(static_cast<T*>(p.gk) + t * p.gks + h * p.gkh + d) = make_uint4(0, 0, 0, 0);
       *reinterpret_cast<uint4*>(static_cast<T*>(p.gv) + t * p.gvs + h * p.gvh + d) = make_uint4(0, 0, 0, 0);
     }

@@ -383,6 +383,21 @@ def test_attend_reads_rows_in_any_order_of_strides(R):
         R.attend_backward(out, q, k, k, out, lse, qo, ko, 20, 300, grad_k=buf.as_strided((300, 2, 32), (32, 256, 1)))
 
 
+def test_attend_zeros_of_a_bag_of_keys_without_queries_past_32_bits(R):
+    """2^27 keys of 128 in one bag without queries: 2^31 pieces of 16 bytes."""
+    if torch.cuda.mem_get_info()[0] < 80 << 30:
+        pytest.skip("needs 80 GB")
+    n, B, D = 1 << 27, 444, 128  # bags enough that the keys are not split
+    k = torch.zeros(8 * n + D, dtype=BF16, device="cuda").as_strided((n, 1, D), (8, D, 1))
+    grad = torch.ones((n, 2, 1, D), dtype=BF16, device="cuda")
+    q = torch.ones((1, 1, D), dtype=BF16, device="cuda")
+    qo, ko = torch.zeros(B + 1, dtype=torch.int64, device="cuda"), _offsets([n] + [0] * (B - 1))
+    R.attend_backward(q, q, k, k, q, torch.zeros((1, 1), device="cuda"), qo, ko, 1, n, grad_k=grad[:, 0],
+                      grad_v=grad[:, 1])
+    R.sequence_status_sync()
+    assert not grad.any()
+
+
 def test_attend_bad_offsets_are_reported(R):
     g = _gen(7)
     q, k, v = (_randn((40, 2, 32), BF16, g) for _ in range(3))
