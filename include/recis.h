@@ -510,7 +510,9 @@ recis_status recis_layer_norm_backward(const void* grad_y, int32_t y_type, int64
  * and so on alike.  lse: fp32 [Tq][Hq], contiguous.  D: a multiple of 8, 8..128.
  * Hq a multiple of Hkv, Hq / Hkv <= 128.  B, Tq, Tk below 2^31 - 65537, max_q * Hq
  * and max_k * Hkv at most 2^30 (a bound of 0 counts as 1 here).
- * max_q and max_k (host) bound the bags' lengths.  Offsets that decrease,
+ * max_q and max_k (host) bound the bags' lengths; a call is refused where the
+ * blocks that B, Hkv and the bounds give room for (one for up to 16 or 128 rows or
+ * keys of a bag and key head) pass 2^31.  Offsets that decrease,
  * leave [0, Tq] or [0, Tk], or give a bag longer than its bound are a
  * device-detected error (RECIS_ERR_INVALID_ARG); such a bag's rows are
  * undefined, every access stays in bounds. */

@@ -477,7 +477,7 @@ recis_status forward(const AttendParams& p, cudaStream_t s) {
   const bool few = few_rows(p.max_q, p.G);
   const int64_t rtiles = ((int64_t)p.max_q * p.G + kRowTile - 1) / kRowTile;
   const int64_t grid = (int64_t)p.B * p.splits * p.Hkv * rtiles, jgrid = (int64_t)p.B * (((int64_t)p.max_q * p.Hq + 3) / 4);
-  if ((few && !grid_fits(grid)) || !grid_fits(jgrid)) {
+  if ((few && !grid_fits(grid)) || (p.splits > 1 && !grid_fits(jgrid))) {
     set_error("attend: too many blocks (bags times max_q times heads)");
     return RECIS_ERR_INVALID_ARG;
   }

@@ -398,6 +398,18 @@ def test_attend_zeros_of_a_bag_of_keys_without_queries_past_32_bits(R):
     assert not grad.any()
 
 
+def test_attend_wide_bounds_need_no_join(R):
+    """Bounds of 2^30 rows for 8 bags of a few: the blocks fit a grid, and nothing is joined."""
+    g = _gen(13)
+    q, k, v = (_randn((40, 1, 32), BF16, g) for _ in range(3))
+    off = _offsets([5] * 8)
+    out, lse = R.attend(q, k, v, off, off, 1 << 30, 5)
+    R.sequence_status_sync()
+    ref = S.attend(q, k, v, off, off, 32 ** -0.5)
+    S.close(out, *ref["out"], "out")
+    S.close(lse, *ref["lse"], "lse")
+
+
 def test_attend_bad_offsets_are_reported(R):
     g = _gen(7)
     q, k, v = (_randn((40, 2, 32), BF16, g) for _ in range(3))
