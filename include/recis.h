@@ -431,7 +431,9 @@ recis_status recis_reduce_grad(recis_batch_t b, const int64_t* bag_offsets, int3
 #define RECIS_F16 2
 
 /* Synchronous: waits for `stream`, returns and clears the device-detected
- * status of earlier calls of this section on the current device.  The first
+ * status of earlier calls of this section on the current device.  The status is
+ * one a device: an error found on any of its streams is returned to the next
+ * caller that asks, on whichever stream, and to no later one.  The first
  * call of the section on a device looks up the status word's address; make it
  * before any stream capture. */
 recis_status recis_sequence_status_sync(recis_stream_t stream);

@@ -698,6 +698,10 @@ cudaError_t grad_launch(SumParams p, const int64_t* tok, char* ws, cudaStream_t 
   return cudaGetLastError();
 }
 
+// Clears the bits of the status word that a caller has read, no others: another
+// stream's kernel may have set one since.
+__global__ void status_clear_kernel(int* status, int bits) { atomicAnd(status, ~bits); }
+
 }  // namespace
 
 int* sequence_status() {
@@ -732,7 +736,8 @@ extern "C" recis_status recis_sequence_status_sync(recis_stream_t stream) {
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
   if (e != cudaSuccess) return cuda_fail(e, "status read");
   if (!h) return RECIS_OK;
-  if ((e = cudaMemsetAsync(st, 0, sizeof(int), s)) != cudaSuccess) return cuda_fail(e, "status clear");
+  status_clear_kernel<<<1, 1, 0, s>>>(st, h);
+  if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "status clear");
   if ((e = cudaStreamSynchronize(s)) != cudaSuccess) return cuda_fail(e, "status clear");
   if (h & kErrTimeout) {
     set_error("a bounded device-side wait gave up");

@@ -4,6 +4,7 @@ gradient, layer norm, attention over the keys of each bag, and the attention
 pooling of a table's bags built from them."""
 import math
 import threading
+import time
 
 import pytest
 import torch
@@ -408,6 +409,49 @@ def test_attend_wide_bounds_need_no_join(R):
     ref = S.attend(q, k, v, off, off, 32 ** -0.5)
     S.close(out, *ref["out"], "out")
     S.close(lse, *ref["lse"], "lse")
+
+
+def test_status_of_calls_in_two_threads(R):
+    """Two threads make calls that fail in different ways and ask for the status:
+    a failure is reported to the thread that made it, or to the other one if that
+    asked meanwhile."""
+    g = _gen(14)
+    w, bad = _randn((4, 8), F32, g), torch.tensor([9], device="cuda")
+    q = _randn((4, 1, 16), BF16, g)
+    good, long = _offsets([4]), _offsets([5])
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    stop, reports = threading.Event(), []  # the other thread's: (from, to)
+
+    def offsets_reported(stream):
+        try:
+            R.sequence_status_sync(stream)
+        except R.RecisError as e:
+            return "bag offsets" in str(e)
+        return False
+
+    def tokens():
+        while not stop.is_set():
+            R.embed_lookup(w, bad, stream=streams[0])
+            t = time.monotonic()
+            if offsets_reported(streams[0]):
+                reports.append((t, time.monotonic()))
+
+    R.attend(q, q, q, good, good, 4, 4)
+    torch.cuda.synchronize()
+    other = threading.Thread(target=tokens)
+    other.start()
+    open_calls = []
+    for _ in range(2000):
+        t = time.monotonic()
+        R.attend(q, q, q, good, long, 4, 5, stream=streams[1])
+        streams[1].synchronize()
+        if not offsets_reported(streams[1]):
+            open_calls.append((t, time.monotonic()))
+    stop.set()
+    other.join()
+    offsets_reported(streams[0])
+    lost = [c for c in open_calls if not any(r[0] <= c[1] and c[0] <= r[1] for r in reports)]
+    assert not lost, f"{len(lost)} of 2000 failures were reported to no thread"
 
 
 def test_attend_bad_offsets_are_reported(R):
