@@ -49,7 +49,8 @@ __device__ __forceinline__ Bag load_bag(const AttendParams& p, int b) {
 // and 112).
 constexpr int kFewRows = 16;
 inline bool few_rows(int64_t max_q, int64_t G) { return max_q * G <= kFewRows; }
-// At most this many keys in a bag: the backward takes ds as two 16-bit values.
+// At most this many keys in a bag (its own, whatever max_k is): the backward takes
+// ds as two 16-bit values.
 // (The gradients of q and k are then within 1.4 times their own rounding of 64
 // bits, at 8 keys as at 128; with one value they are at 1.7 times at 8 keys and
 // at 1.45 from 128 on.)

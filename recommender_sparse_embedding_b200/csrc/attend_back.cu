@@ -24,7 +24,8 @@
 // products take 1294 and 1038 (64 columns a product from shared memory take 49
 // cycles instead of 32), issuing them and their waits and commits about 1400.
 //
-// Bags of few keys (SPLIT) have dS go into its products as two 16-bit values,
+// Bags of few keys (SPLIT, by the bag's own length, so that its gradients do not
+// depend on its neighbours) have dS go into its products as two 16-bit values,
 // its rounding and what that leaves out (over the two halves of dP's columns):
 // there the rounding of dS and that of `out` in delta would add up to more than
 // 1.5 times the gradients' own rounding.  The more keys, the more the second
@@ -69,9 +70,10 @@ struct BackMaps {
   CUtensorMap x1, x2, y1, y2;
 };
 
+// One block's work: tile `tile` of key head h of a bag, against part sp of its keys
 template <typename T, int DP, bool KEYS, bool SPLIT>
-__global__ void __launch_bounds__(BackCfg<DP, KEYS>::kThreads, 1)
-    attend_back_kernel(const __grid_constant__ AttendParams p, const __grid_constant__ BackMaps maps, int spin_max) {
+__device__ __forceinline__ void attend_back_block(const AttendParams& p, const BackMaps& maps, int spin_max,
+                                                  const Bag& bag, int tile, int h, int sp) {
   using C = BackCfg<DP, KEYS>;
   constexpr int NB = C::kBuf, WG = C::kWG, kNS = C::kNS;
   extern __shared__ __align__(1024) uint8_t base[];  // nothing else is in shared memory: it starts at a tile's boundary
@@ -87,16 +89,6 @@ __global__ void __launch_bounds__(BackCfg<DP, KEYS>::kThreads, 1)
 
   // the block's tile: of keys, or of (query, head) rows against a part of the keys
   const int TQ = kX / p.G;                                  // queries: queries a tile
-  const int per_bag = KEYS ? (p.max_k + kX - 1) / kX : (p.max_q + TQ - 1) / TQ;
-  unsigned id = blockIdx.x;
-  const int tile = id % per_bag;
-  id /= per_bag;
-  const int h = id % p.Hkv;
-  id /= p.Hkv;
-  pdl_wait();
-  pdl_trigger();  // the next kernel may be brought in; it waits for this grid's end
-  const int sp = KEYS ? 0 : id % p.splits, b = KEYS ? id : id / p.splits;
-  const Bag bag = load_bag(p, b);
   const int first = tile * (KEYS ? kX : TQ);                // first key, or query, of the tile
   const int ks = KEYS ? 0 : sp * p.split_keys, ke = KEYS ? bag.nk : min(ks + p.split_keys, bag.nk);
   if (first >= (KEYS ? bag.nk : bag.nq) || (!KEYS && sp > 0 && ks >= bag.nk)) return;
@@ -461,6 +453,26 @@ __global__ void __launch_bounds__(BackCfg<DP, KEYS>::kThreads, 1)
   if (w == kIssuer) tmem_free(tmem, C::kCols);
 }
 
+template <typename T, int DP, bool KEYS>
+__global__ void __launch_bounds__(BackCfg<DP, KEYS>::kThreads, 1)
+    attend_back_kernel(const __grid_constant__ AttendParams p, const __grid_constant__ BackMaps maps, int spin_max) {
+  const int TQ = kX / p.G;
+  const int per_bag = KEYS ? (p.max_k + kX - 1) / kX : (p.max_q + TQ - 1) / TQ;
+  unsigned id = blockIdx.x;
+  const int tile = id % per_bag;
+  id /= per_bag;
+  const int h = id % p.Hkv;
+  id /= p.Hkv;
+  pdl_wait();
+  pdl_trigger();  // the next kernel may be brought in; it waits for this grid's end
+  const int sp = KEYS ? 0 : id % p.splits, b = KEYS ? id : id / p.splits;
+  const Bag bag = load_bag(p, b);
+  // (two whole bodies: with a branch around the second values alone, or two loops
+  // in the compute warps, both passes of long bags take 5 % longer)
+  if (bag.nk <= kSplitKeys) attend_back_block<T, DP, KEYS, true>(p, maps, spin_max, bag, tile, h, sp);
+  else attend_back_block<T, DP, KEYS, false>(p, maps, spin_max, bag, tile, h, sp);
+}
+
 // What the passes need of a row: -delta, delta[t][h] = sum_d grad_out * out, and
 // -lse * log2(e) (-inf for a row without keys: p = 0).  16 lanes a (query,
 // head), 8 columns each.
@@ -515,10 +527,10 @@ __global__ void __launch_bounds__(128) join_q_kernel(const __grid_constant__ Att
       make_uint2(pack2<T>(a.x, a.y), pack2<T>(a.z, a.w));
 }
 
-template <typename T, int DP, bool KEYS, bool SPLIT>
+template <typename T, int DP, bool KEYS>
 cudaError_t back_go(const AttendParams& p, const BackMaps& m, int64_t grid, cudaStream_t s) {
   using C = BackCfg<DP, KEYS>;
-  auto kernel = attend_back_kernel<T, DP, KEYS, SPLIT>;
+  auto kernel = attend_back_kernel<T, DP, KEYS>;
   static std::atomic<uint64_t> done[2];
   const cudaError_t e = allow_smem(kernel, C::kTotal, done);
   if (e != cudaSuccess) return e;
@@ -527,9 +539,7 @@ cudaError_t back_go(const AttendParams& p, const BackMaps& m, int64_t grid, cuda
 
 template <typename T, bool KEYS>
 cudaError_t back_launch(const AttendParams& p, const BackMaps& m, int64_t grid, cudaStream_t s) {
-  const bool split = p.max_k <= kSplitKeys;
-  if (p.D <= 64) return split ? back_go<T, 64, KEYS, true>(p, m, grid, s) : back_go<T, 64, KEYS, false>(p, m, grid, s);
-  return split ? back_go<T, 128, KEYS, true>(p, m, grid, s) : back_go<T, 128, KEYS, false>(p, m, grid, s);
+  return p.D <= 64 ? back_go<T, 64, KEYS>(p, m, grid, s) : back_go<T, 128, KEYS>(p, m, grid, s);
 }
 
 // joins the parts of grad_q

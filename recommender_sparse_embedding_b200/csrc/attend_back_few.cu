@@ -54,11 +54,14 @@ struct FewBackCfg {
   static constexpr int kTotal = 2 * kStages * kTile + 2 * 16384 + 2 * kRows + 1024 + 128 + 2 * NR * 4;
 };
 
+struct FewMaps {
+  CUtensorMap q, o, k, v;  // o: grad_out
+};
+
+// One block's work: the rows of key head h of a bag against part sp of its keys
 template <typename T, int DP, int NR, bool SPLIT>
-__global__ void __launch_bounds__(kThreads, FewBackCfg<DP, NR>::kTwo ? 2 : 1)
-    attend_back_few_kernel(const __grid_constant__ AttendParams p, const __grid_constant__ CUtensorMap mq,
-                           const __grid_constant__ CUtensorMap mo, const __grid_constant__ CUtensorMap mk,
-                           const __grid_constant__ CUtensorMap mv, int spin_max) {
+__device__ __forceinline__ void few_back_block(const AttendParams& p, const FewMaps& maps, int spin_max, const Bag& bag,
+                                               int h, int sp) {
   using C = FewBackCfg<DP, NR>;
   constexpr int NS = C::kStages, H = NR / 2;  // H: columns a compute warpgroup takes
   extern __shared__ uint8_t s_raw[];
@@ -71,13 +74,6 @@ __global__ void __launch_bounds__(kThreads, FewBackCfg<DP, NR>::kTwo ? 2 : 1)
   float* s_delta = s_lse + NR;
   __shared__ uint32_t s_tmem;
 
-  unsigned id = blockIdx.x;
-  const int h = id % p.Hkv;
-  id /= p.Hkv;
-  const int sp = id % p.splits, b = id / p.splits;
-  pdl_wait();
-  pdl_trigger();  // the join may be brought in; it waits for this grid's end
-  const Bag bag = load_bag(p, b);
   const int rows = bag.nq * p.G;  // <= NR
   const int ks = sp * p.split_keys, ke = min(ks + p.split_keys, bag.nk);
   if (sp > 0 && ks >= bag.nk) return;
@@ -122,16 +118,16 @@ __global__ void __launch_bounds__(kThreads, FewBackCfg<DP, NR>::kTwo ? 2 : 1)
         uint8_t* at = skv + 2 * st * C::kTile;
         mbar_arrive_expect(kv_full + st, 2 * C::kTile);
         for (int i = 0; i < C::kBlocks; ++i) {
-          tma_load3(at + i * kKeys * 128, &mk, 64 * i, h, row, kv_full + st);
-          tma_load3(at + C::kTile + i * kKeys * 128, &mv, 64 * i, h, row, kv_full + st);
+          tma_load3(at + i * kKeys * 128, &maps.k, 64 * i, h, row, kv_full + st);
+          tma_load3(at + C::kTile + i * kKeys * 128, &maps.v, 64 * i, h, row, kv_full + st);
         }
         asked = j + 1;
       };
       if (lane == 0) {
         mbar_arrive_expect(q_raw, (unsigned)(2 * C::kBlocks * p.max_q * p.G * 128));
         for (int i = 0; i < C::kBlocks; ++i) {
-          tma_load3(sq + i * NR * 128, &mq, 64 * i, h * p.G, (int)bag.q0, q_raw);
-          tma_load3(so + i * NR * 128, &mo, 64 * i, h * p.G, (int)bag.q0, q_raw);
+          tma_load3(sq + i * NR * 128, &maps.q, 64 * i, h * p.G, (int)bag.q0, q_raw);
+          tma_load3(so + i * NR * 128, &maps.o, 64 * i, h * p.G, (int)bag.q0, q_raw);
         }
         for (int j = 0; j < min(n, NS); ++j) ask(j);
       }
@@ -412,20 +408,28 @@ __global__ void __launch_bounds__(kThreads, FewBackCfg<DP, NR>::kTwo ? 2 : 1)
   if (w == kIssuer) tmem_free(tmem, C::kCols);
 }
 
-template <typename T, int DP, int NR, bool SPLIT>
-cudaError_t few_back_go(const AttendParams& p, const CUtensorMap (&m)[4], int64_t grid, cudaStream_t s) {
-  using C = FewBackCfg<DP, NR>;
-  auto kernel = attend_back_few_kernel<T, DP, NR, SPLIT>;
-  static std::atomic<uint64_t> done[2];
-  const cudaError_t e = allow_smem(kernel, C::kTotal, done);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(kernel, (unsigned)grid, kThreads, C::kTotal, s, p, m[0], m[1], m[2], m[3], kSpinLimit);
+template <typename T, int DP, int NR>
+__global__ void __launch_bounds__(kThreads, FewBackCfg<DP, NR>::kTwo ? 2 : 1)
+    attend_back_few_kernel(const __grid_constant__ AttendParams p, const __grid_constant__ FewMaps maps, int spin_max) {
+  unsigned id = blockIdx.x;
+  const int h = id % p.Hkv;
+  id /= p.Hkv;
+  const int sp = id % p.splits, b = id / p.splits;
+  pdl_wait();
+  pdl_trigger();  // the join may be brought in; it waits for this grid's end
+  const Bag bag = load_bag(p, b);
+  if (bag.nk <= kSplitKeys) few_back_block<T, DP, NR, true>(p, maps, spin_max, bag, h, sp);
+  else few_back_block<T, DP, NR, false>(p, maps, spin_max, bag, h, sp);
 }
 
 template <typename T, int DP, int NR>
-cudaError_t few_back_launch(const AttendParams& p, const CUtensorMap (&m)[4], int64_t grid, cudaStream_t s) {
-  return p.max_k <= kSplitKeys ? few_back_go<T, DP, NR, true>(p, m, grid, s)
-                               : few_back_go<T, DP, NR, false>(p, m, grid, s);
+cudaError_t few_back_go(const AttendParams& p, const FewMaps& m, int64_t grid, cudaStream_t s) {
+  using C = FewBackCfg<DP, NR>;
+  auto kernel = attend_back_few_kernel<T, DP, NR>;
+  static std::atomic<uint64_t> done[2];
+  const cudaError_t e = allow_smem(kernel, C::kTotal, done);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kernel, (unsigned)grid, kThreads, C::kTotal, s, p, m, kSpinLimit);
 }
 
 }  // namespace
@@ -436,15 +440,15 @@ recis_status launch_attend_back_few(const AttendParams& p, bool bf16, cudaStream
     set_error("attend_backward: too many blocks (bags times longest bag times heads)");
     return RECIS_ERR_INVALID_ARG;
   }
-  CUtensorMap m[4] = {};
+  FewMaps m = {};
   // a map is made only where its array has rows; without rows no block uses it
   bool ok = true;
   if (p.Tq > 0)
-    ok = rows_map(&m[0], p.q, bf16, p.D, p.Hq, p.Tq, p.qs, p.qh, p.G, p.max_q) &&
-         rows_map(&m[1], p.go, bf16, p.D, p.Hq, p.Tq, p.gos, p.goh, p.G, p.max_q);
+    ok = rows_map(&m.q, p.q, bf16, p.D, p.Hq, p.Tq, p.qs, p.qh, p.G, p.max_q) &&
+         rows_map(&m.o, p.go, bf16, p.D, p.Hq, p.Tq, p.gos, p.goh, p.G, p.max_q);
   if (p.Tk > 0)
-    ok = ok && rows_map(&m[2], p.k, bf16, p.D, p.Hkv, p.Tk, p.ks, p.kh, 1, kKeys) &&
-         rows_map(&m[3], p.v, bf16, p.D, p.Hkv, p.Tk, p.vs, p.vh, 1, kKeys);
+    ok = ok && rows_map(&m.k, p.k, bf16, p.D, p.Hkv, p.Tk, p.ks, p.kh, 1, kKeys) &&
+         rows_map(&m.v, p.v, bf16, p.D, p.Hkv, p.Tk, p.vs, p.vh, 1, kKeys);
   if (!ok) {
     set_error("attend_backward: the driver refused a tensor map");
     return RECIS_ERR_CUDA;
@@ -454,12 +458,12 @@ recis_status launch_attend_back_few(const AttendParams& p, bool bf16, cudaStream
   auto go = [&](auto t) {
     using T = decltype(t);
     if (p.D <= 64)
-      return rows <= 16   ? few_back_launch<T, 64, 16>(p, m, grid, s)
-             : rows <= 32 ? few_back_launch<T, 64, 32>(p, m, grid, s)
-                          : few_back_launch<T, 64, 64>(p, m, grid, s);
-    return rows <= 16   ? few_back_launch<T, 128, 16>(p, m, grid, s)
-           : rows <= 32 ? few_back_launch<T, 128, 32>(p, m, grid, s)
-                        : few_back_launch<T, 128, 64>(p, m, grid, s);
+      return rows <= 16   ? few_back_go<T, 64, 16>(p, m, grid, s)
+             : rows <= 32 ? few_back_go<T, 64, 32>(p, m, grid, s)
+                          : few_back_go<T, 64, 64>(p, m, grid, s);
+    return rows <= 16   ? few_back_go<T, 128, 16>(p, m, grid, s)
+           : rows <= 32 ? few_back_go<T, 128, 32>(p, m, grid, s)
+                        : few_back_go<T, 128, 64>(p, m, grid, s);
   };
   const cudaError_t e = bf16 ? go(__nv_bfloat16()) : go(__half());
   return e == cudaSuccess ? RECIS_OK : cuda_fail(e, "attend_back_few launch");

@@ -501,6 +501,26 @@ def test_attend_rows_of_no_bag_with_a_bound_of_zero(R, Hq, Hkv):
         assert not t[:680].any() and (t[680:] == 7.0).all()
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("rows,keys,D", [(5, 8, 64), (40, 100, 128), (150, 8, 128), (70, 128, 64)])
+def test_attend_gradients_do_not_depend_on_neighbours(R, rows, keys, D, dtype):
+    """A bag of few keys, alone and beside a bag of more than 128: the same bits."""
+    g = _gen(rows + keys)
+    ql, kl = [rows, 3, rows], [keys, 300, keys]
+    q, grad = (_randn((sum(ql), 2, D), dtype, g) for _ in range(2))
+    k, v = (_randn((sum(kl), 2, D), dtype, g) for _ in range(2))
+    qo, ko = _offsets(ql), _offsets(kl)
+    out, lse = R.attend(q, k, v, qo, ko, rows, 300)
+    both = R.attend_backward(grad, q, k, v, out, lse, qo, ko, rows, 300)
+    for i in (0, 2):
+        a, b = slice(*qo[i:i + 2].tolist()), slice(*ko[i:i + 2].tolist())
+        alone = R.attend_backward(grad[a], q[a], k[b], v[b], out[a], lse[a], _offsets([rows]), _offsets([keys]), rows,
+                                  keys)
+        for x, y, r in zip(both, alone, (a, b, b)):
+            assert torch.equal(x[r], y)
+    R.sequence_status_sync()
+
+
 # ------------------------------------------------------------------ differences
 def test_gradients_against_differences(R):
     """Each gradient's product with a direction against the central difference
