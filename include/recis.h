@@ -505,8 +505,10 @@ recis_status recis_layer_norm_backward(const void* grad_y, int32_t y_type, int64
  *
  * type: RECIS_BF16 or RECIS_F16, of every array but lse.  p and ds are rounded
  * to it before their matrix products (tensor-core operands; ds of a bag of at most
- * 128 keys to two such values); all sums, the softmax statistics and the joining of
- * partial results are fp32.
+ * 128 keys to two such values; fp16 in the backward after scaling by powers of two,
+ * taken out of the sums again, so that long bags and small or large gradients leave
+ * its normal numbers neither below nor above); all sums, the softmax statistics and
+ * the joining of partial results are fp32.
  * Strides in elements, positive multiples of 8 (16 bytes), arrays 16-byte aligned:
  * element (t, h, j) of q is q[t * q_stride + h * q_head_stride + j], grad_q
  * and so on alike.  lse: fp32 [Tq][Hq], contiguous.  D: a multiple of 8, 8..128.

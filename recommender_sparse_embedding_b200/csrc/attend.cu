@@ -350,7 +350,7 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Atten
 // ---------------------------------------------------------------- host
 struct AttendPlan {
   int splits, split_keys;
-  int64_t po_bytes, pl_bytes, delta_bytes;
+  int64_t po_bytes, pl_bytes, delta_bytes, vnorm_bytes;  // delta_bytes: one array of rows
   int64_t bytes;
 };
 
@@ -375,7 +375,8 @@ AttendPlan attend_plan(const recis_attend_args& a, bool backward) {
     // over query tiles of its own, two blocks an SM.  At least 512 keys a part.
     const int64_t G = a.Hq / a.Hkv, rows = a.max_q * G;
     const bool few = few_back_rows(a.max_q, G);
-    if (!few) g.delta_bytes = 2 * align256(a.Tq * a.Hq * 4);
+    if (!few) g.delta_bytes = align256(a.Tq * a.Hq * 4);
+    if (!few && a.type == RECIS_F16) g.vnorm_bytes = align256(value_slots(a.B, a.Tk) * a.Hkv * 4);
     const int64_t blocks = std::max<int64_t>(1, a.B * a.Hkv * (few ? 1 : (a.max_q + 128 / G - 1) / (128 / G)));
     const int64_t target = kSMs * (few ? 3 * few_back_per_sm(a.D, rows) : 2);
     const int64_t want = std::min<int64_t>((target + blocks - 1) / blocks, (a.max_k + 511) / 512);
@@ -402,7 +403,7 @@ AttendPlan attend_plan(const recis_attend_args& a, bool backward) {
       g.pl_bytes = align256(g.splits * a.Tq * a.Hq * 4);
     }
   }
-  g.bytes = g.po_bytes + g.pl_bytes + g.delta_bytes;
+  g.bytes = g.po_bytes + g.pl_bytes + (g.vnorm_bytes ? 3 : 2) * g.delta_bytes + g.vnorm_bytes;
   return g;
 }
 
@@ -456,8 +457,11 @@ recis_status fill(const recis_attend_args* a, AttendParams* p, const AttendPlan&
   char* at = static_cast<char*>(ws);
   p->po = reinterpret_cast<float*>(at);
   p->pl = reinterpret_cast<float*>(at + g.po_bytes);
-  p->delta = reinterpret_cast<float*>(at + g.po_bytes + g.pl_bytes);
-  p->nlse = reinterpret_cast<float*>(at + g.po_bytes + g.pl_bytes + g.delta_bytes / 2);
+  at += g.po_bytes + g.pl_bytes;
+  p->delta = reinterpret_cast<float*>(at);
+  p->nlse = reinterpret_cast<float*>(at + g.delta_bytes);
+  p->gnorm = reinterpret_cast<float*>(at + 2 * g.delta_bytes);
+  p->vnorm = reinterpret_cast<float*>(at + 3 * g.delta_bytes);
   p->status = st;
   return RECIS_OK;
 }

@@ -21,7 +21,9 @@ struct AttendParams {
   float* po;                // splits > 1: [splits][Tq][Hq][D] each part's output ...
   float* pl;                // ... and [splits][Tq][Hq] its lse
   float* delta;             // backward, many rows: [Tq][Hq] -sum(grad_out * out) ...
-  float* nlse;              // ... and [Tq][Hq] -lse * log2(e)
+  float* nlse;              // ... and [Tq][Hq] -lse * log2(e) (plus kShiftP)
+  float* gnorm;             // fp16 too: [Tq][Hq] |grad_out| ...
+  float* vnorm;             // ... and value_slots() maxima of |v|, one a warp of a key tile
   int* status;
 };
 
@@ -62,6 +64,36 @@ constexpr int kFewBackRows = 64;
 inline bool few_back_rows(int64_t max_q, int64_t G) { return max_q * G <= kFewBackRows; }
 // blocks of that pass an SM holds
 inline int few_back_per_sm(int D, int64_t rows) { return D <= 64 && rows <= 32 ? 2 : 1; }
+
+// fp16 has no normal numbers below 2^-14, and p and ds of a long bag lie there
+// (5000 keys: p about 2^-12, times a gradient of 10^-3).  Its backward therefore
+// rounds p 2^kShiftP and ds 2^e, e from a bound on |ds| so that ds 2^e stays below
+// 2^14 (or the block's largest so far is followed, attend_back_few.cu); the
+// accumulators take the powers of two out again.  bf16 has fp32's range: 0.
+template <typename T>
+constexpr int kShiftP = 0;
+template <>
+constexpr int kShiftP<__half> = 14;
+// 2^e for -126 <= e <= 127
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+// 2^e * scale, finite (a zero accumulator stays zero)
+__device__ __forceinline__ float pow2_times(int e, float scale) {
+  return fminf(fmaxf(pow2(e) * scale, -3e38f), 3e38f);
+}
+// e with 2^13 <= bound * 2^e < 2^14; 0 where bound is 0 or not finite
+__device__ __forceinline__ int half_exponent(float bound) {
+  if (!(bound > 0.f && bound < INFINITY)) return 0;
+  return min(13 + 127 - (int)(__float_as_uint(bound) >> 23), 100);
+}
+__device__ __forceinline__ float finite_max(float a, float b) { return b < INFINITY ? fmaxf(a, b) : a; }  // b >= 0
+__device__ __forceinline__ float warp_max(float v) {  // of values >= 0
+  return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
+}
+// The maxima of |v| of a bag's key tiles (of 128, 4 warps each), bags and tiles in
+// order of their keys: tile i of bag b begins at value_slot(k0, b) + 4 i.
+__host__ __device__ inline int64_t value_slots(int64_t B, int64_t Tk) { return (Tk / 128 + B + 1) * 4; }
+__device__ __forceinline__ int64_t value_slot(int64_t k0, int b) { return (k0 / 128 + b) * 4; }
+
 recis_status launch_attend_back_few(const AttendParams& p, bool bf16, cudaStream_t s);
 recis_status launch_attend_tc(const AttendParams& p, bool bf16, cudaStream_t s);
 recis_status launch_attend_back(const AttendParams& p, bool bf16, cudaStream_t s);

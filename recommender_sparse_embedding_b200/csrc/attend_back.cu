@@ -31,6 +31,13 @@
 // 1.5 times the gradients' own rounding.  The more keys, the more the second
 // averages out, and one value is enough.
 //
+// fp16 (kShiftP in attend.cuh): a thread's row of X is a row of the accumulators, so
+// each thread scales ds by a power of two of its own, from |ds| <= |dO| |V| + |delta|:
+// over keys its own |V| and the largest |dO| and |delta| of the bag's rows, over
+// queries its own |dO| and delta and the largest |V| of the bag's keys, which the
+// pass over keys has left.  (16 bags of 512-1024 over 1024-4096 keys, 8 heads of 128
+// over 4: 564 us, bf16 531; the product more a pair of scores over keys costs most.)
+//
 // Rows of a tile that belong to another bag, or to masked keys, are overwritten
 // with zeros before the products (0 * NaN is NaN) by the warp that issues the
 // copies, which waits for such a tile's data itself.
@@ -61,8 +68,8 @@ struct BackCfg {
   static constexpr int kThreads = kWG * 128 + 64;
   static constexpr uint32_t kCols = 512;
   static constexpr uint32_t kAcc1 = kBuf * 128, kAcc2 = kAcc1 + (KEYS ? DP : 0);
-  // tiles, barriers, lse and delta (or masks) of the streamed rows
-  static constexpr int kBars = 2 * kXBytes + 2 * kNS * kYBytes, kRowData = kBars + 256;
+  // tiles, barriers, the warps' maxima, lse and delta (or masks) of the streamed rows
+  static constexpr int kBars = 2 * kXBytes + 2 * kNS * kYBytes, kMax = kBars + 256, kRowData = kMax + 64;
   static constexpr int kTotal = kRowData + kNS * (KEYS ? 2 * kY * 4 : 8);
 };
 
@@ -73,7 +80,7 @@ struct BackMaps {
 // One block's work: tile `tile` of key head h of a bag, against part sp of its keys
 template <typename T, int DP, bool KEYS, bool SPLIT>
 __device__ __forceinline__ void attend_back_block(const AttendParams& p, const BackMaps& maps, int spin_max,
-                                                  const Bag& bag, int tile, int h, int sp) {
+                                                  const Bag& bag, int b, int tile, int h, int sp) {
   using C = BackCfg<DP, KEYS>;
   constexpr int NB = C::kBuf, WG = C::kWG, kNS = C::kNS;
   extern __shared__ __align__(1024) uint8_t base[];  // nothing else is in shared memory: it starts at a tile's boundary
@@ -329,6 +336,55 @@ __device__ __forceinline__ void attend_back_block(const AttendParams& p, const B
     }
     const bool any = __any_sync(0xffffffffu, live);
     const float c = p.scale_log2;
+    float up = 1.f;  // fp16: ds 2^kShiftP to its own scale
+    if constexpr (kShiftP<T> > 0) {
+      float bound = 0.f;
+      if (KEYS && n > 0) {
+        float* s_max = reinterpret_cast<float*>(base + C::kMax);
+        float go = 0.f, de = 0.f;
+        for (int r = tid; r < bag.nq * p.G; r += WG * 128) {
+          const int64_t i = (bag.q0 + r / p.G) * p.Hq + h * p.G + r % p.G;
+          go = finite_max(go, p.gnorm[i]);
+          de = finite_max(de, fabsf(p.delta[i]));
+        }
+        go = warp_max(go);
+        de = warp_max(de);
+        if (lane == 0) {
+          s_max[w] = go;
+          s_max[8 + w] = de;
+        }
+        asm volatile("bar.sync 3, 256;" ::: "memory");
+#pragma unroll
+        for (int i = 0; i < WG * 4; ++i) {
+          go = fmaxf(go, s_max[i]);
+          de = fmaxf(de, s_max[8 + i]);
+        }
+        ok = mbar_wait(x_full, 0, spin_max);
+        float v = 0.f;
+        for (int i = 0; i < C::kBlocks; ++i)
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            RawVec<T, 8> raw;
+            raw.load(reinterpret_cast<const T*>(x2 + (i * kX + row) * 128 + ((u ^ (row & 7)) << 4)));
+            float f[8];
+            raw.unpack(f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v = fmaf(f[e], f[e], v);
+          }
+        v = live && (!p.mask || p.mask[t]) && v < INFINITY ? sqrtf(v) : 0.f;
+        bound = fmaf(go, v, de);
+        v = warp_max(v);
+        if (wg == 0 && lane == 0) p.vnorm[value_slots(p.B, p.Tk) * h + value_slot(bag.k0, b) + 4 * tile + w] = v;
+      } else if (!KEYS) {
+        float v = 0.f;
+        const float* slots = p.vnorm + value_slots(p.B, p.Tk) * h + value_slot(bag.k0, b);
+        for (int i = ks / kX * 4 + lane; i < (ke + kX - 1) / kX * 4; i += 32) v = fmaxf(v, slots[i]);
+        v = warp_max(v);
+        if (live) bound = fmaf(p.gnorm[t * p.Hq + hx], v, fabsf(delta));
+      }
+      up = pow2(half_exponent(bound) - kShiftP<T>);
+      delta *= up;
+    }
     // two warpgroups take every other tile, each its own S and dP, so that one's
     // exponentials run under the other's products
     for (int j = wg; j < n; j += WG) {
@@ -367,8 +423,20 @@ __device__ __forceinline__ void attend_back_block(const AttendParams& p, const B
             float2 e1 = fma2(as_f2(s[i + 2], s[i + 3]), c2, make_float2(ls.z, ls.w));
             e0 = make_float2(ex2(e0.x), ex2(e0.y));
             e1 = make_float2(ex2(e1.x), ex2(e1.y));
-            float2 f0 = mul2(e0, add2(as_f2(d[i], d[i + 1]), make_float2(de.x, de.y)));
-            float2 f1 = mul2(e1, add2(as_f2(d[i + 2], d[i + 3]), make_float2(de.z, de.w)));
+            float2 f0, f1;
+            if constexpr (kShiftP<T> > 0) {
+              const float2 u2 = make_float2(up, up);
+              if (KEYS) {
+                f0 = mul2(e0, mul2(add2(as_f2(d[i], d[i + 1]), make_float2(de.x, de.y)), u2));
+                f1 = mul2(e1, mul2(add2(as_f2(d[i + 2], d[i + 3]), make_float2(de.z, de.w)), u2));
+              } else {  // delta is scaled already
+                f0 = mul2(e0, fma2(as_f2(d[i], d[i + 1]), u2, make_float2(de.x, de.y)));
+                f1 = mul2(e1, fma2(as_f2(d[i + 2], d[i + 3]), u2, make_float2(de.z, de.w)));
+              }
+            } else {
+              f0 = mul2(e0, add2(as_f2(d[i], d[i + 1]), make_float2(de.x, de.y)));
+              f1 = mul2(e1, add2(as_f2(d[i + 2], d[i + 3]), make_float2(de.z, de.w)));
+            }
             if (!KEYS && valid != 0xffffffffu) {
               if (!(valid >> i & 1)) f0.x = 0.f;
               if (!(valid >> (i + 1) & 1)) f0.y = 0.f;
@@ -401,6 +469,8 @@ __device__ __forceinline__ void attend_back_block(const AttendParams& p, const B
     tc_fence_after();
     const bool have = n > 0 && ok;
     const bool takes = !KEYS || !p.mask || (live && p.mask[t]);  // a masked key's gradients are zero
+    float back = p.scale;  // takes ds's scale out of its sums again
+    if constexpr (kShiftP<T> > 0) back = pow2_times(127 - (int)(__float_as_uint(up) >> 23) - kShiftP<T>, p.scale);
     // 2 accumulators (keys) or 1 (queries) of DP columns, in pieces of 64: the
     // thread's row goes to shared memory (X's tiles are done with), 8 lanes store
     // a row's 128 bytes together.  Parts of grad_q are stored directly, in fp32.
@@ -409,7 +479,7 @@ __device__ __forceinline__ void attend_back_block(const AttendParams& p, const B
     for (int piece = wg; piece < kPieces; piece += WG) {
       const bool acc1 = KEYS && piece < C::kBlocks;
       const int d0 = piece * 64 % DP;
-      const float mul = acc1 ? 1.0f : p.scale;
+      const float mul = acc1 ? pow2(-kShiftP<T>) : back;
       uint8_t* stage = x1 + piece * kX * 128;
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
@@ -469,20 +539,20 @@ __global__ void __launch_bounds__(BackCfg<DP, KEYS>::kThreads, 1)
   const Bag bag = load_bag(p, b);
   // (two whole bodies: with a branch around the second values alone, or two loops
   // in the compute warps, both passes of long bags take 5 % longer)
-  if (bag.nk <= kSplitKeys) attend_back_block<T, DP, KEYS, true>(p, maps, spin_max, bag, tile, h, sp);
-  else attend_back_block<T, DP, KEYS, false>(p, maps, spin_max, bag, tile, h, sp);
+  if (bag.nk <= kSplitKeys) attend_back_block<T, DP, KEYS, true>(p, maps, spin_max, bag, b, tile, h, sp);
+  else attend_back_block<T, DP, KEYS, false>(p, maps, spin_max, bag, b, tile, h, sp);
 }
 
-// What the passes need of a row: -delta, delta[t][h] = sum_d grad_out * out, and
-// -lse * log2(e) (-inf for a row without keys: p = 0).  16 lanes a (query,
-// head), 8 columns each.
+// What the passes need of a row: -delta, delta[t][h] = sum_d grad_out * out,
+// -lse * log2(e) + kShiftP (-inf for a row without keys: p = 0), for fp16 |grad_out|.
+// 16 lanes a (query, head), 8 columns each.
 template <typename T>
 __global__ void __launch_bounds__(256) delta_kernel(const __grid_constant__ AttendParams p) {
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 15, d = lane * 8;
   const int64_t i = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
-  float s = 0.f;
+  float s = 0.f, g = 0.f;
   if (i < p.Tq * p.Hq && d < p.D) {
     const int64_t t = i / p.Hq;
     const int h = (int)(i - t * p.Hq);
@@ -493,14 +563,21 @@ __global__ void __launch_bounds__(256) delta_kernel(const __grid_constant__ Atte
     a.unpack(x);
     b.unpack(y);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) s = fmaf(x[j], y[j], s);
+    for (int j = 0; j < 8; ++j) {
+      s = fmaf(x[j], y[j], s);
+      if (kShiftP<T> > 0) g = fmaf(y[j], y[j], g);
+    }
   }
 #pragma unroll
-  for (int off = 8; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+  for (int off = 8; off > 0; off >>= 1) {
+    s += __shfl_xor_sync(0xffffffffu, s, off);
+    if (kShiftP<T> > 0) g += __shfl_xor_sync(0xffffffffu, g, off);
+  }
   if (lane == 0 && i < p.Tq * p.Hq) {
     const float lse = p.lse[i];
     p.delta[i] = -s;
-    p.nlse[i] = lse == -INFINITY ? -INFINITY : -lse * 1.4426950408889634f;
+    p.nlse[i] = lse == -INFINITY ? -INFINITY : fmaf(-lse, 1.4426950408889634f, (float)kShiftP<T>);
+    if (kShiftP<T> > 0) p.gnorm[i] = sqrtf(g);
   }
 }
 

@@ -24,6 +24,12 @@
 // product of NR more values.  (On long bags, where it is not needed, it takes 170
 // us instead of 152 for 0-16 queries over 256 bags of 1000-5000 keys.)
 //
+// fp16 (kShiftP in attend.cuh): ds takes a power of two of the block's own that
+// follows its largest |ds| so far.  When a tile passes what fp16 holds, all compute
+// warps lower the power, and dQ in tensor memory with it; the barrier that every
+// tile has before P and dS are stored carries the question.  (One query, 8 heads of
+// 128 over 2: 306 us, bf16 303; up to 64 rows of 64: 101 and 99.)
+//
 // While the compute warps store dV and dK of one tile, the scores of the next
 // are made; the copies run further ahead.  Parts of dQ (several blocks a bag)
 // are joined in order by join_q_kernel.
@@ -54,6 +60,32 @@ struct FewBackCfg {
   static constexpr int kTotal = 2 * kStages * kTile + 2 * 16384 + 2 * kRows + 1024 + 128 + 2 * NR * 4;
 };
 
+// fp16: the power of two that dS begins with, above any tile's; `scale` and what
+// takes it and P's out of the accumulators
+constexpr int kHalfUp = 60;
+template <typename T>
+__device__ __forceinline__ float half_down(int up, float scale) {
+  return kShiftP<T> > 0 ? pow2_times(-up - kShiftP<T>, scale) : scale;
+}
+// whether a pair of halves holds an infinity (NaN aside)
+template <int N>
+__device__ __forceinline__ bool any_infinite(const uint32_t (&v)[N]) {
+  __half2 m = __float2half2_rn(0.f);
+#pragma unroll
+  for (int i = 0; i < N; ++i) m = __hmax2(m, __habs2(*reinterpret_cast<const __half2*>(&v[i])));
+  return __hisinf(__low2half(m)) || __hisinf(__high2half(m));
+}
+// whether `v` holds in any compute thread; a barrier of them all
+__device__ __forceinline__ bool block_any(bool v) {
+  uint32_t any;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 5, %2, p;\n selp.u32 %0, 1, 0, q;\n}"
+      : "=r"(any)
+      : "r"((uint32_t)v), "n"(kCompute)
+      : "memory");
+  return any != 0;
+}
+
 struct FewMaps {
   CUtensorMap q, o, k, v;  // o: grad_out
 };
@@ -70,9 +102,10 @@ __device__ __forceinline__ void few_back_block(const AttendParams& p, const FewM
   uint64_t* bar = reinterpret_cast<uint64_t*>(so + C::kRows);
   uint64_t *q_raw = bar, *q_full = bar + 1, *s_full = bar + 2, *e_full = bar + 3, *o_full = bar + 4, *all_done = bar + 5;
   uint64_t *kv_full = bar + 6, *kv_empty = kv_full + NS;
-  float* s_lse = reinterpret_cast<float*>(so + C::kRows + 128);  // [NR] lse * log2(e)
-  float* s_delta = s_lse + NR;
+  float* s_lse = reinterpret_cast<float*>(so + C::kRows + 128);  // [NR] lse * log2(e) - kShiftP
+  float* s_delta = s_lse + NR;                                   // [NR] delta (fp16: times ds's scale)
   __shared__ uint32_t s_tmem;
+  __shared__ float s_max[kCompute / 32];
 
   const int rows = bag.nq * p.G;  // <= NR
   const int ks = sp * p.split_keys, ke = min(ks + p.split_keys, bag.nk);
@@ -225,12 +258,12 @@ __device__ __forceinline__ void few_back_block(const AttendParams& p, const FewM
         }
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-        lse = p.lse[t * p.Hq + hq] * 1.4426950408889634f;
+        lse = fmaf(p.lse[t * p.Hq + hq], 1.4426950408889634f, -(float)kShiftP<T>);
         if (lse == -INFINITY) lse = INFINITY;  // a row without keys: p = 0
       }
       if (lane == 0) {
         s_lse[r] = lse;
-        s_delta[r] = s;
+        s_delta[r] = kShiftP<T> > 0 ? s * pow2(kHalfUp) : s;
       }
     }
     asm volatile("bar.sync 5, 256;" ::: "memory");
@@ -246,6 +279,8 @@ __device__ __forceinline__ void few_back_block(const AttendParams& p, const FewM
       return m;
     };
     unsigned takes_next = mask_at(0);
+    int up = kHalfUp;  // fp16: ds 2^(up + kShiftP) is what is rounded
+    float scaled = kShiftP<T> > 0 ? pow2(kHalfUp) : 1.f;  // 2^up
     for (int j = 0; j < n; ++j) {
       const int k0 = ks + j * kKeys;
       const bool takes = takes_next != 0;
@@ -258,29 +293,67 @@ __device__ __forceinline__ void few_back_block(const AttendParams& p, const FewM
       tmem_ld(mine + wg * H, s);
       tmem_ld(mine + C::kDp + wg * H, d);
       tmem_wait_ld();
-      // both warps of these lanes have read: P and dS go over S and dP
-      asm volatile("bar.sync %0, 64;" ::"r"(1 + (w & 3)) : "memory");
+      // both warps of these lanes have read before P and dS go over S and dP (fp16: all warps, below)
+      if (kShiftP<T> == 0) asm volatile("bar.sync %0, 64;" ::"r"(1 + (w & 3)) : "memory");
+      float f[H];
 #pragma unroll
       for (int i = 0; i < H; i += 4) {
         const float4 ls = *reinterpret_cast<const float4*>(s_lse + wg * H + i);
         const float4 de = *reinterpret_cast<const float4*>(s_delta + wg * H + i);
-        float e[4], f[4];
-        e[0] = ex2(fmaf(__uint_as_float(s[i]), c, -ls.x));
-        e[1] = ex2(fmaf(__uint_as_float(s[i + 1]), c, -ls.y));
-        e[2] = ex2(fmaf(__uint_as_float(s[i + 2]), c, -ls.z));
-        e[3] = ex2(fmaf(__uint_as_float(s[i + 3]), c, -ls.w));
-        f[0] = takes ? e[0] * (__uint_as_float(d[i]) - de.x) : 0.f;
-        f[1] = takes ? e[1] * (__uint_as_float(d[i + 1]) - de.y) : 0.f;
-        f[2] = takes ? e[2] * (__uint_as_float(d[i + 2]) - de.z) : 0.f;
-        f[3] = takes ? e[3] * (__uint_as_float(d[i + 3]) - de.w) : 0.f;
+        const float l4[4] = {ls.x, ls.y, ls.z, ls.w}, d4[4] = {de.x, de.y, de.z, de.w};
+        float e[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const float dp = __uint_as_float(d[i + u]);
+          e[u] = ex2(fmaf(__uint_as_float(s[i + u]), c, -l4[u]));
+          f[i + u] = takes ? e[u] * (kShiftP<T> > 0 ? fmaf(dp, scaled, -d4[u]) : dp - d4[u]) : 0.f;
+        }
         pk[i / 2] = pack2<T>(e[0], e[1]);
         pk[i / 2 + 1] = pack2<T>(e[2], e[3]);
+        dk[i / 2] = pack2<T>(f[i], f[i + 1]);
+        dk[i / 2 + 1] = pack2<T>(f[i + 2], f[i + 3]);
+      }
+      if constexpr (kShiftP<T> > 0) {
+        if (block_any(any_infinite(dk))) {
+          float most = 0.f;
 #pragma unroll
-        for (int u = 0; u < 4; u += 2) {
-          const uint32_t hi = pack2<T>(f[u], f[u + 1]);
-          const float2 r = unpack2<T>(hi);
-          dk[(i + u) / 2] = hi;
-          if (SPLIT) dl[(i + u) / 2] = pack2<T>(f[u] - r.x, f[u + 1] - r.y);
+          for (int i = 0; i < H; ++i) most = finite_max(most, fabsf(f[i]));
+          most = warp_max(most);
+          if (lane == 0) s_max[w] = most;
+          asm volatile("bar.sync 5, 256;" ::: "memory");
+#pragma unroll
+          for (int i = 0; i < kCompute / 32; ++i) most = fmaxf(most, s_max[i]);
+          if (most >= 65520.f) {  // what rounds to infinity (not if only infinities did)
+            const int by = half_exponent(most);
+            const float lower = pow2(by);
+            up += by;
+            scaled *= lower;
+            if (tid < NR) s_delta[tid] *= lower;
+            if (wg == 0 && j > 0) {  // dQ so far; the tile before is done with it
+#pragma unroll
+              for (int q = 0; q < DP / 8; ++q) {
+                uint32_t r[8];
+                tmem_ld(mine + C::kDq + 8 * q, r);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * lower);
+                tmem_st(mine + C::kDq + 8 * q, r);
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < H; i += 2) {
+              f[i] *= lower;
+              f[i + 1] *= lower;
+              dk[i / 2] = pack2<T>(f[i], f[i + 1]);
+            }
+          }
+        }
+      }
+      if (SPLIT) {
+#pragma unroll
+        for (int i = 0; i < H; i += 2) {
+          const float2 r = unpack2<T>(dk[i / 2]);
+          dl[i / 2] = pack2<T>(f[i] - r.x, f[i + 1] - r.y);
         }
       }
       tmem_st(mine + wg * (H / 2), pk);
@@ -311,7 +384,7 @@ __device__ __forceinline__ void few_back_block(const AttendParams& p, const FewM
       // done), and 8 lanes store a row's 128 bytes together
       T* out = wg == 0 ? static_cast<T*>(p.gv) + h * p.gvh : static_cast<T*>(p.gk) + h * p.gkh;
       const int64_t stride = wg == 0 ? p.gvs : p.gks;
-      const float mul = wg == 0 ? 1.0f : p.scale;
+      const float mul = wg == 0 ? pow2(-kShiftP<T>) : half_down<T>(up, p.scale);
       uint8_t* stage = sds + wg * 16384;
 #pragma unroll
       for (int half = 0; half < C::kBlocks; ++half) {
@@ -353,6 +426,7 @@ __device__ __forceinline__ void few_back_block(const AttendParams& p, const FewM
       float* rest = reinterpret_cast<float*>(skv);
       const int row = tid & 127;
       const bool have = n > 0 && ok;
+      const float mul = half_down<T>(up, p.scale);
       tc_fence_after();
       if (SPLIT) {
         if (have && (w & 3) * 32 < 2 * NR) {
@@ -391,7 +465,7 @@ __device__ __forceinline__ void few_back_block(const AttendParams& p, const FewM
               x.unpack(e);
             }
 #pragma unroll
-            for (int u = 0; u < 8; ++u) f[u] = have ? (__uint_as_float(r[8 * i + u]) + e[u]) * p.scale : 0.f;
+            for (int u = 0; u < 8; ++u) f[u] = have ? (__uint_as_float(r[8 * i + u]) + e[u]) * mul : 0.f;
             if (row < rows && d < p.D) {
               if (p.splits == 1) store_vec(static_cast<T*>(p.gq) + t * p.gqs + hq * p.gqh + d, f);
               else store_vec(p.po + (((int64_t)sp * p.Tq + t) * p.Hq + hq) * p.D + d, f);

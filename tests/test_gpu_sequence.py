@@ -521,6 +521,84 @@ def test_attend_gradients_do_not_depend_on_neighbours(R, rows, keys, D, dtype):
     R.sequence_status_sync()
 
 
+def _half_gradients(q, k, v, grad, scale):
+    """The gradients of one bag and head in 64 bits with the errors that they may
+    carry, [rows, D] each.  As sequence_ref.attend, but a term p or ds may be off by
+    no subnormal step of fp16: the backward scales p by 2^14, and ds so that its
+    bound, |grad| |v| + |delta| at their largest, is 2^13 or more."""
+    Q, K, V, dO = (t.double() for t in (q, k, v, grad))
+    D, n, u, step = Q.shape[1], K.shape[0], S.half_step(F16), S.least(F16)
+    s = Q @ K.T * scale
+    e = 2 * ((D + 4) * 2 * S.F32 * (Q.abs() @ K.abs().T) * abs(scale) + 4 * S.F32 * s.abs()).amax(
+        1, keepdim=True) + (n + 64) * 2 * S.F32
+    lse = torch.logsumexp(s, 1, keepdim=True)
+    p = torch.exp(s - lse)
+    o = p @ V
+    o_err = (u + e) * (p @ V.abs()) + step * p.amax(1, keepdim=True) * V.abs().sum(0) + u * o.abs() + step
+    dp, delta = dO @ V.T, (dO * o).sum(1, keepdim=True)
+    ds = p * (dp - delta)
+    pe = p * (2 * e + 8 * S.F32 * lse.abs() + 2 * S.F32 * s.abs().amax(1, keepdim=True))
+    delta_err = (dO.abs() * o_err).sum(1, keepdim=True) + (D + 2) * S.F32 * (dO * o).abs().sum(1, keepdim=True)
+    dp_err = (D + 2) * 2 * S.F32 * (dO.abs() @ V.abs().T)
+    bound = dO.norm(dim=1).max() * V.norm(dim=1).max() + (delta.abs() + delta_err).max()
+    ds_err = pe * (dp - delta).abs() + p * (delta_err + dp_err) + (u + 4 * S.F32) * ds.abs() + step * 2.0 ** -13 * bound
+    nq = (Q.shape[0] + 8) * 2 * S.F32
+    gq, gk, gv = ds @ K * scale, ds.T @ Q * scale, p.T @ dO
+    return ((gq, (ds_err + (n + 8) * 2 * S.F32 * ds.abs()) @ K.abs() * abs(scale) + (u + 4 * S.F32) * gq.abs() + step),
+            (gk, (ds_err + nq * ds.abs()).T @ Q.abs() * abs(scale) + (u + 4 * S.F32) * gk.abs() + step),
+            (gv, (pe + (u + nq) * p + step * 2.0 ** -14).T @ dO.abs() + (u + 4 * S.F32) * gv.abs() + step))
+
+
+def _check_half_gradients(R, q, k, v, grad):
+    qo, ko = _offsets([q.shape[0]]), _offsets([k.shape[0]])
+    heads = [t[:, None].contiguous() for t in (q, k, v, grad)]
+    out, lse = R.attend(*heads[:3], qo, ko, q.shape[0], k.shape[0], scale=0.125)
+    got = R.attend_backward(heads[3], *heads[:3], out, lse, qo, ko, q.shape[0], k.shape[0], scale=0.125)
+    R.sequence_status_sync()
+    for x, (want, tol), name in zip(got, _half_gradients(q, k, v, grad, 0.125), ("grad_q", "grad_k", "grad_v")):
+        # 65504 is fp16's largest number, and 65520 (half a step on) rounds to infinity
+        want = torch.where(want.abs() - tol >= 65520, torch.copysign(torch.full_like(want, math.inf), want), want)
+        S.close(x[:, 0], want, tol, name)
+
+
+@pytest.mark.parametrize("rows,D", [(12, 64), (50, 128), (100, 64), (300, 128)])
+@pytest.mark.parametrize("size", [1e-3, 1e-4, 1e-5])
+def test_attend_half_gradients_of_long_bags(R, rows, D, size):
+    """fp16, 6000 keys, gradients small enough for p (dp - delta) to be below the
+    smallest normal number of fp16.  dp has the sign of a key's column of K, so that
+    errors of ds add up in grad_q; q has columns that K lacks, for grad_k."""
+    g = _gen(rows)
+    n, h = 6000, D // 2
+    sign = torch.where(torch.rand((n, 1), device="cuda", generator=g) < 0.5, -1.0, 1.0)
+    pos = lambda m: torch.rand((m, D), device="cuda", generator=g) + 0.5  # noqa: E731
+    q, k = _randn((rows, D), F32, g, 0.25), _randn((n, D), F32, g, 0.25)
+    q[:, h:h + 8], k[:, h:h + 8] = 0.0, 4.0 * sign
+    q[:, h + 8:], k[:, h + 8:] = 32.0, 0.0
+    _check_half_gradients(R, *(t.to(F16) for t in (q, k, pos(n) * sign, pos(rows) * size)))
+
+
+@pytest.mark.parametrize("rows,D", [(12, 64), (50, 128), (100, 64), (300, 128)])
+def test_attend_half_gradients_of_keys_hardly_attended(R, rows, D):
+    """fp16, half of 3000 keys with p about 2e-9 under gradients of thousands."""
+    g = _gen(rows + 1)
+    q, k, v = (_randn((m, D), F32, g, 0.25) for m in (rows, 3000, 3000))
+    q[:, 0], k[:, 0] = 1.0, torch.where(torch.rand(3000, device="cuda", generator=g) < 0.5, -96.0, 0.0)
+    grad = torch.rand((rows, D), device="cuda", generator=g) * 2000 + 1000
+    _check_half_gradients(R, *(t.to(F16) for t in (q, k, v, grad)))
+
+
+@pytest.mark.parametrize("rows,D", [(1, 64), (20, 64), (50, 128), (100, 64), (300, 128)])
+@pytest.mark.parametrize("n", [2, 200])
+def test_attend_half_gradients_with_ds_beyond_the_type(R, rows, D, n):
+    """fp16, gradients of 10^4: ds of 2 keys passes 65504, grad_q and grad_k do not.
+    The first 128 of 200 keys' are small, so that the scale of ds has to follow."""
+    g = _gen(rows + 2)
+    q, k, v, grad = (_randn((m, D), F32, g, x) for m, x in ((rows, 1e-4), (n, 1e-4), (n, 4.0), (rows, 8000.0)))
+    if n > 128:
+        v[:128] *= 1e-4
+    _check_half_gradients(R, *(t.to(F16) for t in (q, k, v, grad)))
+
+
 # ------------------------------------------------------------------ differences
 def test_gradients_against_differences(R):
     """Each gradient's product with a direction against the central difference
