@@ -408,7 +408,13 @@ class SequenceAttention:
         """keys int64[N] in bags bag_offsets int64[B+1]; tokens int64[T] in bags
         token_offsets int64[B+1]; returns [T, heads, head_dim], zeros for tokens
         of no bag or of a bag that passes max_tokens or max_keys.  keys and
-        bag_offsets stay unchanged until backward."""
+        bag_offsets stay unchanged until backward.  What a forward keeps for its
+        backward is let go by the backward, or by the next forward.  Runs on the
+        current stream of the tensors' device, the table's."""
+        if _elsewhere(None, keys, bag_offsets, tokens, token_offsets, key_mask, self.query_weight, self.norm_weight,
+                      self.norm_bias):
+            with _on(None, keys):
+                return self.forward(batch, keys, bag_offsets, tokens, token_offsets, max_tokens, max_keys, key_mask)
         B = bag_offsets.numel() - 1
         rows = torch.empty((keys.numel(), self.table.dim), dtype=torch.float32, device=keys.device)
         self.table.lookup_pooled(batch, keys, bag_offsets, 1, B, unpooled_out=rows)
@@ -427,6 +433,9 @@ class SequenceAttention:
         max_tokens, have gradients of zero."""
         if self._ctx is None:
             raise RuntimeError("backward before forward")
+        if _elsewhere(None, grad_out, self._ctx[1]):
+            with _on(None, grad_out):
+                return self.backward(grad_out)
         batch, rows, mean, rstd, tokens, q, kv, out, lse, bags, key_mask = self._ctx
         k, v = self._halves(kv)
         # attend_backward leaves the rows of no bag, and of a bag it reports, as they

@@ -198,6 +198,21 @@ def test_sequence_attention_refuses_rows_that_do_not_fit(R):
         R.SequenceAttention(T(), torch.zeros(5, 64), 4, 2, w, w).backward(w)
 
 
+def test_sequence_attention_looks_at_the_device_first(R):
+    """Tensors that are not on one GPU are refused before the table sees them, which
+    takes its stream from the current device."""
+    class T:
+        dim = 64
+
+        def lookup_pooled(self, *a, **kw):
+            raise AssertionError("the lookup ran")
+
+    w, n, o = torch.ones(64), torch.zeros(3, dtype=torch.int64), torch.tensor([0, 3])
+    att = R.SequenceAttention(T(), torch.zeros(5, 64), 4, 2, w, w)
+    with pytest.raises(ValueError):
+        att.forward(None, n, o, n, o, 3, 3)
+
+
 def test_rows_of_views():
     from recommender_sparse_embedding_b200.sequence import _rows
     x = torch.zeros(4, 6, 10)
