@@ -568,16 +568,18 @@ GradPlan grad_plan(int64_t N, int64_t V, int D) {
   if (N <= kSmallN) return g;
   int bits = 1;
   while (((int64_t)1 << bits) <= V) ++bits;  // keys 0 .. V
-  // a pass costs a block its bins as well as its keys: digits of at most 8 bits
-  // where there are keys for many blocks, of 10 where launches are what counts
-  // (1.5M tokens of 20 bits: 283 us with digits of 8, 293 of 10; 65536 of 18
-  // bits: 98 and 93)
-  const int most = N >= 400000 ? 8 : kMaxDigit;
+  // Fewest passes, of at most 10 bits: a pass costs three launches (65536 tokens of
+  // 18 bits: 46 us in two passes, 52 in three of 6; 1.5M: 198 and 212; 1.5M of 19
+  // bits: 237 and 243).  Only two full digits of 10 bits, whose bins cost a block as
+  // much as its keys, fall behind three of 7 where there are many tokens (20 bits:
+  // 800000 tokens 202 and 208, 1.5M 308 and 292).
+  const int most = N >= 1000000 && bits == 20 ? 8 : kMaxDigit;
   g.passes = (bits + most - 1) / most;
   g.bits = (bits + g.passes - 1) / g.passes;
   if (g.bits < 5) g.bits = 5;  // the scan takes 32 bins at a time
-  // 8 keys a thread once there are tiles for every SM, 4 below (1.5M tokens: 283 and 305 us)
-  g.items = N >= (int64_t)kSMs * kSortThreads * 8 ? 8 : 4;
+  // 8 keys a thread once they make two tiles for every SM, 4 below (1M rows: 500000
+  // tokens 171 us at 8 and 167 at 4, 650000 179 and 198, 1.5M 288 and 308)
+  g.items = N >= (int64_t)kSMs * kSortThreads * 16 ? 8 : 4;
   const int64_t tile = (int64_t)kSortThreads * g.items;
   g.tiles = (int)((N + tile - 1) / tile);
   g.pairs_bytes = align256(N * 8);

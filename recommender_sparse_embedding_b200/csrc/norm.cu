@@ -589,12 +589,13 @@ template <typename TX, typename TY, int VEC>
 cudaError_t norm_launch(NormParams p, cudaStream_t s) {
   p.units = p.D / VEC;
   LaunchScope ls("layer_norm", s);
-  // A warp a row while it holds in 64 registers a lane and there are rows for every
-  // SM (bf16, with a block's threads a row instead: 16384 x 4096 65 and 82 us, 65536
-  // x 1024 55 and 65, 1200 x 2048 16 and 23).
+  // A warp a row while it holds in 64 registers a lane, and, where that takes more
+  // than 8 vectors a lane, there are rows for every SM (bf16, with a block's threads a
+  // row instead: 16384 x 4096 60 and 75 us, 16384 x 2048 34 and 44, 64 x 1024 8.7 and
+  // 10.5; 64 x 4096 18.5 and 14.6, 888 x 4096 18.5 and 19).
   if constexpr (VEC == 8) {
     constexpr int most = sizeof(TX) == 2 ? 16 : 8;
-    if (p.units > 64 && p.units <= 32 * most && p.M >= kSMs * 8) {
+    if (p.units > 64 && p.units <= 32 * most && (p.units <= 256 || p.M >= kSMs * 6)) {
       if (p.units <= 128) return norm_row_go<TX, TY, 4>(p, s);
       if (p.units <= 256) return norm_row_go<TX, TY, 8>(p, s);
       return norm_row_go<TX, TY, most>(p, s);
@@ -602,8 +603,9 @@ cudaError_t norm_launch(NormParams p, cudaStream_t s) {
   }
   // Else up to two vectors a thread (single columns: 8), then more threads.  More
   // columns a thread share the sums' shuffles and barriers, fewer leave registers
-  // for more rows an SM: 16384 x 4096 bf16 takes 89 us at 8 columns (issue), 82 at
-  // 16, 97 at 32 (latency at 16 warps an SM).
+  // for more rows an SM and more threads for few rows: 16384 x 4096 fp32 takes 135 us
+  // at 8 columns, 106 at 16, 112 at 32; 64 x 8192 bf16 16 at 16 and 23 at 32 (16384
+  // rows 143 and 126).
   int upt = p.units <= 32 ? 1 : 2;
   if (VEC == 1 && p.units > 64) upt = 8;
   p.tpr = row_threads(p.units, upt);
