@@ -454,7 +454,8 @@ recis_status recis_embed_lookup(const void* weight, int32_t weight_type, int64_t
  * are left alone).  Padding tokens have no gradient; a token out of range is
  * skipped and reported as above.  The tokens are sorted and each row's terms
  * added in occurrence order: fp32 within spans of the sorted positions, fp64
- * across spans, so results do not depend on scheduling.  grad_weight: [V][D],
+ * across spans (up to 1024 tokens: fp32 within every n-th term of a row, n by D,
+ * fp64 across these), so results do not depend on scheduling.  grad_weight: [V][D],
  * contiguous.  0 <= N < 2^30, otherwise as above. */
 recis_status recis_embed_grad_workspace(int64_t N, int64_t V, int32_t D, int64_t* bytes_out);
 recis_status recis_embed_grad(const int64_t* tokens, int64_t N, const void* grad_out,

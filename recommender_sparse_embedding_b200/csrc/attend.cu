@@ -21,8 +21,6 @@ namespace recis {
 
 namespace {
 
-__host__ __device__ constexpr int64_t align256(int64_t b) { return (b + 255) & ~(int64_t)255; }
-
 template <typename T>
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
 template <>
@@ -387,7 +385,7 @@ AttendPlan attend_plan(const recis_attend_args& a, bool backward) {
     if (g.splits > 1) g.po_bytes = align256(g.splits * a.Tq * a.Hq * a.D * 4);
   } else {
     // parts of the keys: enough blocks for every SM to hold a few, each part
-    // at least 256 keys (few rows: 16 iterations a warp) or 512 (tiles: 4 steps)
+    // at least 256 keys (few rows: 4 tiles) or 512 (tiles: 4 steps)
     const int64_t G = a.Hq / a.Hkv;
     const bool few = few_rows(a.max_q, G);
     const int64_t tile = few ? std::max<int64_t>(kRowTile / G, 1) : 128 / G;  // queries a block

@@ -37,8 +37,6 @@ constexpr int kMaxDigit = 10;     // bits a pass sorts by
 constexpr int kMaxSpan = 64;      // sorted positions a group of lanes walks: 16, 32 or 64
 constexpr int kMaxSpans = 64;     // spans a block takes
 
-__host__ __device__ constexpr int64_t align256(int64_t b) { return (b + 255) & ~(int64_t)255; }
-
 // ---------------------------------------------------------------- lookup
 struct LookupParams {
   const void* w;
@@ -149,7 +147,6 @@ struct PassParams {
   ZeroSlice zero[3];        // beside the count, the scan and the scatter
 };
 
-template <int ITEMS>
 __device__ __forceinline__ uint2 pass_item(const PassParams& p, int64_t i, bool report) {
   if (p.in) return p.in[i];  // written by the kernel before: no read-only path
   return make_uint2(sort_key(__ldg(p.tok + i), p.V, p.padding, p.status, report), (uint32_t)i);
@@ -173,7 +170,7 @@ __global__ void __launch_bounds__(kSortThreads) grad_count_kernel(const __grid_c
 #pragma unroll
   for (int j = 0; j < ITEMS; ++j) {
     const int64_t i = base + j * kSortThreads + threadIdx.x;
-    key[j] = i < p.N ? pass_item<ITEMS>(p, i, true).x : 0;
+    key[j] = i < p.N ? pass_item(p, i, true).x : 0;
   }
 #pragma unroll
   for (int j = 0; j < ITEMS; ++j)
@@ -236,7 +233,7 @@ __global__ void __launch_bounds__(kSortThreads) grad_scatter_kernel(const __grid
   uint2 v[ITEMS];
 #pragma unroll
   for (int j = 0; j < ITEMS; ++j)
-    v[j] = base + j * 32 < p.N ? pass_item<ITEMS>(p, base + j * 32, false) : make_uint2(0, 0);
+    v[j] = base + j * 32 < p.N ? pass_item(p, base + j * 32, false) : make_uint2(0, 0);
   // exclusive scan of the digit totals: 4 (at most) consecutive bins a thread
   constexpr int kPer = (1 << kMaxDigit) / kSortThreads;
   uint32_t tot[kPer], pre[kPer], mine = 0;

@@ -12,6 +12,7 @@ namespace recis {
 // its address could not be had)
 int* sequence_status();
 
+constexpr int64_t align256(int64_t b) { return (b + 255) & ~(int64_t)255; }
 inline bool float_type(int t) { return t == RECIS_F32 || t == RECIS_BF16 || t == RECIS_F16; }
 inline int type_bytes(int t) { return t == RECIS_F32 ? 4 : 2; }
 
