@@ -427,7 +427,9 @@ bool bad_array(const void* p, int64_t stride, int64_t head_stride, int64_t rows)
 // bags, rows and blocks of a launch fit its grid
 bool grid_fits(int64_t n) { return n < ((int64_t)1 << 31); }
 
-recis_status fill(const recis_attend_args* a, AttendParams* p, const AttendPlan& g, void* ws) {
+// a: of launch_sizes; `given`: the caller's
+recis_status fill(const recis_attend_args* a, const recis_attend_args* given, AttendParams* p, const AttendPlan& g,
+                  void* ws) {
   int* st = sequence_status();
   if (!st) {
     set_error("the sequence operators' status word is not reachable (no usable sm_100 device?)");
@@ -446,6 +448,7 @@ recis_status fill(const recis_attend_args* a, AttendParams* p, const AttendPlan&
   p->Tq = a->Tq; p->Tk = a->Tk;
   p->B = (int)a->B; p->Hq = a->Hq; p->Hkv = a->Hkv; p->G = a->Hq / a->Hkv; p->D = a->D;
   p->max_q = (int)a->max_q; p->max_k = (int)a->max_k;
+  p->bound_q = (int)given->max_q; p->bound_k = (int)given->max_k;
   p->scale = (float)a->scale;
   p->scale_log2 = (float)(a->scale * 1.4426950408889634);
   // a scale of 0 makes every score 0; 1e-30 does too, and keeps the -inf of keys that take no part
@@ -559,7 +562,7 @@ extern "C" recis_status recis_attend(const recis_attend_args* args, void* worksp
   if (st != RECIS_OK) return st;
   if (a->B == 0 || a->Tq == 0) return RECIS_OK;
   AttendParams p;
-  if ((st = fill(a, &p, attend_plan(*a, false), workspace)) != RECIS_OK) return st;
+  if ((st = fill(a, args, &p, attend_plan(*a, false), workspace)) != RECIS_OK) return st;
   return a->type == RECIS_BF16 ? forward<__nv_bfloat16>(p, (cudaStream_t)stream)
                                : forward<__half>(p, (cudaStream_t)stream);
 }
@@ -571,6 +574,6 @@ extern "C" recis_status recis_attend_backward(const recis_attend_args* args, voi
   if (st != RECIS_OK) return st;
   if (a->B == 0) return RECIS_OK;
   AttendParams p;
-  if ((st = fill(a, &p, attend_plan(*a, true), workspace)) != RECIS_OK) return st;
+  if ((st = fill(a, args, &p, attend_plan(*a, true), workspace)) != RECIS_OK) return st;
   return launch_attend_back(p, a->type == RECIS_BF16, (cudaStream_t)stream);
 }

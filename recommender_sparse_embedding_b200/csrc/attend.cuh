@@ -15,7 +15,8 @@ struct AttendParams {
   int64_t qs, qh, ks, kh, vs, vh, os, oh, gos, goh, gqs, gqh, gks, gkh, gvs, gvh;  // strides: row, head
   int64_t Tq, Tk;
   int B, Hq, Hkv, G, D;
-  int max_q, max_k;
+  int max_q, max_k;         // at least 1 (launch_sizes in attend.cu)
+  int bound_q, bound_k;     // what no bag may pass: the caller's max_q and max_k
   float scale, scale_log2;  // scale, scale * log2(e)
   int splits, split_keys;   // parts of a bag's keys, keys a part
   float* po;                // splits > 1: [splits][Tq][Hq][D] each part's output ...
@@ -36,8 +37,8 @@ struct Bag {
 // reported and has none, so no access leaves the arrays.
 __device__ __forceinline__ Bag load_bag(const AttendParams& p, int b) {
   const int64_t q0 = __ldg(p.qo + b), q1 = __ldg(p.qo + b + 1), k0 = __ldg(p.ko + b), k1 = __ldg(p.ko + b + 1);
-  const bool ok = q0 >= 0 && q1 >= q0 && q1 <= p.Tq && q1 - q0 <= p.max_q && k0 >= 0 && k1 >= k0 && k1 <= p.Tk &&
-                  k1 - k0 <= p.max_k;
+  const bool ok = q0 >= 0 && q1 >= q0 && q1 <= p.Tq && q1 - q0 <= p.bound_q && k0 >= 0 && k1 >= k0 && k1 <= p.Tk &&
+                  k1 - k0 <= p.bound_k;
   if (!ok) {
     if (threadIdx.x == 0) atomicOr(p.status, kErrBadOffsets);
     return Bag{0, 0, 0, 0};

@@ -484,6 +484,24 @@ def test_attend_empty_calls(R):
     assert not gk.any() and not gv.any()
 
 
+@pytest.mark.parametrize("Hq", [2, 40, 128])
+def test_attend_bounds_of_zero_are_bounds(R, Hq):
+    """A bag of one row, or of one key, passes a bound of 0."""
+    g = _gen(Hq)
+    q, k = _randn((3, Hq, 16), F16, g), _randn((5, 1, 16), F16, g)
+    one, none = _offsets([1, 2]), _offsets([0, 0])
+    lse = torch.zeros((3, Hq), device="cuda")
+    for qo, ko, mq, mk in ((_offsets([0, 1]), none, 0, 5), (none, _offsets([1, 0]), 3, 0), (one, _offsets([1, 0]), 2, 0)):
+        R.attend(q, k, k, qo, ko, mq, mk)
+        with pytest.raises(R.RecisError):
+            R.sequence_status_sync()
+        R.attend_backward(q, q, k, k, q, lse, qo, ko, mq, mk)
+        with pytest.raises(R.RecisError):
+            R.sequence_status_sync()
+    R.attend(q, k, k, one, none, 2, 0)
+    R.sequence_status_sync()
+
+
 @pytest.mark.parametrize("Hq,Hkv", [(2, 2), (17, 1), (128, 1), (256, 2)])
 def test_attend_rows_of_no_bag_with_a_bound_of_zero(R, Hq, Hkv):
     """max_q 0: no bag has queries, q's rows belong to none; keys get zeros."""
