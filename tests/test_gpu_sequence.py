@@ -347,6 +347,43 @@ def test_attend_large_scores(R):
     S.close(lse, *ref["lse"], "lse")
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("scale", [-0.7, 0.0])
+@pytest.mark.parametrize("rows,keys,masked", [(9, 300, 0.1), (40, 100, 0.0), (150, 300, 0.1)])
+def test_attend_negative_and_zero_scale(R, rows, keys, masked, scale, dtype):
+    g = _gen(rows)
+    q, grad = (_randn((rows, 2, 32), dtype, g) for _ in range(2))
+    k, v = (_randn((keys, 1, 32), dtype, g) for _ in range(2))
+    mask = torch.rand(keys, device="cuda", generator=g) >= masked
+    k[~mask], v[~mask] = math.nan, math.inf
+    qo, ko = _offsets([rows]), _offsets([keys])
+    out, lse = R.attend(q, k, v, qo, ko, rows, keys, scale=scale, key_mask=mask)
+    grads = R.attend_backward(grad, q, k, v, out, lse, qo, ko, rows, keys, scale=scale, key_mask=mask)
+    R.sequence_status_sync()
+    ref = S.attend(q, k, v, qo, ko, scale, mask, grad)
+    for t, n in zip((out, lse, *grads), ("out", "lse", "grad_q", "grad_k", "grad_v")):
+        S.close(t, *ref[n], n)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("rows", [1, 33])
+def test_attend_of_many_short_bags(R, rows, dtype):
+    """70000 bags of 3 keys, more than a grid's second dimension holds."""
+    g = _gen(15)
+    B, D = 70000, 16
+    q, grad = (_randn((B * rows, 2, D), dtype, g) for _ in range(2))
+    k, v = (_randn((B * 3, 2, D), dtype, g) for _ in range(2))
+    qo, ko = (torch.arange(B + 1, device="cuda") * n for n in (rows, 3))
+    out, lse = R.attend(q, k, v, qo, ko, rows, 3)
+    gq, gk, gv = R.attend_backward(grad, q, k, v, out, lse, qo, ko, rows, 3)
+    R.sequence_status_sync()
+    for b in (0, 1, 32767, 65535, 65536, B - 1):
+        a, c = slice(b * rows, (b + 1) * rows), slice(3 * b, 3 * b + 3)
+        ref = S.attend(q[a], k[c], v[c], _offsets([rows]), _offsets([3]), 0.25, None, grad[a])
+        for t, n in zip((out[a], lse[a], gq[a], gk[c], gv[c]), ("out", "lse", "grad_q", "grad_k", "grad_v")):
+            S.close(t, *ref[n], n)
+
+
 def test_attend_offsets_past_32_bits(R):
     """A cache whose last rows lie more than 2^32 elements in."""
     Tk, H, D = 1 << 20, 40, 128
@@ -615,6 +652,29 @@ def test_attend_half_gradients_with_ds_beyond_the_type(R, rows, D, n):
     if n > 128:
         v[:128] *= 1e-4
     _check_half_gradients(R, *(t.to(F16) for t in (q, k, v, grad)))
+
+
+@pytest.mark.parametrize("rows", [3, 100])
+def test_attend_half_gradients_beside_infinities(R, rows):
+    """fp16: a row whose gradient holds an infinity spoils grad_k and grad_v of its
+    bag, not grad_q of the other rows nor another bag."""
+    g = _gen(rows + 3)
+    q, grad = (_randn((2 * rows, 2, 64), F16, g) for _ in range(2))
+    k, v = (_randn((800, 2, 64), F16, g) for _ in range(2))
+    qo, ko = _offsets([rows, rows]), _offsets([400, 400])
+    out, lse = R.attend(q, k, v, qo, ko, rows, 400)
+    want = R.attend_backward(grad, q, k, v, out, lse, qo, ko, rows, 400)
+    grad[1, 0, 5] = math.inf
+    got = R.attend_backward(grad, q, k, v, out, lse, qo, ko, rows, 400)
+    ref = S.attend(q, k, v, qo, ko, 0.125, None, grad.clamp(-65504, 65504))
+    keep = torch.ones_like(q, dtype=torch.bool)
+    keep[1, 0] = False
+    S.close(got[0][keep], *(t[keep] for t in ref["grad_q"]), "grad_q")
+    assert not torch.isfinite(got[0][1, 0]).any()
+    assert torch.equal(got[0][rows:], want[0][rows:]) and torch.equal(got[0][:, 1], want[0][:, 1])
+    for i in (1, 2):
+        assert torch.equal(got[i][400:], want[i][400:]) and torch.equal(got[i][:, 1], want[i][:, 1])
+        assert not torch.isfinite(got[i][:400, 0]).all()
 
 
 # ------------------------------------------------------------------ differences
