@@ -408,7 +408,9 @@ class SequenceAttention:
         """keys int64[N] in bags bag_offsets int64[B+1]; tokens int64[T] in bags
         token_offsets int64[B+1]; returns [T, heads, head_dim], zeros for tokens
         of no bag or of a bag that passes max_tokens or max_keys.  keys and
-        bag_offsets stay unchanged until backward.  What a forward keeps for its
+        bag_offsets stay unchanged until backward.  A lookup that the table rejects
+        (Table.status_sync) leaves the answers and the dense gradients undefined, and
+        the table's rows as they were.  What a forward keeps for its
         backward is let go by the backward, or by the next forward.  Runs on the
         current stream of the tensors' device, the table's."""
         if _elsewhere(None, keys, bag_offsets, tokens, token_offsets, key_mask, self.query_weight, self.norm_weight,
@@ -416,8 +418,10 @@ class SequenceAttention:
             with _on(None, keys):
                 return self.forward(batch, keys, bag_offsets, tokens, token_offsets, max_tokens, max_keys, key_mask)
         B = bag_offsets.numel() - 1
-        rows = torch.empty((keys.numel(), self.table.dim), dtype=torch.float32, device=keys.device)
+        # (a row at least: a lookup without an output array is refused, and bags may all be empty)
+        rows = torch.empty((max(keys.numel(), 1), self.table.dim), dtype=torch.float32, device=keys.device)
         self.table.lookup_pooled(batch, keys, bag_offsets, 1, B, unpooled_out=rows)
+        rows = rows[:keys.numel()]
         kv, mean, rstd = layer_norm(rows, self.norm_weight, self.norm_bias, self.eps, self.dtype)
         q = embed_lookup(self.query_weight, tokens, self.query_scale, out_dtype=self.dtype)
         q = q.view(-1, self.heads, self.head_dim)

@@ -900,3 +900,26 @@ def test_sequence_attention_gives_rows_of_no_bag_no_gradient(R):
         assert (p == q).all()
     for t in (*tables, *batches):
         t.close()
+
+
+@pytest.mark.parametrize("kl,ql", [([0, 0], [2, 1]), ([3, 4], [0, 0]), ([0, 0], [0, 0]), ([5, 0], [0, 3]), ([], [])])
+def test_sequence_attention_of_empty_bags(R, kl, ql):
+    """Steps without keys, without tokens, without either, without bags."""
+    g = _gen(52)
+    table, batch = R.Table(64, R.ADAM, lr=0.05, init_scale=1.0, init_seed=3), R.Batch()
+    w = torch.ones(64, device="cuda")
+    att = R.SequenceAttention(table, _randn((30, 64), F32, g), 4, 2, w, w)
+    keys = torch.arange(sum(kl), device="cuda") + 7
+    tok = torch.randint(0, 30, (sum(ql),), device="cuda", generator=g)
+    qo, ko = (torch.tensor([0] + n, device="cuda").cumsum(0) for n in (ql, kl))
+    for _ in range(2):
+        out = att.forward(batch, keys, ko, tok, qo, max(ql + [0]), max(kl + [0]))
+        dquery, dnw, dnb = att.backward(_randn(out.shape, BF16, g))
+        R.sequence_status_sync()
+        table.status_sync()
+        assert out.shape == (sum(ql), 4, 16) and dquery.shape == (30, 64)
+        met = any(n and q for n, q in zip(kl, ql))  # a bag has both
+        assert met == bool(out.any()) and all(met == bool(t.any()) for t in (dquery, dnw, dnb))
+    assert table.size()[0] == sum(kl)
+    table.close()
+    batch.close()
