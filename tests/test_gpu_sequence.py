@@ -335,6 +335,37 @@ def test_attend_strided(R, i):
     _check_attend(R, 200 + i, ATTEND[i], BF16, strided=True)
 
 
+@pytest.mark.parametrize("dtype,D,masked", [(BF16, 128, 0.0), (F16, 72, 0.1), (BF16, 64, 0.1)])
+def test_attend_of_keys_and_values_that_arrive_late(R, dtype, D, masked):
+    """Passes over different inputs in a row while copies keep the memory busy, so
+    that a tile's values may still be on their way when the next tile's turn comes;
+    most bags end inside a tile."""
+    states = []
+    for i in range(2):
+        g = _gen(60 + i)
+        ql, kl = _bags(60 + i, 12, (150, 300), (129, 1500))
+        q, k, v = (_randn((sum(n), h, D), dtype, g) for n, h in ((ql, 4), (kl, 2), (kl, 2)))
+        mask = torch.rand(sum(kl), device="cuda", generator=g) >= masked if masked else None
+        qo, ko = _offsets(ql), _offsets(kl)
+        ref = S.attend(q, k, v, qo, ko, D ** -0.5, mask)
+        states.append(((q, k, v, qo, ko, max(ql), max(kl)), mask, ref))
+    buf, side = torch.zeros(256 << 20, dtype=torch.uint8, device="cuda"), torch.cuda.Stream()
+    got = []
+    torch.cuda.synchronize()
+    for i in range(24):
+        with torch.cuda.stream(side):
+            for _ in range(4):
+                buf[: 128 << 20].copy_(buf[128 << 20:])
+        a, mask, _ = states[i % 2]
+        got.append(R.attend(*a, key_mask=mask))
+    R.sequence_status_sync()
+    torch.cuda.synchronize()
+    for i, (out, lse) in enumerate(got):
+        ref = states[i % 2][2]
+        S.close(out, *ref["out"], f"out of pass {i}")
+        S.close(lse, *ref["lse"], f"lse of pass {i}")
+
+
 def test_attend_large_scores(R):
     """Scores of thousands, of both signs: the running maximum carries them."""
     g = _gen(5)
