@@ -19,8 +19,8 @@
 // accumulator.
 //
 // Measured on B200, bf16: 4 bags of 4096 queries over 4096 keys, 8 heads of 128, 771
-// us, 891 TFLOP/s counted as 5 products (keys 409 us, queries 346); heads of 64, 544
-// us, 632.  A step of 64 rows takes 1750 cycles over keys, 1400 over queries; its
+// us, 891 TFLOP/s counted as 5 products (keys 405 us, queries 353); heads of 64, 546-
+// 578 us, 630-595.  A step of 64 rows takes 1750 cycles over keys, 1400 over queries; its
 // products take 1294 and 1038 (64 columns a product from shared memory take 49
 // cycles instead of 32), issuing them and their waits and commits about 1400.
 //

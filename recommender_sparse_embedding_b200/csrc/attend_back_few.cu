@@ -14,9 +14,9 @@
 //   dV = P^T dO, dK = dS^T Q        (128 keys x D), stored
 //   dQ += dS K                      (NR rows x D, kept in tensor memory)
 //
-// Measured on B200: 256 bags of 0-16 queries over 1000-5000 keys, 2 heads of 64, 160
-// us with the join (4.9 TB/s of K, V, dK and dV); one query, 8 heads of 128 over 2,
-// 305-350 us (4.5 TB/s: one block an SM, and the chain of a tile's steps shows).
+// Measured on B200: 256 bags of 0-16 queries over 1000-5000 keys, 2 heads of 64,
+// 161-181 us with the join (4.9 to 4.3 TB/s of K, V, dK and dV); one query, 8 heads of
+// 128 over 2, 303 us (one block an SM, and the chain of a tile's steps shows).
 //
 // Bags of few keys (SPLIT, as in the other backward) have dS go into its products
 // as two 16-bit values, its rounding and what that leaves out: for dQ the second

@@ -16,9 +16,9 @@
 // kernel adds those in span order in fp64: no float atomic is used.
 //
 // Measured on B200 (L2 flushed): 1.5M tokens over 1M rows of 128, fp32 weight to
-// bf16 rows, 129 us, 5.1 TB/s of DRAM traffic; their gradient (bf16 to fp32, dW
-// of 512 MB) 283 us, of which the spans 135 us at 4.3 TB/s, the sort about 95 us
-// beside 77 us worth of zeros that hide a quarter of it, the join 22 us.
+// bf16 rows, 125-130 us, 5.5 TB/s of DRAM traffic; their gradient (bf16 to fp32, dW
+// of 512 MB) 278 us, of which the spans 127 us at 4.5 TB/s, the sort about 125 us
+// with the 77 us worth of zeros beside it, the join 20 us.
 #include <algorithm>
 
 #include "seqops.cuh"

@@ -13,10 +13,10 @@
 // the blocks' sums in block order in fp64 (no float atomic).
 //
 // Measured on B200 (L2 flushed): 1.5M rows of 128, fp32 to bf16, forward 187 us
-// (6.2 TB/s), backward 308 us (6.2 TB/s); 16384 rows of 4096 bf16, forward 65 us
-// (4.1 TB/s, bound by instructions: a value is unpacked three times), backward 94
-// us (4.3 TB/s, by instructions: two sums a column kept in registers leave 16 warps
-// an SM).
+// (6.2 TB/s), backward 308 us (6.2 TB/s); 16384 rows of 4096 bf16, forward 60 us
+// (4.5 TB/s; instructions issue in 40 % of the cycles: 16 warps an SM with no row
+// fetched ahead leave latency), backward 91 us (4.4 TB/s; issue 63 %, two sums a
+// column kept in registers leave 16 warps an SM).
 #include <algorithm>
 #include <atomic>
 
