@@ -237,6 +237,9 @@ __global__ void __launch_bounds__(kFewWarps * 32 + 32)
         mma16816<T>(o[2 * i], pa, vf[0], vf[1]);
         mma16816<T>(o[2 * i + 1], pa, vf[2], vf[3]);
       }
+      // the tile's reads are done before a copy may overwrite it: an arrival alone does
+      // not order them before writes of the copy engine's
+      fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(empty + st);
     }

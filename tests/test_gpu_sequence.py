@@ -335,6 +335,34 @@ def test_attend_strided(R, i):
     _check_attend(R, 200 + i, ATTEND[i], BF16, strided=True)
 
 
+@pytest.mark.parametrize("dtype,D,q", [(BF16, 64, 1), (F16, 64, 5), (BF16, 128, 1), (F16, 40, 16)])
+def test_attend_of_few_rows_while_the_memory_is_busy(R, dtype, D, q):
+    """Passes in a row over keys that L2 does not hold, beside copies: bit for bit
+    what a pass by itself gives (and that is right)."""
+    g = _gen(D + q)
+    B = 100 * 64 // D
+    ql, kl = _bags(D, B, (1, q), (1500, 5000))
+    qo, ko = _offsets(ql), _offsets(kl)
+    Q = _randn((sum(ql), 2, D), dtype, g)
+    k, v = (_randn((sum(kl), 2, D), dtype, g) for _ in range(2))
+    want = R.attend(Q, k, v, qo, ko, q, max(kl))
+    torch.cuda.synchronize()
+    some = slice(0, int(qo[4])), slice(0, int(ko[4]))
+    ref = S.attend(Q[some[0]], k[some[1]], v[some[1]], qo[:5], ko[:5], D ** -0.5)
+    S.close(want[0][some[0]], *ref["out"], "out")
+    buf, side, got = torch.zeros(256 << 20, dtype=torch.uint8, device="cuda"), torch.cuda.Stream(), []
+    torch.cuda.synchronize()
+    for _ in range(30):
+        with torch.cuda.stream(side):
+            for _ in range(3):
+                buf[: 128 << 20].copy_(buf[128 << 20:])
+        got.append(R.attend(Q, k, v, qo, ko, q, max(kl)))
+    R.sequence_status_sync()
+    torch.cuda.synchronize()
+    for out, lse in got:
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
 @pytest.mark.parametrize("dtype,D,masked", [(BF16, 128, 0.0), (F16, 72, 0.1), (BF16, 64, 0.1)])
 def test_attend_of_keys_and_values_that_arrive_late(R, dtype, D, masked):
     """Passes over different inputs in a row while copies keep the memory busy, so
