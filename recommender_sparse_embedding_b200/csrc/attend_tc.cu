@@ -245,8 +245,10 @@ __global__ void __launch_bounds__(kTcThreads, 2)
       const float grown = fmaxf(m, top == -INFINITY ? top : top * fabsf(c));
       const bool move = j == 0 || grown > m + kLazy;
       if (__any_sync(0xffffffffu, move)) {
-        const float next = grown == -INFINITY ? m : grown;
-        const float f = m == -INFINITY ? 0.f : ex2(m - next);
+        // each row by its own maximum: the warp's other rows, which may be another
+        // bag's or none, do not show in it
+        const float next = move && grown != -INFINITY ? grown : m;
+        const float f = !move ? 1.f : m == -INFINITY ? 0.f : ex2(m - next);
         m = next;
         l *= f;
         if (j > 0) {

@@ -394,6 +394,24 @@ def test_attend_of_keys_and_values_that_arrive_late(R, dtype, D, masked):
         S.close(lse, *ref["lse"], f"lse of pass {i}")
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("Hq,rows", [(1, 20), (3, 50), (5, 200)])
+def test_attend_does_not_depend_on_rows_beside_it(R, Hq, rows, dtype):
+    """A bag alone, before a bag of other queries, and after a call that leaves large
+    values in shared memory: the same bits."""
+    g = _gen(rows)
+    q, k, v = (_randn((n, h, 64), dtype, g) for n, h in ((2 * rows, Hq), (1200, 1), (1200, 1)))
+    q[rows:] *= 30
+    alone = R.attend(q[:rows], k[:600], v[:600], _offsets([rows]), _offsets([600]), rows, 600)
+    two = R.attend(q, k, v, _offsets([rows, rows]), _offsets([600, 600]), rows, 600)
+    big = _randn((148 * 2 * 128, 1, 64), dtype, g, 60.0)
+    R.attend(big, k[:128], v[:128], _offsets([big.shape[0]]), _offsets([128]), big.shape[0], 128)
+    again = R.attend(q[:rows], k[:600], v[:600], _offsets([rows]), _offsets([600]), rows, 600)
+    R.sequence_status_sync()
+    for x, y, z in zip(alone, two, again):
+        assert torch.equal(x, y[:rows]) and torch.equal(x, z)
+
+
 def test_attend_large_scores(R):
     """Scores of thousands, of both signs: the running maximum carries them."""
     g = _gen(5)
