@@ -197,19 +197,12 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         const unsigned bits = __ballot_sync(0xffffffffu, v != 0);
         if (lane == 0) s_valid[j & 1][w] = bits;
         asm volatile("bar.sync 1, 128;" ::: "memory");
-      }
-      // a warp that gave up goes on without waiting: the others' barrier needs it
-      ok = ok && mbar_wait(s_full, j & 1, spin_max);
-      __syncwarp();
-      tc_fence_after();
-      if (tail) {
-        // Rows of V that take no part are zeroed.  Only now is the wait for V's copy
-        // one for this tile's: these scores were asked for after the tile before had
-        // taken its V, so at most one phase of the barrier is open (earlier, with a
-        // tile's V still on its way, the parity of the one before that would pass).
+        // Rows of V that take no part are zeroed.  The scores come first: they were
+        // asked for after the tile before had taken its V, so that only then the wait
+        // for V's copy is one for this tile's (earlier, with the V of the tile before
+        // still on its way, the parity of the one before that would pass).
         const int st = j % NS;
-        ok = ok && mbar_wait(v_full + st, (j / NS) & 1, spin_max);
-        __syncwarp();
+        ok = ok && mbar_wait(s_full, j & 1, spin_max) && mbar_wait(v_full + st, (j / NS) & 1, spin_max);
         if (!v)
           for (int i = 0; i < L::kBlocks; ++i) {
             uint4* row = reinterpret_cast<uint4*>(sv + st * L::kBytes + (i * kTile + tid) * 128);
@@ -217,8 +210,11 @@ __global__ void __launch_bounds__(kTcThreads, 2)
             for (int c = 0; c < 8; ++c) row[c] = make_uint4(0, 0, 0, 0);
           }
         fence_async_smem();
-        __syncwarp();
       }
+      // a warp that gave up goes on without waiting: the others' barrier needs it
+      ok = ok && mbar_wait(s_full, j & 1, spin_max);
+      __syncwarp();
+      tc_fence_after();
       uint32_t r[kTile];  // the row's scores, in registers from here on
 #pragma unroll
       for (int q = 0; q < 4; ++q) tmem_ld32(mine + 32 * q, *reinterpret_cast<uint32_t(*)[32]>(r + 32 * q));
