@@ -36,7 +36,7 @@
 // over keys its own |V| and the largest |dO| and |delta| of the bag's rows, over
 // queries its own |dO| and delta and the largest |V| of the bag's keys, which the
 // pass over keys has left.  (16 bags of 512-1024 over 1024-4096 keys, 8 heads of 128
-// over 4: 564 us, bf16 531; the product more a pair of scores over keys costs most.)
+// over 4: 560 us, bf16 531; the product more a pair of scores over keys costs most.)
 //
 // Rows of a tile that belong to another bag, or to masked keys, are overwritten
 // with zeros before the products (0 * NaN is NaN) by the warp that issues the
@@ -342,10 +342,21 @@ __device__ __forceinline__ void attend_back_block(const AttendParams& p, const B
       if (KEYS && n > 0) {
         float* s_max = reinterpret_cast<float*>(base + C::kMax);
         float go = 0.f, de = 0.f;
-        for (int r = tid; r < bag.nq * p.G; r += WG * 128) {
-          const int64_t i = (bag.q0 + r / p.G) * p.Hq + h * p.G + r % p.G;
-          go = finite_max(go, p.gnorm[i]);
-          de = finite_max(de, fabsf(p.delta[i]));
+        const int rows = bag.nq * p.G;
+        for (int r = tid; r < rows; r += 4 * WG * 128) {
+          float a[4], c[4];  // 8 loads in flight
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int at = min(r + u * WG * 128, rows - 1);
+            const int64_t i = (bag.q0 + at / p.G) * p.Hq + h * p.G + at % p.G;
+            a[u] = p.gnorm[i];
+            c[u] = p.delta[i];
+          }
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            go = finite_max(go, a[u]);
+            de = finite_max(de, fabsf(c[u]));
+          }
         }
         go = warp_max(go);
         de = warp_max(de);
