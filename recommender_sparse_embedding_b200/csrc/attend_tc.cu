@@ -358,9 +358,17 @@ bool rows_map(CUtensorMap* map, const void* p, bool bf16, int D, int H, int64_t 
   const cuuint64_t strides[2] = {(cuuint64_t)head_stride * 2, (cuuint64_t)stride * 2};
   const cuuint32_t box[3] = {64, (cuuint32_t)heads, (cuuint32_t)rows};
   const cuuint32_t one[3] = {1, 1, 1};
-  return encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(p),
-                dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  auto make = [&] {
+    return encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+                  const_cast<void*>(p), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  };
+  if (make() == CUDA_SUCCESS) return true;
+  // A host thread's first CUDA call: it has no context yet, which the runtime's
+  // calls make current and the driver's do not.
+  int dev = 0;
+  return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess && make() == CUDA_SUCCESS;
 }
 
 template <typename T, int DP>

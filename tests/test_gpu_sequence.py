@@ -860,6 +860,33 @@ def test_operators_together_captured_and_replayed(R):
     R.sequence_status_sync()
 
 
+@pytest.mark.parametrize("rows", [3, 150])
+def test_attention_as_a_threads_first_call(R, rows):
+    """A host thread that has made no CUDA call of its own has no context yet."""
+    g = _gen(rows)
+    q, k, v = (_randn((n, 2, 64), BF16, g) for n in (rows, 300, 300))
+    bags = (_offsets([rows]), _offsets([300]), rows, 300)
+    want = R.attend(q, k, v, *bags)
+    want += R.attend_backward(q, q, k, v, *want, *bags)
+    torch.cuda.synchronize()
+    got, failed = {}, []
+
+    def run(name, call):
+        try:
+            got[name] = call()
+        except R.RecisError as e:
+            failed.append((name, str(e)))
+
+    for name, call in (("forward", lambda: R.attend(q, k, v, *bags)),
+                       ("backward", lambda: R.attend_backward(q, q, k, v, *want[:2], *bags))):
+        t = threading.Thread(target=run, args=(name, call))
+        t.start()
+        t.join()
+    assert not failed, failed
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(got["forward"] + got["backward"], want))
+
+
 def test_calls_on_two_streams_at_once(R):
     states = [_state(40 + i) for i in range(4)]
     want = [_step(R, s) for s in states]
